@@ -35,9 +35,13 @@ SYMBOLS = (
     "eec_energy_forces", "eec_energy_forces_folded", "eec_energy_forces_folded_noalloc",
     "eec_energy_forces_timed", "eec_workspace_bytes",
     "eec_radial_table_floats", "eec_radial_table_levels", "eec_radial_table_build", "eec_energy_forces_tabulated", "eec_last_error",
+    "eec_add_rms_norm", "eec_add_rms_norm_backward", "eec_add_rms_norm_backward_workspace_bytes",
+    "eec_linear", "eec_linear_workspace_bytes", "eec_linear_backward", "eec_linear_backward_workspace_bytes",
 )
 PHASES = ("prepare", "forward", "readout", "backward", "scatter")
 VARIANTS = {"direct": 0, "folded": 1, "tabulated": 2}
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
 class EECError(RuntimeError):
@@ -117,6 +121,20 @@ def lib() -> ctypes.CDLL:
     L.eec_radial_table_levels.restype = sz
     L.eec_radial_table_levels.argtypes = [P(_Model), i32]
     L.eec_radial_table_build.argtypes = [vp, P(_Model), i32, vp, sz, vp, vp]
+    L.eec_add_rms_norm.restype = ctypes.c_int
+    L.eec_add_rms_norm.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, dbl, vp, vp, vp, vp]
+    L.eec_add_rms_norm_backward_workspace_bytes.restype = sz
+    L.eec_add_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.eec_add_rms_norm_backward.restype = ctypes.c_int
+    L.eec_add_rms_norm_backward.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp, sz]
+    L.eec_linear_workspace_bytes.restype = sz
+    L.eec_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.eec_linear.restype = ctypes.c_int
+    L.eec_linear.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, i64, i32, vp, vp, vp, sz]
+    L.eec_linear_backward_workspace_bytes.restype = sz
+    L.eec_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    L.eec_linear_backward.restype = ctypes.c_int
+    L.eec_linear_backward.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, sz]
     _lib = L
     return L
 
@@ -409,6 +427,139 @@ def energy_forces_folded_noalloc(graph: Graph, pos: torch.Tensor, box, species: 
                                                   _ptr(out.get("atom_energy")), _ptr(out["forces"]),
                                                   _ptr(out.get("virial"))), "energy_forces_folded_noalloc")
     return out
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, width: int, dtype, device) -> int:
+    """Checks a [rows][width] matrix of adjacent columns; returns its row stride."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be [{rows}][{width}], not {list(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, not {t.dtype} on {t.device}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"the columns of {name} must be adjacent")
+    return t.stride(0) if rows > 1 else width
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, dtype, device):
+    """Checks a contiguous vector of n elements (or None); returns its address."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous elements of {dtype} on {device}")
+    return t.data_ptr()
+
+
+def _dense_input(t: torch.Tensor, name: str):
+    """(rows, width, dtype, device) of an operator's first matrix."""
+    if t.dim() != 2 or t.dtype not in DTYPES or not t.is_cuda:
+        raise ValueError(f"{name} must be a device matrix of float32, float16, bfloat16 or (linear) float8_e4m3fn")
+    return t.shape[0], t.shape[1], t.dtype, t.device
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                 eps: float = 1e-6, quantize: bool = False, save_rstd: bool = False) -> dict:
+    """eec_add_rms_norm on rows of ``x`` (any row stride): ``y``, ``sum`` (x +
+    residual; x itself without a residual), with ``quantize`` ``y`` in
+    float8_e4m3fn and its row ``scale``, with ``save_rstd`` ``rstd``."""
+    rows, n, dt, dev = _dense_input(x, "x")
+    ldx = _matrix(x, "x", rows, n, dt, dev)
+    ldr = _matrix(residual, "residual", rows, n, dt, dev) if residual is not None else 0
+    w = _vector(weight, "weight", n, dt, dev)
+    out = dict(y=torch.empty((rows, n), dtype=torch.float8_e4m3fn if quantize else dt, device=dev), sum=x)
+    total = scale = rstd = None
+    if residual is not None:
+        total = out["sum"] = torch.empty((rows, n), dtype=dt, device=dev)
+    if quantize:
+        scale = out["scale"] = torch.empty(rows, dtype=torch.float32, device=dev)
+    if save_rstd:
+        rstd = out["rstd"] = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(lib().eec_add_rms_norm(_stream(dev), rows, n, DTYPES[dt], x.data_ptr(), ldx, _ptr(residual), ldr, w,
+                                  float(eps), _ptr(total), out["y"].data_ptr(), _ptr(scale), _ptr(rstd)),
+           "add_rms_norm")
+    return out
+
+
+def add_rms_norm_backward(gy: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
+                          gsum: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> dict:
+    """eec_add_rms_norm_backward: ``gx`` (the gradient of x and of residual) and
+    ``gweight`` (None without a weight), from the forward's ``sum`` and ``rstd``."""
+    rows, n, dt, dev = _dense_input(sum, "sum")
+    lds = _matrix(sum, "sum", rows, n, dt, dev)
+    ldgy = _matrix(gy, "gy", rows, n, dt, dev)
+    ldgs = _matrix(gsum, "gsum", rows, n, dt, dev) if gsum is not None else 0
+    w = _vector(weight, "weight", n, dt, dev)
+    rs = _vector(rstd, "rstd", rows, torch.float32, dev)
+    gx = torch.empty((rows, n), dtype=dt, device=dev)
+    gw = ws = None
+    if weight is not None:
+        gw = torch.empty(n, dtype=dt, device=dev)
+        ws = workspace
+        if ws is None:
+            ws = _workspace(lib().eec_add_rms_norm_backward_workspace_bytes(rows, n), dev)
+    _check(lib().eec_add_rms_norm_backward(_stream(dev), rows, n, DTYPES[dt], gy.data_ptr(), ldgy, sum.data_ptr(),
+                                           lds, w, rs, _ptr(gsum), ldgs, gx.data_ptr(), _ptr(gw), _ptr(ws),
+                                           ws.numel() if ws is not None else 0), "add_rms_norm_backward")
+    return dict(gx=gx, gweight=gw)
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+           residual: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
+           w_scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, save_preact: bool = False,
+           workspace: torch.Tensor | None = None) -> dict:
+    """eec_linear: ``y`` = act(x w^T + bias) + residual and, with
+    ``save_preact``, ``preact`` (what act is applied to).  float8_e4m3fn
+    operands take their row scales and ``out_dtype`` (bfloat16 by default)."""
+    rows, k, dt, dev = _dense_input(x, "x")
+    n = w.shape[0]
+    ot = out_dtype if out_dtype is not None else (torch.bfloat16 if dt == torch.float8_e4m3fn else dt)
+    if ot not in DTYPES or act not in ACTS:
+        raise ValueError(f"unknown out_dtype {ot} or activation {act!r}")
+    ldx = _matrix(x, "x", rows, k, dt, dev)
+    ldw = _matrix(w, "w", n, k, dt, dev)
+    ldr = _matrix(residual, "residual", rows, n, ot, dev) if residual is not None else 0
+    xs = _vector(x_scale, "x_scale", rows, torch.float32, dev)
+    wsc = _vector(w_scale, "w_scale", n, torch.float32, dev)
+    b = _vector(bias, "bias", n, ot, dev)
+    y = torch.empty((rows, n), dtype=ot, device=dev)
+    out = dict(y=y)
+    if save_preact:
+        out["preact"] = torch.empty((rows, n), dtype=ot, device=dev)
+    ws = workspace
+    if ws is None:
+        need = lib().eec_linear_workspace_bytes(rows, n, k, DTYPES[dt])
+        ws = _workspace(need, dev) if need else None
+    _check(lib().eec_linear(_stream(dev), rows, n, k, DTYPES[dt], DTYPES[ot], x.data_ptr(), ldx, xs, w.data_ptr(),
+                            ldw, wsc, b, _ptr(residual), ldr, ACTS[act], y.data_ptr(), _ptr(out.get("preact")),
+                            _ptr(ws), ws.numel() if ws is not None else 0), "linear")
+    return out
+
+
+def linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: torch.Tensor | None = None,
+                    act: str = "none", bias: bool = True, workspace: torch.Tensor | None = None) -> dict:
+    """eec_linear_backward: ``gx``, ``gw`` and, with ``bias``, ``gbias`` (the
+    gradient of the residual is ``gy``)."""
+    rows, k, dt, dev = _dense_input(x, "x")
+    n = w.shape[0]
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    ldx = _matrix(x, "x", rows, k, dt, dev)
+    ldw = _matrix(w, "w", n, k, dt, dev)
+    ldgy = _matrix(gy, "gy", rows, n, dt, dev)
+    if act != "none":
+        if preact is None:
+            raise ValueError("an activation's backward needs preact")
+        if _matrix(preact, "preact", rows, n, dt, dev) != n:
+            raise ValueError("preact must be contiguous")
+    gx = torch.empty((rows, k), dtype=dt, device=dev)
+    gw = torch.empty((n, k), dtype=dt, device=dev)
+    gb = torch.empty(n, dtype=dt, device=dev) if bias else None
+    ws = workspace
+    if ws is None:
+        ws = _workspace(lib().eec_linear_backward_workspace_bytes(rows, n, k, DTYPES[dt], ACTS[act]), dev)
+    _check(lib().eec_linear_backward(_stream(dev), rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
+                                     x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(preact), gx.data_ptr(),
+                                     gw.data_ptr(), _ptr(gb), ws.data_ptr(), ws.numel()), "linear_backward")
+    return dict(gx=gx, gw=gw, gbias=gb)
 
 
 class HipEvents:

@@ -520,4 +520,174 @@ eec_status eec_radial_table_build(void* stream, const eec_model* m, int32_t log2
   return launched("radial_table_build");
 }
 
+// ---- atom-wise dense operators
+
+namespace {
+
+constexpr int64_t MAX_SIZE = INT32_MAX;
+
+size_t dtype_bytes(int32_t t) { return t == EEC_F32 ? 4 : t == EEC_E4M3 ? 1 : 2; }
+bool float_dtype(int32_t t) { return t == EEC_F32 || t == EEC_F16 || t == EEC_BF16; }
+
+// A [rows][width] matrix with a row stride; nothing is read of an empty one.
+eec_status check_matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int32_t dtype, const char* name) {
+  if (rows == 0 || width == 0) return EEC_OK;
+  if (p == nullptr) return fail(EEC_ERR_NULL, std::string(name) + " is NULL");
+  if (ld < width || ld > MAX_SIZE) return fail(EEC_ERR_SHAPE, std::string(name) + ": bad row stride");
+  if (((uintptr_t)p & (dtype_bytes(dtype) - 1)) != 0)
+    return fail(EEC_ERR_SHAPE, std::string(name) + " is not aligned to its elements");
+  return EEC_OK;
+}
+eec_status check_optional(const void* p, int64_t rows, int64_t width, int64_t ld, int32_t dtype, const char* name) {
+  return p == nullptr ? EEC_OK : check_matrix(p, rows, width, ld, dtype, name);
+}
+Span matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int32_t dtype, const char* name) {
+  const size_t n = rows > 0 && width > 0 ? (size_t)(rows - 1) * (size_t)ld + (size_t)width : 0;
+  return span(p, n * dtype_bytes(dtype), name);
+}
+bool bad_size(int64_t n) { return n < 0 || n > MAX_SIZE; }
+
+eec_status check_act(int32_t act) {
+  if (act < EEC_ACT_NONE || act > EEC_ACT_GELU) return fail(EEC_ERR_SHAPE, "unknown activation");
+  return EEC_OK;
+}
+
+}  // namespace
+
+eec_status eec_add_rms_norm(void* stream, int64_t rows, int64_t width, int32_t dtype, const void* x, int64_t ldx,
+                            const void* residual, int64_t ldr, const void* weight, double eps, void* sum, void* y,
+                            float* scale, float* rstd) {
+  if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
+  if (bad_size(rows) || width < 1 || bad_size(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
+  if (!(isfinite(eps) && eps >= 0.0)) return fail(EEC_ERR_SHAPE, "eps must be finite and >= 0");
+  const int32_t ytype = scale != nullptr ? (int32_t)EEC_E4M3 : dtype;
+  TRY(check_matrix(x, rows, width, ldx, dtype, "x"));
+  TRY(check_optional(residual, rows, width, ldr, dtype, "residual"));
+  TRY(check_optional(weight, 1, width, width, dtype, "weight"));
+  TRY(check_optional(sum, rows, width, width, dtype, "sum"));
+  TRY(check_matrix(y, rows, width, width, ytype, "y"));
+  TRY(check_optional(scale, rows, 1, 1, EEC_F32, "scale"));
+  TRY(check_optional(rstd, rows, 1, 1, EEC_F32, "rstd"));
+  TRY(check_alias({matrix(sum, rows, width, width, dtype, "sum"), matrix(y, rows, width, width, ytype, "y"),
+                   matrix(scale, rows, 1, 1, EEC_F32, "scale"), matrix(rstd, rows, 1, 1, EEC_F32, "rstd")},
+                  {matrix(x, rows, width, ldx, dtype, "x"), matrix(residual, rows, width, ldr, dtype, "residual"),
+                   matrix(weight, 1, width, width, dtype, "weight")}));
+  if (rows == 0) return ok();
+  launch_norm((hipStream_t)stream, dtype, rows, width, x, ldx, residual, ldr, weight, (float)eps, sum, y, scale, rstd);
+  return launched("add_rms_norm");
+}
+
+size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t width) {
+  if (bad_size(rows) || width < 1 || bad_size(width)) return 0;
+  return norm_bwd_workspace(rows, width);
+}
+
+eec_status eec_add_rms_norm_backward(void* stream, int64_t rows, int64_t width, int32_t dtype, const void* gy,
+                                     int64_t ldgy, const void* sum, int64_t lds, const void* weight,
+                                     const float* rstd, const void* gsum, int64_t ldgs, void* gx, void* gweight,
+                                     void* workspace, size_t workspace_bytes) {
+  if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
+  if (bad_size(rows) || width < 1 || bad_size(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
+  TRY(check_matrix(gy, rows, width, ldgy, dtype, "gy"));
+  TRY(check_matrix(sum, rows, width, lds, dtype, "sum"));
+  TRY(check_matrix(rstd, rows, 1, 1, EEC_F32, "rstd"));
+  TRY(check_optional(weight, 1, width, width, dtype, "weight"));
+  TRY(check_optional(gsum, rows, width, ldgs, dtype, "gsum"));
+  TRY(check_optional(gx, rows, width, width, dtype, "gx"));
+  TRY(check_optional(gweight, 1, width, width, dtype, "gweight"));
+  const size_t need = gweight ? norm_bwd_workspace(rows, width) : 0;
+  TRY(check_ws(workspace, workspace_bytes, need));
+  TRY(check_alias({matrix(gx, rows, width, width, dtype, "gx"), matrix(gweight, 1, width, width, dtype, "gweight"),
+                   span(workspace, workspace_bytes, "workspace")},
+                  {matrix(gy, rows, width, ldgy, dtype, "gy"), matrix(sum, rows, width, lds, dtype, "sum"),
+                   matrix(rstd, rows, 1, 1, EEC_F32, "rstd"), matrix(weight, 1, width, width, dtype, "weight"),
+                   matrix(gsum, rows, width, ldgs, dtype, "gsum")}));
+  if ((rows == 0 || gx == nullptr) && gweight == nullptr) return ok();
+  launch_norm_bwd((hipStream_t)stream, dtype, rows, width, gy, ldgy, sum, lds, weight, rstd, gsum, ldgs, gx, gweight,
+                  (char*)workspace);
+  return launched("add_rms_norm_backward");
+}
+
+static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
+  if (bad_size(rows) || bad_size(outer) || bad_size(inner)) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
+  // output tiles of one product, counted as the kernels launch them
+  const int64_t r = rows / 128 + 1, o = outer / 128 + 1, i = inner / 128 + 1;
+  if (r * o >= (1 << 23) || r * i >= (1 << 23) || o * i >= (1 << 23))
+    return fail(EEC_ERR_SHAPE, "a product of more than 2^37 outputs");
+  return EEC_OK;
+}
+
+size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype) {
+  if (bad_size(rows) || bad_size(outer) || bad_size(inner) || (!float_dtype(dtype) && dtype != EEC_E4M3)) return 0;
+  return linear_workspace(rows, outer, inner, dtype);
+}
+
+eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype,
+                      const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                      const float* w_scale, const void* bias, const void* residual, int64_t ldr, int32_t act,
+                      void* y, void* preact, void* workspace, size_t workspace_bytes) {
+  const bool eight = dtype == EEC_E4M3;
+  if (!eight && !float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16, bf16 or e4m3");
+  if (eight ? !float_dtype(out_dtype) : out_dtype != dtype)
+    return fail(EEC_ERR_SHAPE, "out_dtype must be dtype (f32, f16 or bf16 with e4m3 operands)");
+  TRY(check_act(act));
+  TRY(check_linear(rows, outer, inner));
+  TRY(check_matrix(x, rows, inner, ldx, dtype, "x"));
+  TRY(check_matrix(w, outer, inner, ldw, dtype, "w"));
+  if (eight) {
+    TRY(check_matrix(x_scale, rows, 1, 1, EEC_F32, "x_scale"));
+    TRY(check_matrix(w_scale, outer, 1, 1, EEC_F32, "w_scale"));
+  } else if (x_scale != nullptr || w_scale != nullptr) {
+    return fail(EEC_ERR_SHAPE, "scales belong to e4m3 operands");
+  }
+  TRY(check_optional(bias, 1, outer, outer, out_dtype, "bias"));
+  TRY(check_optional(residual, rows, outer, ldr, out_dtype, "residual"));
+  TRY(check_matrix(y, rows, outer, outer, out_dtype, "y"));
+  TRY(check_optional(preact, rows, outer, outer, out_dtype, "preact"));
+  TRY(check_ws(workspace, workspace_bytes, linear_workspace(rows, outer, inner, dtype)));
+  TRY(check_alias({matrix(y, rows, outer, outer, out_dtype, "y"), matrix(preact, rows, outer, outer, out_dtype, "preact"),
+                   span(workspace, workspace_bytes, "workspace")},
+                  {matrix(x, rows, inner, ldx, dtype, "x"), matrix(w, outer, inner, ldw, dtype, "w"),
+                   matrix(x_scale, rows, 1, 1, EEC_F32, "x_scale"), matrix(w_scale, outer, 1, 1, EEC_F32, "w_scale"),
+                   matrix(bias, 1, outer, outer, out_dtype, "bias"),
+                   matrix(residual, rows, outer, ldr, out_dtype, "residual")}));
+  if (rows == 0 || outer == 0) return ok();
+  const LinearArgs a{rows, outer, inner, x, w, bias, residual, ldx, ldw, ldr, x_scale, w_scale, dtype, out_dtype, act,
+                     y, preact};
+  launch_linear((hipStream_t)stream, a, (char*)workspace);
+  return launched("linear");
+}
+
+size_t eec_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
+  if (bad_size(rows) || bad_size(outer) || bad_size(inner) || !float_dtype(dtype)) return 0;
+  return linear_bwd_workspace(rows, outer, inner, dtype, act);
+}
+
+eec_status eec_linear_backward(void* stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act,
+                               const void* gy, int64_t ldgy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                               const void* preact, void* gx, void* gw, void* gbias, void* workspace,
+                               size_t workspace_bytes) {
+  if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
+  TRY(check_act(act));
+  TRY(check_linear(rows, outer, inner));
+  TRY(check_matrix(gy, rows, outer, ldgy, dtype, "gy"));
+  if (gw) TRY(check_matrix(x, rows, inner, ldx, dtype, "x"));
+  if (gx) TRY(check_matrix(w, outer, inner, ldw, dtype, "w"));
+  if (act != EEC_ACT_NONE) TRY(check_matrix(preact, rows, outer, outer, dtype, "preact"));
+  TRY(check_optional(gx, rows, inner, inner, dtype, "gx"));
+  TRY(check_optional(gw, outer, inner, inner, dtype, "gw"));
+  TRY(check_optional(gbias, 1, outer, outer, dtype, "gbias"));
+  TRY(check_ws(workspace, workspace_bytes, linear_bwd_workspace(rows, outer, inner, dtype, act)));
+  TRY(check_alias({matrix(gx, rows, inner, inner, dtype, "gx"), matrix(gw, outer, inner, inner, dtype, "gw"),
+                   matrix(gbias, 1, outer, outer, dtype, "gbias"), span(workspace, workspace_bytes, "workspace")},
+                  {matrix(gy, rows, outer, ldgy, dtype, "gy"), matrix(x, rows, inner, ldx, dtype, "x"),
+                   matrix(w, outer, inner, ldw, dtype, "w"), matrix(preact, rows, outer, outer, dtype, "preact")}));
+  if (outer == 0 && inner == 0) return ok();
+  const LinearBwdArgs a{rows, outer, inner, gy, x, w, preact, ldgy, ldx, ldw, dtype, act,
+                        rows > 0 && inner > 0 ? gx : nullptr, outer > 0 && inner > 0 ? gw : nullptr,
+                        outer > 0 ? gbias : nullptr};
+  launch_linear_bwd((hipStream_t)stream, a, (char*)workspace);
+  return launched("linear_backward");
+}
+
 }  // extern "C"

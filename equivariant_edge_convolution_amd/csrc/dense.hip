@@ -1,0 +1,485 @@
+// Dense layer y = act(x w^T + bias) + residual and its backward products.
+//
+// All products are C[m][n] = sum_k A(m, k) B(n, k), m the rows of x (of gz, of
+// gz^T) and n the rows of w (the columns of w, of x):
+//   forward  A = x  [m][k],  B = w  [n][k];
+//   gx       A = gz [m][k],  B = w  [k][n];
+//   gw       A = gz [k][m],  B = x  [k][n].
+#include <algorithm>
+#include <type_traits>
+
+#include "dense.hpp"
+#include "eec_internal.hpp"
+
+namespace eec {
+namespace {
+using namespace dense;
+
+// ------------------------------------------------------------------ epilogue
+
+struct Epilogue {
+  const void *bias, *residual;
+  int64_t ldr;
+  const float *x_scale, *w_scale;
+  int32_t act;
+  void *y, *preact;
+  int64_t M, N;
+  float* part;  // split sums [split][M][N] instead of all of the above, or NULL
+};
+
+// L consecutive columns of one row, from their sums over k.
+template <typename O, int L>
+__device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, int64_t n, float (&v)[L]) {
+  const int64_t left = e.N - n;
+  if (m >= e.M || left <= 0) return;
+  float t[L];
+  if (e.x_scale) {
+    const float xs = e.x_scale[m];
+    load_run(e.w_scale + n, left, t);
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] *= xs * t[i];
+  }
+  if (e.bias) {
+    load_run((const O*)e.bias + n, left, t);
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] += t[i];
+  }
+  if (e.preact) store_run((O*)e.preact + m * e.N + n, left, v);
+  if (e.act != EEC_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] = act_value(v[i], e.act);
+  }
+  if (e.residual) {
+    load_run((const O*)e.residual + m * e.ldr + n, left, t);
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] += t[i];
+  }
+  store_run((O*)e.y + m * e.N + n, left, v);
+}
+
+// Adds the splits in order and finishes: 4 columns a thread.
+template <typename O>
+__global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
+  const int64_t per_row = (e.N + 3) / 4, total = e.M * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / per_row, n = i % per_row * 4;
+    float v[4], t[4];
+    load_run(e.part + m * e.N + n, e.N - n, v);
+    for (int s = 1; s < splits; ++s) {
+      load_run(e.part + ((int64_t)s * e.M + m) * e.N + n, e.N - n, t);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += t[c];
+    }
+    finish_run<O>(e, m, n, v);
+  }
+}
+
+// ------------------------------------------------------------------ matrix instructions
+
+// float32 as the exact sum of three bf16 parts (8 + 8 + 8 significant bits, cut
+// towards zero, so that no part overflows; below 2^-109 the last parts end at
+// bf16's smallest step, 2^-133).  NaN and infinities stay in the first part, the
+// others are 0 then.
+__device__ __forceinline__ void split3(float x, bf16& h, bf16& m, bf16& l) {
+  const uint32_t u = __float_as_uint(x);
+  const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+  const uint32_t hi = (u & 0xffff0000u) | (x != x ? 0x400000u : 0u);  // a NaN keeps a bit of its fraction
+  const float r = finite ? x - __uint_as_float(hi) : 0.f;
+  const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
+  const float rl = r - __uint_as_float(mid);
+  h = __builtin_bit_cast(bf16, (uint16_t)(hi >> 16));
+  m = __builtin_bit_cast(bf16, (uint16_t)(mid >> 16));
+  l = __builtin_bit_cast(bf16, (uint16_t)(__float_as_uint(rl) >> 16));
+}
+
+template <typename T>
+struct Mat;  // operand planes in LDS (element type, count), and the product of 8-element fragments in ACCS sums
+template <>
+struct Mat<f16> {
+  using E = f16;
+  static constexpr int PLANES = 1, ACCS = 1;
+  using Frag = f16x8;
+  static __device__ __forceinline__ void mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 (&c)[1]) {
+    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0], a[0], c[0], 0, 0, 0);
+  }
+  static __device__ __forceinline__ float total(const f32x4 (&c)[1], int i) { return c[0][i]; }
+};
+template <>
+struct Mat<bf16> {
+  using E = bf16;
+  static constexpr int PLANES = 1, ACCS = 1;
+  using Frag = bf16x8;
+  static __device__ __forceinline__ void mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 (&c)[1]) {
+    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[0], c[0], 0, 0, 0);
+  }
+  static __device__ __forceinline__ float total(const f32x4 (&c)[1], int i) { return c[0][i]; }
+};
+// The 8-bit instructions align a sum's products before they add them: over all
+// bit patterns their result was up to 9e-5 of sum |a||b| off (1e-5 for normally
+// distributed values), where the bf16 instruction on the same values was exact
+// to 1e-7.  That is far below the rounding of a 16-bit output; a float32 output
+// is computed from the same codes widened to bf16 (exact, e4m3_wide).
+template <>
+struct Mat<e4m3> {
+  using E = e4m3;
+  static constexpr int PLANES = 1, ACCS = 1;
+  using Frag = long;
+  static __device__ __forceinline__ void mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 (&c)[1]) {
+    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b[0], a[0], c[0], 0, 0, 0);
+  }
+  static __device__ __forceinline__ float total(const f32x4 (&c)[1], int i) { return c[0][i]; }
+};
+struct e4m3_wide : e4m3 {};
+template <>
+struct Mat<e4m3_wide> : Mat<bf16> {};
+template <>
+struct Mat<float> {
+  using E = bf16;
+  static constexpr int PLANES = 3, ACCS = 2;
+  using Frag = bf16x8;
+  // The products of the first parts in one sum, the five next in size in another;
+  // the three left out are below 2^-24 of the whole.  The sums are kept apart
+  // because an infinity times a part that is 0 makes the second a NaN: a first
+  // sum that is not finite is the result by itself.
+  static __device__ __forceinline__ void mul(const Frag (&b)[3], const Frag (&a)[3], f32x4 (&c)[2]) {
+    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[0], c[0], 0, 0, 0);
+    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[1], a[1], c[1], 0, 0, 0);
+    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[2], a[0], c[1], 0, 0, 0);
+    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[2], c[1], 0, 0, 0);
+    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[1], a[0], c[1], 0, 0, 0);
+    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[1], c[1], 0, 0, 0);
+  }
+  static __device__ __forceinline__ float total(const f32x4 (&c)[2], int i) {
+    return (__float_as_uint(c[0][i]) & 0x7f800000u) == 0x7f800000u ? c[0][i] : c[0][i] + c[1][i];
+  }
+};
+
+// 8 elements of T as they come from memory.
+template <typename T>
+struct Raw {
+  T v[8];
+};
+
+// Writes one 8-element chunk into its planes, `stride` bytes apart.
+template <typename T>
+__device__ __forceinline__ void put_chunk(char* at, int stride, const Raw<T>& r) {
+  if constexpr (std::is_same<T, float>::value) {
+    bf16 p[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split3(r.v[i], p[0][i], p[1][i], p[2][i]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) __builtin_memcpy(__builtin_assume_aligned(at + q * stride, 16), p[q], 16);
+  } else if constexpr (std::is_same<T, e4m3_wide>::value) {
+    int q[2];
+    __builtin_memcpy(q, &r, 8);
+    bf16x8 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(q[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(q[i], true);
+      w[4 * i] = (bf16)lo[0];
+      w[4 * i + 1] = (bf16)lo[1];
+      w[4 * i + 2] = (bf16)hi[0];
+      w[4 * i + 3] = (bf16)hi[1];
+    }
+    __builtin_memcpy(__builtin_assume_aligned(at, 16), &w, 16);
+  } else {
+    __builtin_memcpy(__builtin_assume_aligned(at, sizeof(r)), &r, sizeof(r));
+  }
+}
+
+// ------------------------------------------------------------------ general product
+
+// Column of a 64-column group held at LDS row p: the four 16-row matrix tiles of
+// a wave take the columns so that a lane ends with 16 adjacent ones (see acc).
+__device__ __forceinline__ int column_at(int p) { return ((p >> 2) & 3) * 16 + (p >> 4 & 3) * 4 + (p & 3); }
+__device__ __forceinline__ int row_of_column(int n) {
+  return (n & ~63) | ((n >> 2) & 3) * 16 | ((n >> 4) & 3) * 4 | (n & 3);
+}
+
+struct Product {
+  const void *a, *b;
+  int64_t lda, ldb;
+  int64_t M, N, K;
+  int64_t k_split;  // k of one split, a multiple of GBK
+};
+
+constexpr int GBM = 128, GBN = 128, GBK = 32;
+
+// A tile of 128 lines x 32 k of one operand, two 8-element chunks per thread.
+// KC: k runs along memory (a chunk is one run), otherwise the lines do (a chunk
+// is 8 runs of 2 lines).
+template <typename T, bool KC, bool IS_B>
+struct Stage {
+  static constexpr int ROW = GBK * sizeof(typename Mat<T>::E) + 8 * sizeof(typename Mat<T>::E);
+  static constexpr int PLANE = GBM * ROW;
+  Raw<T> r[2];
+
+  __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int64_t line0, int64_t lines, int64_t k0,
+                                       int64_t k_end) {
+    if constexpr (KC) {
+      const int64_t k = k0 + (threadIdx.x & 3) * 8, left = k_end - k;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t line = min(line0 + (threadIdx.x >> 2) + 64 * i, lines - 1);  // lines past the end: not stored
+        const T* s = p + line * ld + k;
+        if (left >= 8) {
+          __builtin_memcpy(&r[i], s, sizeof(r[i]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[i].v[j] = j < left ? s[j] : T{};
+        }
+      }
+    } else {
+      const int64_t line = line0 + (threadIdx.x & 63) * 2;
+      const int64_t k = k0 + (threadIdx.x >> 6) * 8;
+      const T* s = p + k * ld + line;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        T two[2] = {};
+        if (k + j < k_end) {
+          if (line + 2 <= lines)
+            __builtin_memcpy(two, s + j * ld, sizeof(two));
+          else if (line < lines)
+            two[0] = s[j * ld];
+        }
+        r[0].v[j] = two[0];
+        r[1].v[j] = two[1];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int line = KC ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x & 63) * 2 + i;
+      const int kc = KC ? threadIdx.x & 3 : threadIdx.x >> 6;
+      const int at = IS_B ? row_of_column(line) : line;
+      put_chunk<T>(lds + at * ROW + kc * 8 * sizeof(typename Mat<T>::E), PLANE, r[i]);
+    }
+  }
+};
+
+// 128 x 128 of C per workgroup, 64 x 64 per wave, any size, stride and alignment.
+// Operands pass through registers (where float32 is split into its parts and
+// k-major ones are turned) into LDS rows of 32 k; the next tile's loads are in
+// flight while the present one is multiplied.  B is the first factor of the
+// matrix instruction, so a lane holds one row of C and, by the column order in
+// LDS, 16 adjacent columns.
+template <typename T, typename O, bool A_KC, bool B_KC>
+__global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
+  using M_ = Mat<T>;
+  constexpr int P = M_::PLANES;
+  using SA = Stage<T, A_KC, false>;
+  using SB = Stage<T, B_KC, true>;
+  __shared__ __attribute__((aligned(16))) char lds[P * (SA::PLANE + SB::PLANE)];
+  char* lds_b = lds + P * SA::PLANE;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t tiles_n = (g.N + GBN - 1) / GBN;
+  const int64_t m0 = blockIdx.x / tiles_n * GBM, n0 = blockIdx.x % tiles_n * GBN;
+  const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  f32x4 acc[4][4][M_::ACCS] = {};
+  SA sa;
+  SB sb;
+  if (kb < ke) {
+    sa.load((const T*)g.a, g.lda, m0, g.M, kb, ke);
+    sb.load((const T*)g.b, g.ldb, n0, g.N, kb, ke);
+  }
+  for (int64_t k = kb; k < ke; k += GBK) {
+    __syncthreads();
+    sa.store(lds);
+    sb.store(lds_b);
+    __syncthreads();
+    if (k + GBK < ke) {
+      sa.load((const T*)g.a, g.lda, m0, g.M, k + GBK, ke);
+      sb.load((const T*)g.b, g.ldb, n0, g.N, k + GBK, ke);
+    }
+    typename M_::Frag fa[4][P], fb[P];
+    const int at = (lane & 15) * SA::ROW + (lane >> 4) * 8 * (int)sizeof(typename M_::E);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        __builtin_memcpy(&fa[i][p], __builtin_assume_aligned(lds + p * SA::PLANE + (wm + 16 * i) * SA::ROW + at, 8),
+                         sizeof(fb[p]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        __builtin_memcpy(&fb[p], __builtin_assume_aligned(lds_b + p * SB::PLANE + (wn + 16 * j) * SB::ROW + at, 8),
+                         sizeof(fb[p]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) M_::mul(fb, fa[i], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = m0 + wm + 16 * i + (lane & 15), n = n0 + wn + (lane >> 4) * 16;
+    float v[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = M_::total(acc[i][c >> 2], c & 3);
+    if (e.part) {
+      if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
+    } else {
+      finish_run<O>(e, m, n, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ gradient of the activation
+
+struct ActGrad {
+  const void *gy, *preact;
+  int64_t ldgy, rows, cols, per;  // rows of one strip
+  int32_t act;
+  void* gz;     // [rows][cols], or NULL
+  float* part;  // [strips][cols] column sums of gz before its rounding, or NULL
+};
+
+// gz = gy act'(preact) and its column sums: a wave takes 64 x 8 (float32: 4)
+// columns, a workgroup's waves deal the rows of a strip in turn.
+template <typename T>
+__global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
+  constexpr int V = VEC<T>;
+  __shared__ float join[3][64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = ((int64_t)blockIdx.x * 64 + lane) * V, left = a.cols - col;
+  const int64_t r0 = (int64_t)blockIdx.y * a.per, r1 = min(a.rows, r0 + a.per);
+  float sum[V] = {};
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    float g[V], z[V];
+    load_run((const T*)a.gy + r * a.ldgy + col, left, g);
+    if (a.act != EEC_ACT_NONE) {
+      load_run((const T*)a.preact + r * a.cols + col, left, z);
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] *= act_slope(z[i], a.act);
+    }
+    if (a.gz) store_run((T*)a.gz + r * a.cols + col, left, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] += g[i];
+  }
+  if (a.part == nullptr) return;
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) join[wave - 1][lane * V + i] = sum[i];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += join[k][lane * V + i];
+    store_run(a.part + (int64_t)blockIdx.y * a.cols + col, left, sum);
+  }
+}
+
+// ------------------------------------------------------------------ plans
+
+// Splits of k for a product of few tiles: enough workgroups to fill the chip's
+// 256 CUs about twice, while each split keeps at least 8 steps of k.
+int64_t product_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + GBM - 1) / GBM) * ((N + GBN - 1) / GBN);
+  const int64_t most = std::max<int64_t>(1, K / (8 * GBK));
+  return std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(1, tiles)));
+}
+size_t product_workspace(int64_t M, int64_t N, int64_t K) {
+  const int64_t s = product_splits(M, N, K);
+  return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
+}
+
+template <typename T, typename O, bool A_KC, bool B_KC>
+void product(hipStream_t st, Product g, Epilogue e, float* ws) {
+  if (g.M == 0 || g.N == 0) return;
+  const int64_t tiles = ((g.M + GBM - 1) / GBM) * ((g.N + GBN - 1) / GBN);
+  int64_t splits = product_splits(g.M, g.N, g.K);
+  g.k_split = (g.K + splits - 1) / splits;
+  g.k_split = std::max<int64_t>(GBK, (g.k_split + GBK - 1) / GBK * GBK);
+  splits = std::max<int64_t>(1, (g.K + g.k_split - 1) / g.k_split);
+  e.M = g.M;
+  e.N = g.N;
+  e.part = splits > 1 ? ws : nullptr;
+  k_product<T, O, A_KC, B_KC><<<dim3((unsigned)tiles, (unsigned)splits), 256, 0, st>>>(g, e);
+  if (splits > 1) {
+    const int64_t runs = g.M * ((g.N + 3) / 4);
+    k_join_splits<O><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)splits);
+  }
+}
+
+template <typename F>
+void by_type(int32_t dtype, F&& f) {
+  if (dtype == EEC_F32) return f(float());
+  if (dtype == EEC_F16) return f(f16());
+  f(bf16());
+}
+
+constexpr int STRIP_ROWS = 4;  // rows of a strip at least, one for each wave
+int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
+  const int64_t per = 64 * (dtype == EEC_F32 ? 4 : 8), wide = (cols + per - 1) / per;
+  return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 2048 / std::max<int64_t>(1, wide)));
+}
+
+struct BwdPlan {
+  size_t off_gz, off_part, off_split, bytes;
+};
+BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
+  BwdPlan p{};
+  size_t at = 0;
+  p.off_gz = at;
+  if (act != EEC_ACT_NONE) at += align256((size_t)rows * (size_t)outer * (dtype == EEC_F32 ? 4 : 2));
+  p.off_part = at;
+  at += align256(4 * (size_t)act_grad_strips(rows, outer, dtype) * (size_t)outer);
+  p.off_split = at;
+  at += std::max(product_workspace(rows, inner, outer), product_workspace(outer, inner, rows));
+  p.bytes = at;
+  return p;
+}
+
+}  // namespace
+
+size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype) {
+  return product_workspace(rows, outer, inner);
+}
+
+void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) {
+  const Product g{a.x, a.w, a.ldx, a.ldw, a.rows, a.outer, a.inner, 0};
+  const Epilogue e{a.bias, a.residual, a.ldr, a.x_scale, a.w_scale, a.act, a.y, a.preact, 0, 0, nullptr};
+  by_type(a.out_dtype, [&](auto zero) {
+    using O = decltype(zero);
+    using E = std::conditional_t<std::is_same<O, float>::value, e4m3_wide, e4m3>;
+    if (a.dtype == EEC_E4M3)
+      product<E, O, true, true>(st, g, e, (float*)ws);
+    else
+      product<O, O, true, true>(st, g, e, (float*)ws);
+  });
+}
+
+size_t linear_bwd_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
+  return bwd_plan(rows, outer, inner, dtype, act).bytes;
+}
+
+void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
+  const BwdPlan p = bwd_plan(a.rows, a.outer, a.inner, a.dtype, a.act);
+  by_type(a.dtype, [&](auto zero) {
+    using T = decltype(zero);
+    const bool products = a.gx != nullptr || a.gw != nullptr, shaped = a.act != EEC_ACT_NONE && products;
+    const void* gz = shaped ? (const void*)(ws + p.off_gz) : a.gy;
+    const int64_t ldgz = shaped ? a.outer : a.ldgy;
+    if (a.outer > 0 && ((shaped && a.rows > 0) || a.gbias)) {
+      const int64_t strips = act_grad_strips(a.rows, a.outer, a.dtype), cols = 64 * VEC<T>;
+      const ActGrad q{a.gy,  a.preact, a.ldgy, a.rows, a.outer, (a.rows + strips - 1) / strips,
+                      a.act, shaped ? ws + p.off_gz : nullptr, a.gbias ? (float*)(ws + p.off_part) : nullptr};
+      k_act_grad<T><<<dim3((unsigned)((a.outer + cols - 1) / cols), (unsigned)strips), 256, 0, st>>>(q);
+      if (a.gbias) launch_column_sum(st, a.dtype, (const float*)(ws + p.off_part), (int)strips, a.outer, a.gbias);
+    }
+    float* split = (float*)(ws + p.off_split);
+    Epilogue e{};
+    if (a.gx) {
+      e.y = a.gx;
+      product<T, T, true, false>(st, Product{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0}, e, split);
+    }
+    if (a.gw) {
+      e.y = a.gw;
+      product<T, T, false, false>(st, Product{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0}, e, split);
+    }
+  });
+}
+
+}  // namespace eec

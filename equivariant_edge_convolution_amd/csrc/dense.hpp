@@ -1,0 +1,110 @@
+// Device building blocks shared by the atom-wise dense operators (norm.hip,
+// dense.hip): element types, loads and stores of short runs, activations.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/eec.h"
+
+namespace eec {
+namespace dense {
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+struct e4m3 {
+  uint8_t bits;
+};
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Elements of one 16-byte access.
+template <typename T>
+constexpr int VEC = 16 / (int)sizeof(T);
+
+// N consecutive elements as floats, of which the first `valid` exist; the
+// others read as zero.  The pointer needs only its elements' alignment: 16-byte
+// global accesses of any alignment are ordinary here (rows of odd width), and an
+// aligned address makes the same instruction fast.
+template <typename T, int N>
+__device__ __forceinline__ void load_run(const T* __restrict__ p, int64_t valid, float (&v)[N]) {
+  if (valid >= N) {
+    T t[N];
+    __builtin_memcpy(t, p, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = (float)t[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < valid ? (float)p[i] : 0.f;
+  }
+}
+
+// The first `valid` of N floats, each rounded once to T (to nearest even).
+template <typename T, int N>
+__device__ __forceinline__ void store_run(T* __restrict__ p, int64_t valid, const float (&v)[N]) {
+  if (valid >= N) {
+    T t[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) t[i] = (T)v[i];
+    __builtin_memcpy(p, t, sizeof(t));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < valid) p[i] = (T)v[i];
+  }
+}
+
+// The same in e4m3 (values within +-448, or NaN, which keeps its code).
+template <int N>
+__device__ __forceinline__ void store_run_e4m3(uint8_t* __restrict__ p, int64_t valid, const float (&v)[N]) {
+  static_assert(N % 4 == 0, "e4m3 runs are packed four to a register");
+  int q[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+    q[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], q[i], true);
+  }
+  if (valid >= N) {
+    __builtin_memcpy(p, q, N);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < valid) p[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + expf(-z)); }
+
+// act(z) and its slope; the branch is uniform over the launch.
+__device__ __forceinline__ float act_value(float z, int act) {
+  if (act == EEC_ACT_SILU) return z * sigmoid(z);
+  if (act == EEC_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == EEC_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
+  return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == EEC_ACT_SILU) {
+    const float p = sigmoid(z);
+    return p * (1.f + z * (1.f - p));
+  }
+  if (act == EEC_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+  if (act == EEC_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  return 1.f;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float nan_max(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float wave_nan_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = nan_max(v, __shfl_xor(v, o));
+  return v;
+}
+
+}  // namespace dense
+}  // namespace eec

@@ -167,6 +167,38 @@ void launch_fold_table(hipStream_t s, const ConvPlan& p, const eec_graph* g, con
                        double cutoff, const eec_model* m, int log2_pieces, const float* tab,
                        const int32_t* level, float* ei, float* gout, char* ws);
 
+// ---- atom-wise dense operators (argument types as in eec.h; dtype checked by the caller)
+void launch_norm(hipStream_t s, int32_t dtype, int64_t rows, int64_t width, const void* x, int64_t ldx,
+                 const void* residual, int64_t ldr, const void* weight, float eps, void* sum, void* y, float* scale,
+                 float* rstd);
+size_t norm_bwd_workspace(int64_t rows, int64_t width);
+void launch_norm_bwd(hipStream_t s, int32_t dtype, int64_t rows, int64_t width, const void* gy, int64_t ldgy,
+                     const void* sum, int64_t lds, const void* weight, const float* rstd, const void* gsum,
+                     int64_t ldgs, void* gx, void* gweight, char* ws);
+// out[j] = sum_p part[p][j], rounded to dtype.
+void launch_column_sum(hipStream_t s, int32_t dtype, const float* part, int parts, int64_t n, void* out);
+
+// One dense layer, or one of its backward products.
+struct LinearArgs {
+  int64_t rows, outer, inner;
+  const void *x, *w, *bias, *residual;
+  int64_t ldx, ldw, ldr;
+  const float *x_scale, *w_scale;
+  int32_t dtype, out_dtype, act;
+  void *y, *preact;
+};
+size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
+void launch_linear(hipStream_t s, const LinearArgs& a, char* ws);
+struct LinearBwdArgs {
+  int64_t rows, outer, inner;
+  const void *gy, *x, *w, *preact;
+  int64_t ldgy, ldx, ldw;
+  int32_t dtype, act;
+  void *gx, *gw, *gbias;
+};
+size_t linear_bwd_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act);
+void launch_linear_bwd(hipStream_t s, const LinearBwdArgs& a, char* ws);
+
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace eec

@@ -381,6 +381,100 @@ EEC_API eec_status eec_energy_forces_timed(void *stream, const eec_graph *g, con
 
 EEC_API size_t eec_workspace_bytes(int32_t n_atoms, int64_t n_edges, const eec_model *m);
 
+/* ------------------------------------------------------------------------
+ * Atom-wise dense operators -- what a network on the atoms' features (rows =
+ * atoms, edges or tokens) is built from, beside the message: a residual
+ * addition with a root-mean-square norm, and a dense layer with bias,
+ * activation and residual, each with its backward, and both with 8-bit (e4m3)
+ * rows for evaluation.
+ *
+ * Conventions on top of those above
+ *   - A matrix input has a row stride in elements (ld* >= its width, so that a
+ *     range of columns of wider features is taken as it is, e.g. the l = 0
+ *     channels of A [n_atoms][16][C] with ld = 16 C); its columns are adjacent.
+ *     Outputs, vectors and preact are contiguous.  Pointers need the alignment of
+ *     their elements only.
+ *   - Sums, norms and products are accumulated in float32; every output is
+ *     rounded once, to nearest even, to its type.
+ *   - NaN and infinities propagate by the formulas.  Sizes may be odd, one, or
+ *     zero (a sum over nothing is 0).  Sizes and strides are at most 2^31 - 1. */
+typedef enum { EEC_F32 = 0, EEC_F16 = 1, EEC_BF16 = 2, EEC_E4M3 = 3 /* OCP: max 448, no infinity */ } eec_dtype;
+typedef enum {
+  EEC_ACT_NONE = 0,
+  EEC_ACT_RELU = 1,
+  EEC_ACT_SILU = 2, /* z / (1 + exp(-z))            */
+  EEC_ACT_GELU = 3  /* z (1 + erf(z / sqrt 2)) / 2  */
+} eec_act;
+
+/* eec_add_rms_norm --
+ *   s = x + residual (kept in float32),  rstd = 1 / sqrt(mean_j s_j^2 + eps),
+ *   y = s rstd weight
+ * per row of `width` elements (>= 1).
+ *   dtype     EEC_F32, EEC_F16 or EEC_BF16: the type of x, residual, weight, sum
+ *             and, without `scale`, y
+ *   residual, weight  or NULL (zeros, ones)
+ *   sum       [rows][width] s rounded to dtype, or NULL
+ *   y         [rows][width] dtype, or with `scale` e4m3
+ *   scale     [rows] float32 or NULL.  Given, y leaves in 8 bits:
+ *             scale = max(max_j |y_j|, 2^-100) / 448 and y_j / scale rounded to
+ *             e4m3; a row that holds a NaN or an infinity has a NaN scale and
+ *             NaN codes
+ *   rstd      [rows] float32 or NULL (what the backward reads)
+ *   eps       finite, >= 0 */
+EEC_API eec_status eec_add_rms_norm(void *stream, int64_t rows, int64_t width, int32_t dtype, const void *x,
+                            int64_t ldx, const void *residual, int64_t ldr, const void *weight, double eps,
+                            void *sum, void *y, float *scale, float *rstd);
+
+/* eec_add_rms_norm_backward -- with a = gy weight and xhat = s rstd:
+ *   gx      = rstd (a - xhat mean_j(a xhat)) + gsum   the gradient of x and of residual
+ *   gweight = sum_rows gy xhat                        (fixed order)
+ *   sum     s as the forward wrote it (or x itself where there was no residual)
+ *   gsum    the gradient that reaches s by other ways, or NULL
+ *   gx [rows][width], gweight [width]: dtype, either may be NULL
+ *   workspace >= eec_add_rms_norm_backward_workspace_bytes(rows, width), read
+ *   only for gweight (may be NULL without it) */
+EEC_API eec_status eec_add_rms_norm_backward(void *stream, int64_t rows, int64_t width, int32_t dtype,
+                                     const void *gy, int64_t ldgy, const void *sum, int64_t lds,
+                                     const void *weight, const float *rstd, const void *gsum, int64_t ldgs,
+                                     void *gx, void *gweight, void *workspace, size_t workspace_bytes);
+EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t width);
+
+/* eec_linear --
+ *   z = x w^T (x_scale_i w_scale_j with 8-bit operands) + bias,
+ *   y = act(z) + residual
+ *   x [rows][inner], w [outer][inner]: dtype;  bias [outer], residual
+ *   [rows][outer]: out_dtype, or NULL
+ *   out_dtype  dtype itself; with EEC_E4M3 operands any of the other three
+ *   x_scale [rows], w_scale [outer] float32: EEC_E4M3 only, and required there
+ *   y       [rows][outer] out_dtype
+ *   preact  [rows][outer] z in out_dtype, or NULL (what the backward reads)
+ *   workspace >= eec_linear_workspace_bytes(rows, outer, inner, dtype); may be
+ *   NULL where that is 0
+ * float32 operands keep float32's accuracy on the bf16 matrix cores: each is
+ * the sum of three bf16 parts (exact above 2^-109, to within 2^-133 below), and
+ * the six part products down to 2^-16 of the largest are taken.  e4m3 products
+ * with a 16-bit output are summed by the 8-bit matrix instructions, whose sums
+ * are good to about 1e-5 of sum |x||w|; with a float32 output, in float32. */
+EEC_API eec_status eec_linear(void *stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                      int32_t out_dtype, const void *x, int64_t ldx, const float *x_scale, const void *w,
+                      int64_t ldw, const float *w_scale, const void *bias, const void *residual, int64_t ldr,
+                      int32_t act, void *y, void *preact, void *workspace, size_t workspace_bytes);
+EEC_API size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
+
+/* eec_linear_backward -- with gz = gy act'(preact), rounded once to dtype for
+ * the products (EEC_ACT_NONE: gz = gy):
+ *   gx [rows][inner] = gz w,  gw [outer][inner] = gz^T x,  gbias [outer] = sum_rows gz
+ * (dtype each, any may be NULL; the gradient of residual is gy itself).
+ *   dtype   EEC_F32, EEC_F16 or EEC_BF16
+ *   preact  [rows][outer] as the forward wrote it; may be NULL with EEC_ACT_NONE
+ *   workspace >= eec_linear_backward_workspace_bytes(rows, outer, inner, dtype, act) */
+EEC_API eec_status eec_linear_backward(void *stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                               int32_t act, const void *gy, int64_t ldgy, const void *x, int64_t ldx,
+                               const void *w, int64_t ldw, const void *preact, void *gx, void *gw,
+                               void *gbias, void *workspace, size_t workspace_bytes);
+EEC_API size_t eec_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                                           int32_t act);
+
 /* Thread-local text of the last error on this thread ("" if none). */
 EEC_API const char *eec_last_error(void);
 
