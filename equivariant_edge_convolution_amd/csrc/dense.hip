@@ -205,6 +205,18 @@ struct Product {
 
 constexpr int GBM = 128, GBN = 128, GBK = 32;
 
+// Tile of a workgroup.  Workgroups go to the 8 XCDs in turn, each with an L2 of
+// its own: an XCD takes a contiguous share of the tiles, in strips of 8 tiles of m
+// that run along n, so that what its CUs hold at one time reuses few rows of A and B.
+__device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
+  const uint32_t total = (uint32_t)(tiles_m * tiles_n), b = blockIdx.x, xcd = b & 7;
+  const uint32_t t = xcd * (total >> 3) + min(xcd, total & 7) + (b >> 3);
+  const uint32_t strip = t / (8 * (uint32_t)tiles_n), first = strip * 8;
+  const uint32_t high = min(8u, (uint32_t)tiles_m - first), in = t - first * (uint32_t)tiles_n;
+  tm = first + in % high;
+  tn = in / high;
+}
+
 // A tile of 128 lines x 32 k of one operand, two 8-element chunks per thread.
 // KC: k runs along memory (a chunk is one run), otherwise the lines do (a chunk
 // is 8 runs of 2 lines).
@@ -273,8 +285,10 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   __shared__ __attribute__((aligned(16))) char lds[P * (SA::PLANE + SB::PLANE)];
   char* lds_b = lds + P * SA::PLANE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t tiles_n = (g.N + GBN - 1) / GBN;
-  const int64_t m0 = blockIdx.x / tiles_n * GBM, n0 = blockIdx.x % tiles_n * GBN;
+  int64_t m0, n0;
+  tile_of((g.M + GBM - 1) / GBM, (g.N + GBN - 1) / GBN, m0, n0);
+  m0 *= GBM;
+  n0 *= GBN;
   const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
   f32x4 acc[4][4][M_::ACCS] = {};
@@ -325,6 +339,207 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   }
 }
 
+// ------------------------------------------------------------------ tiled product (16- and 8-bit, aligned)
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// One operand's LDS tile, filled by direct loads of 16 bytes a lane (no
+// registers, so the next tile's loads run under the present one's products).
+// A direct load writes its 64 lanes' data one after another, so what is
+// permuted against bank conflicts is the address each lane loads from:
+//   KC  (k along memory): LINES rows of 128 bytes, the 16-byte chunk c of row r
+//       at slot c ^ (r & 7);  fragments by ds_read_b128;
+//   else (lines along memory, 16-bit): 64 rows (k) of LINES elements, the 32-byte
+//       chunk c of row k at c ^ f(k), f = (k & 3) | (k >> 1 & 4);  fragments by the
+//       transposing read, 16 rows of 32 bytes each spread over all banks.
+template <typename T, bool KC, bool IS_B, int LINES, int WAVES>
+struct Tile {
+  static constexpr int BK = 128 / (int)sizeof(T);       // k of a tile
+  static constexpr int BYTES = LINES * 128;
+  static constexpr int LOADS = BYTES / 1024 / WAVES;    // direct loads of one wave
+  static constexpr int PER_ROW = LINES * (int)sizeof(T) / 16;  // chunks of a k row (not KC)
+  static constexpr uint32_t NOWHERE = 0x80000000u;      // past every buffer: reads as zero
+  const char* base;  // of the next tile, uniform
+  int64_t step;      // bytes from tile to tile
+  uint32_t off[LOADS];
+  int at_k[LOADS];   // first k of this lane's chunk within a tile
+
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    base = (const char*)p + (KC ? (line0 * ld + k0) : (k0 * ld + line0)) * (int64_t)sizeof(T);
+    step = (KC ? (int64_t)BK : (int64_t)BK * ld) * (int64_t)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int slot = (wave * LOADS + i) * 64 + lane;
+      if constexpr (KC) {
+        const int r = slot >> 3, c = (slot & 7) ^ (r & 7);
+        // the LDS rows of B are its columns in the order a lane keeps them (column_at)
+        const int64_t line = min((int64_t)(IS_B ? (r & ~63) + column_at(r & 63) : r), lines - 1 - line0);
+        off[i] = (uint32_t)(line * ld * (int64_t)sizeof(T)) + c * 16;
+        at_k[i] = c * (16 / (int)sizeof(T));
+      } else {
+        const int k = slot / PER_ROW, f = ((k & 3) | (k >> 1 & 4)) << 1, c = (slot % PER_ROW) ^ f;
+        at_k[i] = k;
+        off[i] = line0 + c * 8 < lines ? (uint32_t)(k * ld * (int64_t)sizeof(T)) + c * 16 : NOWHERE;
+      }
+    }
+  }
+  // Loads the next tile, of which `left` k exist.
+  __device__ __forceinline__ void load(char* lds, int64_t left) {
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)0x7fffffff, 0x00020000);
+    char* to = lds + (threadIdx.x >> 6) * LOADS * 1024;
+    if (left < BK) {  // the last tile, perhaps: what lies past the end reads as zero from here on
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) off[i] = at_k[i] < left ? off[i] : NOWHERE;
+    }
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(to + i * 1024), 16,
+                                               off[i], 0, 0, 0);
+    base += step;
+  }
+  // 8-bit fragment of 16 lines and the tile's 128 k: a lane's 32 k are two of its
+  // 16-byte chunks; which ones is free as long as both operands agree.
+  static __device__ __forceinline__ i32x8 fragment128(const char* lds, int line) {
+    const int lane = threadIdx.x & 63, r = line + (lane & 15);
+    i32x8 f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      __builtin_memcpy((char*)&f + 16 * h,
+                       __builtin_assume_aligned(lds + r * 128 + (((h * 4 + (lane >> 4)) ^ (r & 7)) * 16), 16), 16);
+    return f;
+  }
+  // Fragment of the 16 lines from `line` (a multiple of 16), step kk of 64 bytes of k.
+  template <typename F>
+  static __device__ __forceinline__ void fragment(F& f, const char* lds, int line, int kk) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (KC) {
+      const int r = line + (lane & 15), c = kk * 4 + (lane >> 4);
+      __builtin_memcpy(&f, __builtin_assume_aligned(lds + r * 128 + ((c ^ (r & 7)) * 16), 16), 16);
+    } else {
+      // rows k, k + 4 (4 of them per 16 lanes), 8 bytes of 4 lines a lane
+      const int k = kk * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      s16x4 h[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = k + 4 * i, sw = ((row & 3) | (row >> 1 & 4));
+        const int chunk = (line >> 4) ^ sw;
+        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(lds + row * (LINES * 2) + chunk * 32 + (lane & 3) * 8));
+      }
+      __builtin_memcpy(&f, h, 16);
+    }
+  }
+};
+
+// One tile's products: MI * 16 x 64 of C per wave.
+template <typename T, typename TA, typename TB, int MI>
+__device__ __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn, f32x4 (&acc)[MI][4]) {
+  if constexpr (sizeof(T) == 1) {
+    i32x8 fb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fb[j] = TB::fragment128(lb, wn + 16 * j);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const i32x8 fa = TA::fragment128(la, wm + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0,
+                                                                     0x7f7f7f7f);
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      typename Mat<T>::Frag fb[4][1], fa[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) TB::fragment(fb[j][0], lb, wn + 16 * j, kk);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        TA::fragment(fa[0], la, wm + 16 * i, kk);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4 c[1] = {acc[i][j]};
+          Mat<T>::mul(fb[j], fa, c);
+          acc[i][j] = c[0];
+        }
+      }
+    }
+  }
+}
+
+// BM x BN of C per workgroup of WM x WN waves, MI * 16 x 64 of it per wave; two
+// LDS buffers.  Needs 16-byte aligned rows and lengths (see tiled_ok).
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
+__global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
+  constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
+  using TA = Tile<T, A_KC, false, BM, WAVES>;
+  using TB = Tile<T, B_KC, true, BN, WAVES>;
+  constexpr int BK = TA::BK;
+  // Two LDS buffers as variables of their own: the compiler then sees that the
+  // direct loads into one do not touch the other, and does not wait for them
+  // before it reads.
+  __shared__ __attribute__((aligned(1024))) char a0[TA::BYTES], a1[TA::BYTES], b0[TB::BYTES], b1[TB::BYTES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t m0, n0;
+  tile_of((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, m0, n0);
+  m0 *= BM;
+  n0 *= BN;
+  const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
+  const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
+  f32x4 acc[MI][4] = {};
+  TA ta;
+  TB tb;
+  ta.init(g.a, g.lda, m0, g.M, kb);
+  tb.init(g.b, g.ldb, n0, g.N, kb);
+  ta.load(a0, ke - kb);
+  tb.load(b0, ke - kb);
+  __syncthreads();
+  int64_t k = kb;
+  for (; k + BK < ke; k += 2 * BK) {  // two tiles
+    ta.load(a1, ke - k - BK);
+    tb.load(b1, ke - k - BK);
+    multiply<T, TA, TB, MI>(a0, b0, wm, wn, acc);
+    __syncthreads();
+    if (k + 2 * BK < ke) {
+      ta.load(a0, ke - k - 2 * BK);
+      tb.load(b0, ke - k - 2 * BK);
+    }
+    multiply<T, TA, TB, MI>(a1, b1, wm, wn, acc);
+    __syncthreads();
+  }
+  if (k < ke) multiply<T, TA, TB, MI>(a0, b0, wm, wn, acc);  // an odd last one
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = m0 + wm + 16 * i + (lane & 15);
+    if constexpr (B_KC) {
+      const int64_t n = n0 + wn + (lane >> 4) * 16;
+      float v[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) v[c] = acc[i][c >> 2][c & 3];
+      if (e.part) {
+        if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
+      } else {
+        finish_run<O>(e, m, n, v);
+      }
+    } else {  // columns in memory order: 4 adjacent ones a lane
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = n0 + wn + 16 * j + (lane >> 4) * 4;
+        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if (e.part) {
+          if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
+        } else {
+          finish_run<O>(e, m, n, v);
+        }
+      }
+    }
+  }
+#endif
+}
+
 // ------------------------------------------------------------------ gradient of the activation
 
 struct ActGrad {
@@ -373,33 +588,62 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
 
 // ------------------------------------------------------------------ plans
 
-// Splits of k for a product of few tiles: enough workgroups to fill the chip's
-// 256 CUs about twice, while each split keeps at least 8 steps of k.
-int64_t product_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ((M + GBM - 1) / GBM) * ((N + GBN - 1) / GBN);
-  const int64_t most = std::max<int64_t>(1, K / (8 * GBK));
-  return std::max<int64_t>(1, std::min<int64_t>(most, 512 / std::max<int64_t>(1, tiles)));
+enum Kind { GENERAL, TILE128, TILE256 };
+struct Plan {
+  Kind kind;
+  int64_t tiles, splits, k_split;
+};
+
+int64_t tiles_of(int64_t M, int64_t N, int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
+
+// How a product is run: a rule on its sizes and on whether its operands take the
+// tiled kernel.  k is split where the tiles alone leave most of the 256 CUs idle,
+// into at least 512 k each.
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled) {
+  Plan p{};
+  const int64_t t256 = tiles_of(M, N, 256);
+  p.kind = !tiled ? GENERAL : t256 >= 192 ? TILE256 : TILE128;
+  p.tiles = p.kind == TILE256 ? t256 : tiles_of(M, N, 128);
+  const int64_t step = 128;  // k of a split is a multiple of every kernel's tile
+  int64_t s = std::min<int64_t>((p.kind == TILE256 ? 256 : 512) / std::max<int64_t>(1, p.tiles), K / 512);
+  s = std::max<int64_t>(1, s);
+  p.k_split = std::max<int64_t>(step, ((K + s - 1) / s + step - 1) / step * step);
+  p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);
+  return p;
 }
 size_t product_workspace(int64_t M, int64_t N, int64_t K) {
-  const int64_t s = product_splits(M, N, K);
+  const int64_t s = std::max(plan_product(M, N, K, false).splits, plan_product(M, N, K, true).splits);
   return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
+}
+
+// Whether an operand of `size`-byte elements goes into LDS by 16-byte direct
+// loads: aligned rows, a whole number of 16-byte chunks along memory, and lanes'
+// offsets within a tile (256 lines or 64 k) that fit 31 bits.
+bool tiled_operand(const void* p, int64_t ld, int64_t along, int size) {
+  return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && along * size % 16 == 0 && ld * size < (1 << 22);
 }
 
 template <typename T, typename O, bool A_KC, bool B_KC>
 void product(hipStream_t st, Product g, Epilogue e, float* ws) {
   if (g.M == 0 || g.N == 0) return;
-  const int64_t tiles = ((g.M + GBM - 1) / GBM) * ((g.N + GBN - 1) / GBN);
-  int64_t splits = product_splits(g.M, g.N, g.K);
-  g.k_split = (g.K + splits - 1) / splits;
-  g.k_split = std::max<int64_t>(GBK, (g.k_split + GBK - 1) / GBK * GBK);
-  splits = std::max<int64_t>(1, (g.K + g.k_split - 1) / g.k_split);
+  bool tiled = false;
+  if constexpr (!std::is_same<T, float>::value && !std::is_same<T, e4m3_wide>::value)
+    tiled = tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
+            tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
+  const Plan p = plan_product(g.M, g.N, g.K, tiled);
+  g.k_split = p.k_split;
   e.M = g.M;
   e.N = g.N;
-  e.part = splits > 1 ? ws : nullptr;
-  k_product<T, O, A_KC, B_KC><<<dim3((unsigned)tiles, (unsigned)splits), 256, 0, st>>>(g, e);
-  if (splits > 1) {
+  e.part = p.splits > 1 ? ws : nullptr;
+  const dim3 grid((unsigned)p.tiles, (unsigned)p.splits);
+  if constexpr (!std::is_same<T, float>::value && !std::is_same<T, e4m3_wide>::value) {
+    if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8><<<grid, 512, 0, st>>>(g, e);
+    if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4><<<grid, 256, 0, st>>>(g, e);
+  }
+  if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC><<<grid, 256, 0, st>>>(g, e);
+  if (p.splits > 1) {
     const int64_t runs = g.M * ((g.N + 3) / 4);
-    k_join_splits<O><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)splits);
+    k_join_splits<O><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)p.splits);
   }
 }
 
