@@ -192,6 +192,10 @@ __device__ __forceinline__ void put_chunk(char* at, int stride, const Raw<T>& r)
 // Column of a 64-column group held at LDS row p: the four 16-row matrix tiles of
 // a wave take the columns so that a lane ends with 16 adjacent ones (see acc).
 __device__ __forceinline__ int column_at(int p) { return ((p >> 2) & 3) * 16 + (p >> 4 & 3) * 4 + (p & 3); }
+// The same for the 32 x 32 tiles of the 8-bit instruction, which leave a lane 32 adjacent ones.
+__device__ __forceinline__ int column_at_8bit(int p) {
+  return (p >> 2 & 1) * 32 + (p >> 5) * 16 + (p >> 3 & 3) * 4 + (p & 3);
+}
 __device__ __forceinline__ int row_of_column(int n) {
   return (n & ~63) | ((n >> 2) & 3) * 16 | ((n >> 4) & 3) * 4 | (n & 3);
 }
@@ -342,20 +346,22 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
 // ------------------------------------------------------------------ tiled product (16- and 8-bit, aligned)
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// One operand's LDS tile, filled by direct loads of 16 bytes a lane (no
-// registers, so the next tile's loads run under the present one's products).
-// A direct load writes its 64 lanes' data one after another, so what is
-// permuted against bank conflicts is the address each lane loads from:
-//   KC  (k along memory): LINES rows of 128 bytes, the 16-byte chunk c of row r
-//       at slot c ^ (r & 7);  fragments by ds_read_b128;
-//   else (lines along memory, 16-bit): 64 rows (k) of LINES elements, the 32-byte
+// One operand's LDS tile of 64 bytes of k, filled by direct loads of 16 bytes a
+// lane (no registers, so later tiles' loads run under the present one's products).
+// A direct load writes its 64 lanes' data one after another, so what is permuted
+// against bank conflicts is the address each lane loads from:
+//   KC  (k along memory): LINES rows of 64 bytes, the 16-byte chunk c of row r at
+//       slot c ^ (r >> 2 & 3);  fragments by ds_read_b128;
+//   else (lines along memory, 16-bit): 32 rows (k) of LINES elements, the 32-byte
 //       chunk c of row k at c ^ f(k), f = (k & 3) | (k >> 1 & 4);  fragments by the
 //       transposing read, 16 rows of 32 bytes each spread over all banks.
+// Neither has a bank conflict by the counter.
 template <typename T, bool KC, bool IS_B, int LINES, int WAVES>
 struct Tile {
-  static constexpr int BK = 128 / (int)sizeof(T);       // k of a tile
-  static constexpr int BYTES = LINES * 128;
+  static constexpr int BK = 64 / (int)sizeof(T);        // k of a tile
+  static constexpr int BYTES = LINES * 64;
   static constexpr int LOADS = BYTES / 1024 / WAVES;    // direct loads of one wave
   static constexpr int PER_ROW = LINES * (int)sizeof(T) / 16;  // chunks of a k row (not KC)
   static constexpr uint32_t NOWHERE = 0x80000000u;      // past every buffer: reads as zero
@@ -372,9 +378,10 @@ struct Tile {
     for (int i = 0; i < LOADS; ++i) {
       const int slot = (wave * LOADS + i) * 64 + lane;
       if constexpr (KC) {
-        const int r = slot >> 3, c = (slot & 7) ^ (r & 7);
-        // the LDS rows of B are its columns in the order a lane keeps them (column_at)
-        const int64_t line = min((int64_t)(IS_B ? (r & ~63) + column_at(r & 63) : r), lines - 1 - line0);
+        const int r = slot >> 2, c = (slot & 3) ^ (r >> 2 & 3);
+        // the LDS rows of B are its columns in the order a lane keeps them
+        const int own = !IS_B ? r : (r & ~63) + (sizeof(T) == 1 ? column_at_8bit(r & 63) : column_at(r & 63));
+        const int64_t line = min((int64_t)own, lines - 1 - line0);
         off[i] = (uint32_t)(line * ld * (int64_t)sizeof(T)) + c * 16;
         at_k[i] = c * (16 / (int)sizeof(T));
       } else {
@@ -384,12 +391,12 @@ struct Tile {
       }
     }
   }
-  // Loads the next tile, of which `left` k exist.
+  // Loads the next tile, of which `left` k exist (none, perhaps).
   __device__ __forceinline__ void load(char* lds, int64_t left) {
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)0x7fffffff, 0x00020000);
     char* to = lds + (threadIdx.x >> 6) * LOADS * 1024;
-    if (left < BK) {  // the last tile, perhaps: what lies past the end reads as zero from here on
+    if (left < BK) {  // the last tile: what lies past the end reads as zero from here on
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) off[i] = at_k[i] < left ? off[i] : NOWHERE;
     }
@@ -399,33 +406,30 @@ struct Tile {
                                                off[i], 0, 0, 0);
     base += step;
   }
-  // 8-bit fragment of 16 lines and the tile's 128 k: a lane's 32 k are two of its
-  // 16-byte chunks; which ones is free as long as both operands agree.
-  static __device__ __forceinline__ i32x8 fragment128(const char* lds, int line) {
-    const int lane = threadIdx.x & 63, r = line + (lane & 15);
-    i32x8 f;
+  // 8-bit: 32 lines from `line`; a lane's 32 k are two of its row's 16-byte
+  // chunks, which two is free as long as both operands agree.
+  static __device__ __forceinline__ void fragment(i32x8& f, const char* lds, int line) {
+    const int lane = threadIdx.x & 63, r = line + (lane & 31);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       __builtin_memcpy((char*)&f + 16 * h,
-                       __builtin_assume_aligned(lds + r * 128 + (((h * 4 + (lane >> 4)) ^ (r & 7)) * 16), 16), 16);
-    return f;
+                       __builtin_assume_aligned(lds + r * 64 + ((((lane >> 5) * 2 + h) ^ (r >> 2 & 3)) * 16), 16), 16);
   }
-  // Fragment of the 16 lines from `line` (a multiple of 16), step kk of 64 bytes of k.
+  // 16-bit: 16 lines from `line`.
   template <typename F>
-  static __device__ __forceinline__ void fragment(F& f, const char* lds, int line, int kk) {
+  static __device__ __forceinline__ void fragment(F& f, const char* lds, int line) {
     const int lane = threadIdx.x & 63;
     if constexpr (KC) {
-      const int r = line + (lane & 15), c = kk * 4 + (lane >> 4);
-      __builtin_memcpy(&f, __builtin_assume_aligned(lds + r * 128 + ((c ^ (r & 7)) * 16), 16), 16);
+      const int r = line + (lane & 15);
+      __builtin_memcpy(&f, __builtin_assume_aligned(lds + r * 64 + (((lane >> 4) ^ (r >> 2 & 3)) * 16), 16), 16);
     } else {
       // rows k, k + 4 (4 of them per 16 lanes), 8 bytes of 4 lines a lane
-      const int k = kk * 32 + (lane >> 4) * 8 + ((lane & 15) >> 2);
+      const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       s16x4 h[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = k + 4 * i, sw = ((row & 3) | (row >> 1 & 4));
-        const int chunk = (line >> 4) ^ sw;
+        const int row = k + 4 * i, chunk = (line >> 4) ^ ((row & 3) | (row >> 1 & 4));
         h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(lds + row * (LINES * 2) + chunk * 32 + (lane & 3) * 8));
       }
@@ -434,54 +438,75 @@ struct Tile {
   }
 };
 
-// One tile's products: MI * 16 x 64 of C per wave.
-template <typename T, typename TA, typename TB, int MI>
-__device__ __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn, f32x4 (&acc)[MI][4]) {
-  if constexpr (sizeof(T) == 1) {
-    i32x8 fb[4];
+// A wave's share of C, MI * 16 rows x 64 columns, and a tile's products into it.
+template <typename T, int MI>
+struct Share {
+  static constexpr int ROWS = 16, GROUPS = MI, RUN = 16;  // rows of a matrix tile, tiles, adjacent columns of a lane
+  f32x4 acc[MI][4] = {};
+  template <typename TA, typename TB>
+  __device__ __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn) {
+    typename Mat<T>::Frag fb[4][1], fa[1];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fb[j] = TB::fragment128(lb, wn + 16 * j);
+    for (int j = 0; j < 4; ++j) TB::fragment(fb[j][0], lb, wn + 16 * j);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const i32x8 fa = TA::fragment128(la, wm + 16 * i);
+      TA::fragment(fa[0], la, wm + 16 * i);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0,
-                                                                     0x7f7f7f7f);
-    }
-  } else {
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      typename Mat<T>::Frag fb[4][1], fa[1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) TB::fragment(fb[j][0], lb, wn + 16 * j, kk);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        TA::fragment(fa[0], la, wm + 16 * i, kk);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f32x4 c[1] = {acc[i][j]};
-          Mat<T>::mul(fb[j], fa, c);
-          acc[i][j] = c[0];
-        }
+      for (int j = 0; j < 4; ++j) {
+        f32x4 c[1] = {acc[i][j]};
+        Mat<T>::mul(fb[j], fa, c);
+        acc[i][j] = c[0];
       }
     }
   }
+  __device__ __forceinline__ float at(int i, int c) const { return acc[i][c >> 2][c & 3]; }
+};
+template <int MI>
+struct Share<e4m3, MI> {
+  static constexpr int ROWS = 32, GROUPS = MI / 2, RUN = 32;
+  f32x16 acc[MI / 2][2] = {};
+  template <typename TA, typename TB>
+  __device__ __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn) {
+    i32x8 fb[2], fa;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) TB::fragment(fb[j], lb, wn + 32 * j);
+#pragma unroll
+    for (int i = 0; i < MI / 2; ++i) {
+      TA::fragment(fa, la, wm + 32 * i);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)  // block scales of 2^0
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0,
+                                                                    0x7f7f7f7f);
+    }
+  }
+  __device__ __forceinline__ float at(int i, int c) const { return acc[i][c >> 4][c & 15]; }
+};
+
+// Waits until at most N of this wave's loads are on their way and its LDS reads
+// are done, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | 0 << 8 | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-// BM x BN of C per workgroup of WM x WN waves, MI * 16 x 64 of it per wave; two
-// LDS buffers.  Needs 16-byte aligned rows and lengths (see tiled_ok).
+// BM x BN of C per workgroup of WM x WN waves, MI * 16 x 64 of it per wave.  Four
+// LDS buffers: while a tile is multiplied the next two are on their way and a
+// third is started, into the buffer that everybody left at the barrier before.
+// Needs 16-byte aligned rows and lengths (see tiled_operand).
 template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
   using TA = Tile<T, A_KC, false, BM, WAVES>;
   using TB = Tile<T, B_KC, true, BN, WAVES>;
-  constexpr int BK = TA::BK;
-  // Two LDS buffers as variables of their own: the compiler then sees that the
-  // direct loads into one do not touch the other, and does not wait for them
-  // before it reads.
-  __shared__ __attribute__((aligned(1024))) char a0[TA::BYTES], a1[TA::BYTES], b0[TB::BYTES], b1[TB::BYTES];
+  constexpr int BK = TA::BK, LOADS = TA::LOADS + TB::LOADS;
+  // The buffers are variables of their own: the compiler then sees that loads into
+  // one do not touch the others, and does not wait for them before it reads.
+  __shared__ __attribute__((aligned(1024))) char a0[TA::BYTES], a1[TA::BYTES], a2[TA::BYTES], a3[TA::BYTES];
+  __shared__ __attribute__((aligned(1024))) char b0[TB::BYTES], b1[TB::BYTES], b2[TB::BYTES], b3[TB::BYTES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t m0, n0;
   tile_of((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, m0, n0);
@@ -489,36 +514,45 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   n0 *= BN;
   const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
-  f32x4 acc[MI][4] = {};
+  Share<T, MI> c;
   TA ta;
   TB tb;
   ta.init(g.a, g.lda, m0, g.M, kb);
   tb.init(g.b, g.ldb, n0, g.N, kb);
   ta.load(a0, ke - kb);
   tb.load(b0, ke - kb);
-  __syncthreads();
-  int64_t k = kb;
-  for (; k + BK < ke; k += 2 * BK) {  // two tiles
-    ta.load(a1, ke - k - BK);
-    tb.load(b1, ke - k - BK);
-    multiply<T, TA, TB, MI>(a0, b0, wm, wn, acc);
-    __syncthreads();
-    if (k + 2 * BK < ke) {
-      ta.load(a0, ke - k - 2 * BK);
-      tb.load(b0, ke - k - 2 * BK);
-    }
-    multiply<T, TA, TB, MI>(a1, b1, wm, wn, acc);
-    __syncthreads();
+  ta.load(a1, ke - kb - BK);
+  tb.load(b1, ke - kb - BK);
+  ta.load(a2, ke - kb - 2 * BK);
+  tb.load(b2, ke - kb - 2 * BK);
+  for (int64_t k = kb; k < ke; k += 4 * BK) {  // four tiles; those past the end are zeros, read from nowhere
+    tile_barrier<2 * LOADS>();
+    ta.load(a3, ke - k - 3 * BK);
+    tb.load(b3, ke - k - 3 * BK);
+    c.template multiply<TA, TB>(a0, b0, wm, wn);
+    tile_barrier<2 * LOADS>();
+    ta.load(a0, ke - k - 4 * BK);
+    tb.load(b0, ke - k - 4 * BK);
+    c.template multiply<TA, TB>(a1, b1, wm, wn);
+    tile_barrier<2 * LOADS>();
+    ta.load(a1, ke - k - 5 * BK);
+    tb.load(b1, ke - k - 5 * BK);
+    c.template multiply<TA, TB>(a2, b2, wm, wn);
+    tile_barrier<2 * LOADS>();
+    ta.load(a2, ke - k - 6 * BK);
+    tb.load(b2, ke - k - 6 * BK);
+    c.template multiply<TA, TB>(a3, b3, wm, wn);
   }
-  if (k < ke) multiply<T, TA, TB, MI>(a0, b0, wm, wn, acc);  // an odd last one
+  using S = Share<T, MI>;
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + wm + 16 * i + (lane & 15);
+  for (int i = 0; i < S::GROUPS; ++i) {
+    const int64_t m = m0 + wm + S::ROWS * i + (lane % S::ROWS);
     if constexpr (B_KC) {
-      const int64_t n = n0 + wn + (lane >> 4) * 16;
-      float v[16];
+      constexpr int L = S::RUN;
+      const int64_t n = n0 + wn + (lane / S::ROWS) * L;
+      float v[L];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) v[c] = acc[i][c >> 2][c & 3];
+      for (int j = 0; j < L; ++j) v[j] = c.at(i, j);
       if (e.part) {
         if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
       } else {
@@ -528,7 +562,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t n = n0 + wn + 16 * j + (lane >> 4) * 4;
-        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        float v[4] = {c.at(i, 4 * j), c.at(i, 4 * j + 1), c.at(i, 4 * j + 2), c.at(i, 4 * j + 3)};
         if (e.part) {
           if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
         } else {
@@ -538,6 +572,106 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
     }
   }
 #endif
+}
+
+// ------------------------------------------------------------------ few rows
+
+// Up to 16 MT rows of x against 16 columns (rows of w) per workgroup: w goes from
+// memory straight into the first factor of the matrix instruction, once, x (a few
+// rows, in the L2) into the second.  The 8 waves deal runs of 128 bytes of k in
+// turn and are joined in LDS, in wave order, so one launch does it all.
+template <typename T, typename O, int MT>
+__global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
+  using M_ = Mat<T>;
+  constexpr int WAVES = 8, P = M_::PLANES;
+  constexpr int CHUNK = sizeof(T) == 4 ? 32 : sizeof(T) == 2 ? 64 : 128;  // k of one run
+  constexpr int STEPS = CHUNK / 32;                                      // matrix steps of one run
+  constexpr int TOGETHER = MT == 1 ? 4 : 2;                              // runs in flight
+  __shared__ f32x4 join[WAVES][MT][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const T* w = (const T*)g.b + min(n0 + (lane & 15), g.N - 1) * g.ldb;
+  const T* x[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) x[t] = (const T*)g.a + min((int64_t)(t * 16 + (lane & 15)), g.M - 1) * g.lda;
+  f32x4 acc[MT][M_::ACCS] = {};
+  // A run of CHUNK k: lane group q holds STEPS * 8 adjacent ones, of which step s
+  // multiplies the s-th 8 (the same k of both operands meet, which is all a sum asks).
+  struct Run {
+    Raw<T> v[STEPS];
+  };
+  auto parts = [](const Raw<T>& r, typename M_::Frag (&f)[P]) {
+    if constexpr (P == 3) {
+      bf16 h[3][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split3(r.v[i], h[0][i], h[1][i], h[2][i]);
+      __builtin_memcpy(f, h, sizeof(h));
+    } else {
+      put_chunk<T>((char*)f, 0, r);
+    }
+  };
+  auto product = [&](const Run& wr, const Run (&xr)[MT]) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      typename M_::Frag fw[P], fx[P];
+      parts(wr.v[s], fw);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        parts(xr[t].v[s], fx);
+        M_::mul(fw, fx, acc[t]);
+      }
+    }
+  };
+  const int64_t full = g.K / CHUNK;
+  const int own = q * STEPS * 8;
+  int64_t c = wave;
+  for (; c + WAVES * (TOGETHER - 1) < full; c += WAVES * TOGETHER) {
+    Run wr[TOGETHER], xr[TOGETHER][MT];
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) {
+      const int64_t k = (c + WAVES * i) * CHUNK + own;
+      __builtin_memcpy(&wr[i], w + k, sizeof(Run));
+#pragma unroll
+      for (int t = 0; t < MT; ++t) __builtin_memcpy(&xr[i][t], x[t] + k, sizeof(Run));
+    }
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) product(wr[i], xr[i]);
+  }
+  for (; c * CHUNK < g.K; c += WAVES) {
+    Run wr, xr[MT];
+    const int64_t k = c * CHUNK + own, left = g.K - k;
+    if (c < full) {
+      __builtin_memcpy(&wr, w + k, sizeof(Run));
+#pragma unroll
+      for (int t = 0; t < MT; ++t) __builtin_memcpy(&xr[t], x[t] + k, sizeof(Run));
+    } else {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool is = s * 8 + i < left;
+          wr.v[s].v[i] = is ? w[k + s * 8 + i] : T{};
+#pragma unroll
+          for (int t = 0; t < MT; ++t) xr[t].v[s].v[i] = is ? x[t][k + s * 8 + i] : T{};
+        }
+    }
+    product(wr, xr);
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = M_::total(acc[t], i);
+    join[wave][t][lane] = v;
+  }
+  __syncthreads();
+  if (wave < MT) {
+    f32x4 v = join[0][wave][lane];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) v += join[i][wave][lane];
+    float r[4] = {v[0], v[1], v[2], v[3]};
+    finish_run<O>(e, wave * 16 + (lane & 15), n0 + q * 4, r);
+  }
 }
 
 // ------------------------------------------------------------------ gradient of the activation
@@ -588,7 +722,7 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
 
 // ------------------------------------------------------------------ plans
 
-enum Kind { GENERAL, TILE128, TILE256 };
+enum Kind { GENERAL, TILE128, TILE256, FEW };
 struct Plan {
   Kind kind;
   int64_t tiles, splits, k_split;
@@ -596,11 +730,21 @@ struct Plan {
 
 int64_t tiles_of(int64_t M, int64_t N, int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
 
+// Rows up to which the forward product reads w straight into the matrix
+// instructions (4096 x 4096 bf16: 14 us at 32 rows, where tiles take 17 us; 21 us
+// at 64, where they take 18 us).
+constexpr int64_t FEW_ROWS = 32;
+
 // How a product is run: a rule on its sizes and on whether its operands take the
 // tiled kernel.  k is split where the tiles alone leave most of the 256 CUs idle,
 // into at least 512 k each.
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled) {
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool forward) {
   Plan p{};
+  if (forward && M <= FEW_ROWS) {
+    p.kind = FEW;
+    p.splits = 1;
+    return p;
+  }
   const int64_t t256 = tiles_of(M, N, 256);
   p.kind = !tiled ? GENERAL : t256 >= 192 ? TILE256 : TILE128;
   p.tiles = p.kind == TILE256 ? t256 : tiles_of(M, N, 128);
@@ -611,8 +755,8 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled) {
   p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);
   return p;
 }
-size_t product_workspace(int64_t M, int64_t N, int64_t K) {
-  const int64_t s = std::max(plan_product(M, N, K, false).splits, plan_product(M, N, K, true).splits);
+size_t product_workspace(int64_t M, int64_t N, int64_t K, bool forward) {
+  const int64_t s = std::max(plan_product(M, N, K, false, forward).splits, plan_product(M, N, K, true, forward).splits);
   return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
 }
 
@@ -630,7 +774,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws) {
   if constexpr (!std::is_same<T, float>::value && !std::is_same<T, e4m3_wide>::value)
     tiled = tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
             tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
-  const Plan p = plan_product(g.M, g.N, g.K, tiled);
+  const Plan p = plan_product(g.M, g.N, g.K, tiled, A_KC && B_KC);
   g.k_split = p.k_split;
   e.M = g.M;
   e.N = g.N;
@@ -639,6 +783,11 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws) {
   if constexpr (!std::is_same<T, float>::value && !std::is_same<T, e4m3_wide>::value) {
     if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8><<<grid, 512, 0, st>>>(g, e);
     if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4><<<grid, 256, 0, st>>>(g, e);
+  }
+  if constexpr (A_KC && B_KC) {
+    const dim3 columns((unsigned)((g.N + 15) / 16));
+    if (p.kind == FEW && g.M <= 16) k_few<T, O, 1><<<columns, 512, 0, st>>>(g, e);
+    if (p.kind == FEW && g.M > 16) k_few<T, O, 2><<<columns, 512, 0, st>>>(g, e);
   }
   if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC><<<grid, 256, 0, st>>>(g, e);
   if (p.splits > 1) {
@@ -671,7 +820,7 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_part = at;
   at += align256(4 * (size_t)act_grad_strips(rows, outer, dtype) * (size_t)outer);
   p.off_split = at;
-  at += std::max(product_workspace(rows, inner, outer), product_workspace(outer, inner, rows));
+  at += std::max(product_workspace(rows, inner, outer, false), product_workspace(outer, inner, rows, false));
   p.bytes = at;
   return p;
 }
@@ -679,7 +828,7 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
 }  // namespace
 
 size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype) {
-  return product_workspace(rows, outer, inner);
+  return product_workspace(rows, outer, inner, true);
 }
 
 void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) {
