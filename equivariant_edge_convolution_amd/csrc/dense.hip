@@ -345,142 +345,194 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
 
 // ------------------------------------------------------------------ tiled product (16- and 8-bit, aligned)
 
+// The wave's number in its workgroup, in a scalar register.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // One operand's LDS tile of 64 bytes of k, filled by direct loads of 16 bytes a
 // lane (no registers, so later tiles' loads run under the present one's products).
-// A direct load writes its 64 lanes' data one after another, so what is permuted
-// against bank conflicts is the address each lane loads from:
+// A direct load writes its 64 lanes' data one after another, 1024 bytes; against
+// bank conflicts the address each lane loads from is permuted within them:
 //   KC  (k along memory): LINES rows of 64 bytes, the 16-byte chunk c of row r at
 //       slot c ^ (r >> 2 & 3);  fragments by ds_read_b128;
-//   else (lines along memory, 16-bit): 32 rows (k) of LINES elements, the 32-byte
-//       chunk c of row k at c ^ f(k), f = (k & 3) | (k >> 1 & 4);  fragments by the
-//       transposing read, 16 rows of 32 bytes each spread over all banks.
+//   else (lines along memory, 16-bit): 32 rows (k) of LINES elements, PER_LOAD of
+//       them a load, the 32-byte chunk c of row k at c ^ (k % PER_LOAD), and PAD
+//       bytes after each load's 1024; the loads in an order (block_of) in which the
+//       8 rows x 32 bytes that half a wave reads at once fill the 256 bytes of all
+//       banks.  Only the low bits of a chunk's place depend on the lane, so a few
+//       address registers serve all fragments.
 // Neither has a bank conflict by the counter.
 template <typename T, bool KC, bool IS_B, int LINES, int WAVES>
 struct Tile {
-  static constexpr int BK = 64 / (int)sizeof(T);        // k of a tile
-  static constexpr int BYTES = LINES * 64;
-  static constexpr int LOADS = BYTES / 1024 / WAVES;    // direct loads of one wave
-  static constexpr int PER_ROW = LINES * (int)sizeof(T) / 16;  // chunks of a k row (not KC)
-  static constexpr uint32_t NOWHERE = 0x80000000u;      // past every buffer: reads as zero
+  static constexpr int BK = 64 / (int)sizeof(T);          // k of a tile
+  static constexpr int LOADS = LINES / 16 / WAVES;        // direct loads of one wave
+  static constexpr int PER_LOAD = 512 / LINES;            // k rows of one load (not KC)
+  static constexpr int CHUNKS = 64 / PER_LOAD;            // 16-byte chunks of a k row (not KC)
+  static constexpr int PAD = KC ? 0 : 16384 / LINES, STRIDE = 1024 + PAD;
+  static constexpr int BYTES = LINES / 16 * STRIDE;
+  static constexpr int READS = KC && sizeof(T) == 2 ? 1 : 2;  // LDS reads of one fragment
+  static constexpr uint32_t NOWHERE = 0x80000000u;        // past every buffer: reads as zero
   const char* base;  // of the next tile, uniform
   int64_t step;      // bytes from tile to tile
   uint32_t off[LOADS];
-  int at_k[LOADS];   // first k of this lane's chunk within a tile
 
+  // Load i of this wave: its place among the tile's loads.
+  static __device__ __forceinline__ int place(int i) { return wave_id() * LOADS + i; }
+  // First k of this lane's chunk of load i within a tile.
+  static __device__ __forceinline__ int at_k(int i) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (KC)
+      return ((lane & 3) ^ (lane >> 4 & 3)) * (16 / (int)sizeof(T));
+    else
+      return block_of(place(i)) * PER_LOAD + lane / CHUNKS;
+  }
+  // The k rows of load u are PER_LOAD from PER_LOAD * block_of(u), and the other way
+  // round: bit 3 of k next to the lowest one, bit 2 (which tells a fragment's first
+  // read from its second) above it.
+  static __device__ __forceinline__ int block_of(int u) {
+    return PER_LOAD == 2 ? (u & 9) | (u & 2) << 1 | (u >> 1 & 2) : (u & 4) | (u & 1) << 1 | (u >> 1 & 1);
+  }
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     base = (const char*)p + (KC ? (line0 * ld + k0) : (k0 * ld + line0)) * (int64_t)sizeof(T);
     step = (KC ? (int64_t)BK : (int64_t)BK * ld) * (int64_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-      const int slot = (wave * LOADS + i) * 64 + lane;
       if constexpr (KC) {
-        const int r = slot >> 2, c = (slot & 3) ^ (r >> 2 & 3);
+        const int r = place(i) * 16 + (lane >> 2), c = (lane & 3) ^ (r >> 2 & 3);
         // the LDS rows of B are its columns in the order a lane keeps them
         const int own = !IS_B ? r : (r & ~63) + (sizeof(T) == 1 ? column_at_8bit(r & 63) : column_at(r & 63));
         const int64_t line = min((int64_t)own, lines - 1 - line0);
         off[i] = (uint32_t)(line * ld * (int64_t)sizeof(T)) + c * 16;
-        at_k[i] = c * (16 / (int)sizeof(T));
       } else {
-        const int k = slot / PER_ROW, f = ((k & 3) | (k >> 1 & 4)) << 1, c = (slot % PER_ROW) ^ f;
-        at_k[i] = k;
+        const int k = at_k(i), c = (lane % CHUNKS) ^ (k % PER_LOAD * 2);
         off[i] = line0 + c * 8 < lines ? (uint32_t)(k * ld * (int64_t)sizeof(T)) + c * 16 : NOWHERE;
       }
     }
   }
-  // Loads the next tile, of which `left` k exist (none, perhaps).
+  // Loads the next tile; with TAIL only `left` of its k exist (none, perhaps).
+  template <bool TAIL>
   __device__ __forceinline__ void load(char* lds, int64_t left) {
     const __amdgpu_buffer_rsrc_t rsrc =
         __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)0x7fffffff, 0x00020000);
-    char* to = lds + (threadIdx.x >> 6) * LOADS * 1024;
-    if (left < BK) {  // the last tile: what lies past the end reads as zero from here on
+    if constexpr (TAIL) {  // what lies past the end reads as zero from here on
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) off[i] = at_k[i] < left ? off[i] : NOWHERE;
+      for (int i = 0; i < LOADS; ++i) off[i] = at_k(i) < left ? off[i] : NOWHERE;
     }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(to + i * 1024), 16,
-                                               off[i], 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(lds + place(i) * STRIDE), 16, off[i], 0, 0, 0);
     base += step;
   }
-  // 8-bit: 32 lines from `line`; a lane's 32 k are two of its row's 16-byte
-  // chunks, which two is free as long as both operands agree.
-  static __device__ __forceinline__ void fragment(i32x8& f, const char* lds, int line) {
+  // Fragment i of the lines from `line` (a multiple of 64).  Each address is one
+  // addition to the buffer: through a longer chain the compiler loses sight of the
+  // buffer and waits for every direct load before it reads.
+  // 8-bit: 32 lines; a lane's 32 k are two of its row's 16-byte chunks, which two
+  // is free as long as both operands agree.
+  static __device__ __forceinline__ void fragment(i32x8& f, const char* lds, int line, int i) {
     const int lane = threadIdx.x & 63, r = line + (lane & 31);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      __builtin_memcpy((char*)&f + 16 * h,
-                       __builtin_assume_aligned(lds + r * 64 + ((((lane >> 5) * 2 + h) ^ (r >> 2 & 3)) * 16), 16), 16);
+    for (int h = 0; h < 2; ++h) {
+      const int at = r * 64 + (((lane >> 5) * 2 + h) ^ (r >> 2 & 3)) * 16 + i * 2048;
+      __builtin_memcpy((char*)&f + 16 * h, __builtin_assume_aligned(lds + at, 16), 16);
+    }
   }
-  // 16-bit: 16 lines from `line`.
+  // 16-bit: 16 lines.
   template <typename F>
-  static __device__ __forceinline__ void fragment(F& f, const char* lds, int line) {
+  static __device__ __forceinline__ void fragment(F& f, const char* lds, int line, int i) {
     const int lane = threadIdx.x & 63;
     if constexpr (KC) {
-      const int r = line + (lane & 15);
-      __builtin_memcpy(&f, __builtin_assume_aligned(lds + r * 64 + (((lane >> 4) ^ (r >> 2 & 3)) * 16), 16), 16);
+      const int r = line + (lane & 15), at = r * 64 + ((lane >> 4) ^ (r >> 2 & 3)) * 16 + i * 1024;
+      __builtin_memcpy(&f, __builtin_assume_aligned(lds + at, 16), 16);
     } else {
-      // rows k, k + 4 (4 of them per 16 lanes), 8 bytes of 4 lines a lane
-      const int k = (lane >> 4) * 8 + ((lane & 15) >> 2);
+      // rows k and k + 4 (4 of them per 16 lanes), 8 bytes of 4 lines a lane
       typedef short s16x4 __attribute__((ext_vector_type(4)));
+      const int k = (lane >> 4) * 8 + (lane >> 2 & 3), low = k % PER_LOAD;
+      const int at = block_of(k / PER_LOAD) * STRIDE + low * (LINES * 2) + ((i % PER_LOAD) ^ low) * 32 + line * 2 +
+                     (lane & 3) * 8 + i / PER_LOAD * PER_LOAD * 32;
       s16x4 h[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = k + 4 * i, chunk = (line >> 4) ^ ((row & 3) | (row >> 1 & 4));
-        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(lds + row * (LINES * 2) + chunk * 32 + (lane & 3) * 8));
-      }
+      for (int u = 0; u < 2; ++u)
+        h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(lds + (at + u * block_of(4 / PER_LOAD) * STRIDE)));
       __builtin_memcpy(&f, h, 16);
     }
   }
 };
 
 // A wave's share of C, MI * 16 rows x 64 columns, and a tile's products into it.
+// `fb` and the first AHEAD of `fa` are read one tile ahead, under the products of
+// the tile before, so that a tile begins with what it needs in registers.
 template <typename T, int MI>
 struct Share {
   static constexpr int ROWS = 16, GROUPS = MI, RUN = 16;  // rows of a matrix tile, tiles, adjacent columns of a lane
-  f32x4 acc[MI][4] = {};
-  template <typename TA, typename TB>
-  __device__ __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn) {
-    typename Mat<T>::Frag fb[4][1], fa[1];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) TB::fragment(fb[j][0], lb, wn + 16 * j);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      TA::fragment(fa[0], la, wm + 16 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f32x4 c[1] = {acc[i][j]};
-        Mat<T>::mul(fb[j], fa, c);
-        acc[i][j] = c[0];
-      }
-    }
+  static constexpr int NB = 4, AHEAD = 2;
+  using Frag = typename Mat<T>::Frag;
+  f32x4 acc[GROUPS][NB] = {};
+  __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {
+    f32x4 c[1] = {acc[i][j]};
+    const Frag fb[1] = {b}, fa[1] = {a};
+    Mat<T>::mul(fb, fa, c);
+    acc[i][j] = c[0];
   }
   __device__ __forceinline__ float at(int i, int c) const { return acc[i][c >> 2][c & 3]; }
 };
 template <int MI>
 struct Share<e4m3, MI> {
   static constexpr int ROWS = 32, GROUPS = MI / 2, RUN = 32;
-  f32x16 acc[MI / 2][2] = {};
-  template <typename TA, typename TB>
-  __device__ __forceinline__ void multiply(const char* la, const char* lb, int wm, int wn) {
-    i32x8 fb[2], fa;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) TB::fragment(fb[j], lb, wn + 32 * j);
-#pragma unroll
-    for (int i = 0; i < MI / 2; ++i) {
-      TA::fragment(fa, la, wm + 32 * i);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)  // block scales of 2^0
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0,
-                                                                    0x7f7f7f7f);
-    }
+  static constexpr int NB = 2, AHEAD = 1;
+  using Frag = i32x8;
+  f32x16 acc[GROUPS][NB] = {};
+  __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {  // block scales of 2^0
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
   }
   __device__ __forceinline__ float at(int i, int c) const { return acc[i][c >> 4][c & 15]; }
 };
+template <typename S>
+struct Ahead {
+  typename S::Frag b[S::NB], a[S::AHEAD];
+};
+template <typename S, typename TA, typename TB>
+__device__ __forceinline__ void read_ahead(Ahead<S>& f, const char* la, const char* lb, int wm, int wn) {
+#pragma unroll
+  for (int j = 0; j < S::NB; ++j) TB::fragment(f.b[j], lb, wn, j);
+#pragma unroll
+  for (int i = 0; i < S::AHEAD; ++i) TA::fragment(f.a[i], la, wm, i);
+}
+// One tile's products from `f` and `la`, the next tile's `next` from `na` and
+// `nb`.  The scheduling groups spread the tile's direct loads and LDS reads
+// between the products; left alone the compiler gathers each read next to its use.
+template <typename S, typename TA, typename TB>
+__device__ __forceinline__ void multiply(S& c, const Ahead<S>& f, const char* la, int wm, Ahead<S>& next, const char* na,
+                                         const char* nb, int wn) {
+  constexpr int LOADS = TA::LOADS + TB::LOADS;
+  typename S::Frag a[S::GROUPS];
+#pragma unroll
+  for (int i = 0; i < S::GROUPS; ++i) {
+    constexpr int LATE = S::GROUPS - S::NB;  // the last groups read one fragment of B each
+    if (i < S::AHEAD) a[i] = f.a[i];
+    if (i + S::AHEAD < S::GROUPS)
+      TA::fragment(a[i + S::AHEAD], la, wm, i + S::AHEAD);
+    else
+      TA::fragment(next.a[i + S::AHEAD - S::GROUPS], na, wm, i + S::AHEAD - S::GROUPS);
+    if (i >= LATE) TB::fragment(next.b[i - LATE], nb, wn, i - LATE);
+#pragma unroll
+    for (int j = 0; j < S::NB; ++j) c.mul(i, j, f.b[j], a[i]);
+  }
+  constexpr int EACH = (LOADS + S::GROUPS - 1) / S::GROUPS;
+#pragma unroll
+  for (int i = 0; i < S::GROUPS; ++i) {
+    if (i * EACH < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, EACH, 0);  // direct loads
+    if (i < S::GROUPS - S::NB)                                                   // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x100, TA::READS, 0);
+    else
+      __builtin_amdgcn_sched_group_barrier(0x100, TA::READS + TB::READS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, S::NB, 0);  // products
+  }
+}
 
 // Waits until at most N of this wave's loads are on their way and its LDS reads
 // are done, then for the workgroup.
@@ -493,8 +545,9 @@ __device__ __forceinline__ void tile_barrier() {
 }
 
 // BM x BN of C per workgroup of WM x WN waves, MI * 16 x 64 of it per wave.  Four
-// LDS buffers: while a tile is multiplied the next two are on their way and a
-// third is started, into the buffer that everybody left at the barrier before.
+// LDS buffers: at the barrier before a tile the next one is there, to be read ahead
+// from, the one after is on its way, and a third is started into the buffer that
+// everybody left at that barrier.
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
 template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
@@ -507,43 +560,47 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   // one do not touch the others, and does not wait for them before it reads.
   __shared__ __attribute__((aligned(1024))) char a0[TA::BYTES], a1[TA::BYTES], a2[TA::BYTES], a3[TA::BYTES];
   __shared__ __attribute__((aligned(1024))) char b0[TB::BYTES], b1[TB::BYTES], b2[TB::BYTES], b3[TB::BYTES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   int64_t m0, n0;
   tile_of((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, m0, n0);
   m0 *= BM;
   n0 *= BN;
   const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
-  Share<T, MI> c;
+  using S = Share<T, MI>;
+  S c;
+  Ahead<S> f0, f1;
   TA ta;
   TB tb;
   ta.init(g.a, g.lda, m0, g.M, kb);
   tb.init(g.b, g.ldb, n0, g.N, kb);
-  ta.load(a0, ke - kb);
-  tb.load(b0, ke - kb);
-  ta.load(a1, ke - kb - BK);
-  tb.load(b1, ke - kb - BK);
-  ta.load(a2, ke - kb - 2 * BK);
-  tb.load(b2, ke - kb - 2 * BK);
-  for (int64_t k = kb; k < ke; k += 4 * BK) {  // four tiles; those past the end are zeros, read from nowhere
-    tile_barrier<2 * LOADS>();
-    ta.load(a3, ke - k - 3 * BK);
-    tb.load(b3, ke - k - 3 * BK);
-    c.template multiply<TA, TB>(a0, b0, wm, wn);
-    tile_barrier<2 * LOADS>();
-    ta.load(a0, ke - k - 4 * BK);
-    tb.load(b0, ke - k - 4 * BK);
-    c.template multiply<TA, TB>(a1, b1, wm, wn);
-    tile_barrier<2 * LOADS>();
-    ta.load(a1, ke - k - 5 * BK);
-    tb.load(b1, ke - k - 5 * BK);
-    c.template multiply<TA, TB>(a2, b2, wm, wn);
-    tile_barrier<2 * LOADS>();
-    ta.load(a2, ke - k - 6 * BK);
-    tb.load(b2, ke - k - 6 * BK);
-    c.template multiply<TA, TB>(a3, b3, wm, wn);
+  ta.template load<true>(a0, ke - kb);
+  tb.template load<true>(b0, ke - kb);
+  ta.template load<true>(a1, ke - kb - BK);
+  tb.template load<true>(b1, ke - kb - BK);
+  ta.template load<true>(a2, ke - kb - 2 * BK);
+  tb.template load<true>(b2, ke - kb - 2 * BK);
+  tile_barrier<2 * LOADS>();
+  read_ahead<S, TA, TB>(f0, a0, b0, wm, wn);
+  int64_t k = kb;
+#define EEC_TILE(TAIL, T, F, A, NEXT, NA, NB, FREE_A, FREE_B)   \
+  tile_barrier<LOADS>();                                        \
+  ta.template load<TAIL>(FREE_A, ke - k - (T + 3) * BK);        \
+  tb.template load<TAIL>(FREE_B, ke - k - (T + 3) * BK);        \
+  multiply<S, TA, TB>(c, F, A, wm, NEXT, NA, NB, wn)
+#define EEC_FOUR_TILES(TAIL)                       \
+  EEC_TILE(TAIL, 0, f0, a0, f1, a1, b1, a3, b3);   \
+  EEC_TILE(TAIL, 1, f1, a1, f0, a2, b2, a0, b0);   \
+  EEC_TILE(TAIL, 2, f0, a2, f1, a3, b3, a1, b1);   \
+  EEC_TILE(TAIL, 3, f1, a3, f0, a0, b0, a2, b2)
+  for (; k + 7 * BK <= ke; k += 4 * BK) {  // every tile it loads is whole
+    EEC_FOUR_TILES(false);
   }
-  using S = Share<T, MI>;
+  for (; k < ke; k += 4 * BK) {  // tiles past the end are zeros, read from nowhere
+    EEC_FOUR_TILES(true);
+  }
+#undef EEC_FOUR_TILES
+#undef EEC_TILE
 #pragma unroll
   for (int i = 0; i < S::GROUPS; ++i) {
     const int64_t m = m0 + wm + S::ROWS * i + (lane % S::ROWS);
