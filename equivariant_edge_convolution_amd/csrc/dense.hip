@@ -27,34 +27,121 @@ struct Epilogue {
   float* part;  // split sums [split][M][N] instead of all of the above, or NULL
 };
 
-// L consecutive columns of one row, from their sums over k.
+// What L adjacent columns have in common over the rows.
 template <typename O, int L>
-__device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, int64_t n, float (&v)[L]) {
-  const int64_t left = e.N - n;
-  if (m >= e.M || left <= 0) return;
-  float t[L];
+struct Columns {
+  int64_t n, left;
+  float bias[L], scale[L];
+  __device__ __forceinline__ void load(const Epilogue& e, int64_t n_) {
+    n = n_;
+    left = e.N - n_;
+    if (e.bias) load_run((const O*)e.bias + n, left, bias);
+    if (e.w_scale) load_run(e.w_scale + n, left, scale);
+  }
+};
+template <typename O, int L>
+struct Residual {
+  O v[L];  // as it comes from memory
+  __device__ __forceinline__ void load(const Epilogue& e, int64_t m, int64_t n) {
+    if (e.residual && m < e.M) load_raw((const O*)e.residual + m * e.ldr + n, e.N - n, v);
+  }
+};
+
+// L adjacent columns of one row, from their sums over k.  The residual comes
+// loaded, for several rows at a time: the compiler keeps loads behind stores, and
+// one after another each would wait for memory.
+template <typename O, int L>
+__device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const Columns<O, L>& c, const Residual<O, L>& r,
+                                           float (&v)[L]) {
+  if (m >= e.M || c.left <= 0) return;
   if (e.x_scale) {
     const float xs = e.x_scale[m];
-    load_run(e.w_scale + n, left, t);
 #pragma unroll
-    for (int i = 0; i < L; ++i) v[i] *= xs * t[i];
+    for (int i = 0; i < L; ++i) v[i] *= xs * c.scale[i];
   }
   if (e.bias) {
-    load_run((const O*)e.bias + n, left, t);
 #pragma unroll
-    for (int i = 0; i < L; ++i) v[i] += t[i];
+    for (int i = 0; i < L; ++i) v[i] += c.bias[i];
   }
-  if (e.preact) store_run((O*)e.preact + m * e.N + n, left, v);
-  if (e.act != EEC_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < L; ++i) v[i] = act_value(v[i], e.act);
-  }
+  if (e.preact) store_run((O*)e.preact + m * e.N + c.n, c.left, v);
+  act_values(v, e.act);
   if (e.residual) {
-    load_run((const O*)e.residual + m * e.ldr + n, left, t);
 #pragma unroll
-    for (int i = 0; i < L; ++i) v[i] += t[i];
+    for (int i = 0; i < L; ++i) v[i] += (float)r.v[i];
   }
-  store_run((O*)e.y + m * e.N + n, left, v);
+  store_run((O*)e.y + m * e.N + c.n, c.left, v);
+}
+
+// Finishes (or, split, stores) the ROWS x 64 sums of a wave, which it has put in
+// LDS row by row of 256 bytes, the 16-byte chunk c of row r at c ^ (r & 15).  From
+// there each access takes 16 bytes a lane of whole rows, and the code is short
+// whatever a lane's registers hold: written out for every register it no longer
+// fits the instruction cache (8192 x 8192 x 32 bf16: 64 us, this 46 us).
+// Up to four rows' residuals a lane are on their way together.
+template <typename O, int ROWS>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, int64_t m0, int64_t n0) {
+  constexpr int L = 16 / (int)sizeof(O), PER = L;              // columns of a lane, rows of one access
+  constexpr int TOGETHER = ROWS / PER < 4 ? ROWS / PER : 4;
+  static_assert(ROWS % (TOGETHER * PER) == 0, "whole accesses");
+  const int lane = threadIdx.x & 63;
+  float* part = e.part ? e.part + (int64_t)blockIdx.y * e.M * e.N : nullptr;
+  if (n0 + 64 <= e.N) {
+    const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
+    Columns<O, L> c;
+    c.load(e, n0 + col);
+#pragma unroll 1
+    for (int r = r0; r < ROWS; r += TOGETHER * PER) {
+      Residual<O, L> res[TOGETHER];
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) res[i].load(e, m0 + r + i * PER, n0 + col);
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) {
+        const int row = r + i * PER;
+        float v[L];
+#pragma unroll
+        for (int u = 0; u < L; u += 4)
+          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
+        if (part == nullptr)
+          finish_run<O, L>(e, m0 + row, c, res[i], v);
+        else if (m0 + row < e.M)
+          __builtin_memcpy(part + (m0 + row) * e.N + n0 + col, v, sizeof(v));
+      }
+    }
+  } else {  // the last columns: one element a lane
+    const int64_t n = n0 + lane;
+    Columns<O, 1> c;
+    c.load(e, n);
+#pragma unroll 1
+    for (int row = 0; row < ROWS; ++row) {
+      const int64_t m = m0 + row;
+      Residual<O, 1> res;
+      if (n < e.N) res.load(e, m, n);
+      float v[1];
+      __builtin_memcpy(v, lds + (row * 256 + ((lane / 4) ^ (row & 15)) * 16 + lane % 4 * 4), 4);
+      if (part == nullptr)
+        finish_run<O, 1>(e, m, c, res, v);
+      else if (m < e.M && n < e.N)
+        part[m * e.N + n] = v[0];
+    }
+  }
+}
+// All of a wave's GROUPS matrix tiles of HIGH rows, PER of them at a time through
+// its own LDS; put(i, chunk(c)) writes the c-th four adjacent columns of tile i.
+template <typename O, int GROUPS, int HIGH, int PER, typename Put>
+__device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, Put put) {
+#pragma unroll 1
+  for (int g = 0; g < GROUPS; g += PER) {
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i)
+      if (i / PER * PER == g) put(i, lds + i % PER * HIGH * 256);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    finish_rows<O, PER * HIGH>(e, lds, m0 + g * HIGH, n0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+// Chunk c (four adjacent columns) of a row of a wave's sums.
+__device__ __forceinline__ void put_sums(char* rows, int row, int c, const f32x4& v) {
+  __builtin_memcpy(__builtin_assume_aligned(rows + (row * 256 + (c ^ (row & 15)) * 16), 16), &v, 16);
 }
 
 // Adds the splits in order and finishes: 4 columns a thread.
@@ -70,7 +157,11 @@ __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) v[c] += t[c];
     }
-    finish_run<O>(e, m, n, v);
+    Columns<O, 4> c;
+    c.load(e, n);
+    Residual<O, 4> r;
+    r.load(e, m, n);
+    finish_run<O, 4>(e, m, c, r, v);
   }
 }
 
@@ -189,17 +280,6 @@ __device__ __forceinline__ void put_chunk(char* at, int stride, const Raw<T>& r)
 
 // ------------------------------------------------------------------ general product
 
-// Column of a 64-column group held at LDS row p: the four 16-row matrix tiles of
-// a wave take the columns so that a lane ends with 16 adjacent ones (see acc).
-__device__ __forceinline__ int column_at(int p) { return ((p >> 2) & 3) * 16 + (p >> 4 & 3) * 4 + (p & 3); }
-// The same for the 32 x 32 tiles of the 8-bit instruction, which leave a lane 32 adjacent ones.
-__device__ __forceinline__ int column_at_8bit(int p) {
-  return (p >> 2 & 1) * 32 + (p >> 5) * 16 + (p >> 3 & 3) * 4 + (p & 3);
-}
-__device__ __forceinline__ int row_of_column(int n) {
-  return (n & ~63) | ((n >> 2) & 3) * 16 | ((n >> 4) & 3) * 4 | (n & 3);
-}
-
 struct Product {
   const void *a, *b;
   int64_t lda, ldb;
@@ -224,7 +304,7 @@ __device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_
 // A tile of 128 lines x 32 k of one operand, two 8-element chunks per thread.
 // KC: k runs along memory (a chunk is one run), otherwise the lines do (a chunk
 // is 8 runs of 2 lines).
-template <typename T, bool KC, bool IS_B>
+template <typename T, bool KC>
 struct Stage {
   static constexpr int ROW = GBK * sizeof(typename Mat<T>::E) + 8 * sizeof(typename Mat<T>::E);
   static constexpr int PLANE = GBM * ROW;
@@ -268,8 +348,7 @@ struct Stage {
     for (int i = 0; i < 2; ++i) {
       const int line = KC ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x & 63) * 2 + i;
       const int kc = KC ? threadIdx.x & 3 : threadIdx.x >> 6;
-      const int at = IS_B ? row_of_column(line) : line;
-      put_chunk<T>(lds + at * ROW + kc * 8 * sizeof(typename Mat<T>::E), PLANE, r[i]);
+      put_chunk<T>(lds + line * ROW + kc * 8 * sizeof(typename Mat<T>::E), PLANE, r[i]);
     }
   }
 };
@@ -284,9 +363,10 @@ template <typename T, typename O, bool A_KC, bool B_KC>
 __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   using M_ = Mat<T>;
   constexpr int P = M_::PLANES;
-  using SA = Stage<T, A_KC, false>;
-  using SB = Stage<T, B_KC, true>;
-  __shared__ __attribute__((aligned(16))) char lds[P * (SA::PLANE + SB::PLANE)];
+  using SA = Stage<T, A_KC>;
+  using SB = Stage<T, B_KC>;
+  constexpr int TILES = P * (SA::PLANE + SB::PLANE), SUMS = 4 * 4096;  // 4 KB of each wave for a matrix tile's sums
+  __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
   char* lds_b = lds + P * SA::PLANE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t m0, n0;
@@ -329,18 +409,17 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
       for (int i = 0; i < 4; ++i) M_::mul(fb, fa[i], acc[i][j]);
     }
   }
+  __syncthreads();
+  constexpr int PER = sizeof(lds) >= 2 * SUMS ? 2 : 1;
+  finish_wave<O, 4, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, [&](int i, char* rows) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + wm + 16 * i + (lane & 15), n = n0 + wn + (lane >> 4) * 16;
-    float v[16];
+    for (int j = 0; j < 4; ++j) {
+      f32x4 v;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) v[c] = M_::total(acc[i][c >> 2], c & 3);
-    if (e.part) {
-      if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
-    } else {
-      finish_run<O>(e, m, n, v);
+      for (int c = 0; c < 4; ++c) v[c] = M_::total(acc[i][j], c);
+      put_sums(rows, lane & 15, j * 4 + (lane >> 4), v);
     }
-  }
+  });
 }
 
 // ------------------------------------------------------------------ tiled product (16- and 8-bit, aligned)
@@ -364,7 +443,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 //       banks.  Only the low bits of a chunk's place depend on the lane, so a few
 //       address registers serve all fragments.
 // Neither has a bank conflict by the counter.
-template <typename T, bool KC, bool IS_B, int LINES, int WAVES>
+template <typename T, bool KC, int LINES, int WAVES>
 struct Tile {
   static constexpr int BK = 64 / (int)sizeof(T);          // k of a tile
   static constexpr int LOADS = LINES / 16 / WAVES;        // direct loads of one wave
@@ -402,9 +481,7 @@ struct Tile {
     for (int i = 0; i < LOADS; ++i) {
       if constexpr (KC) {
         const int r = place(i) * 16 + (lane >> 2), c = (lane & 3) ^ (r >> 2 & 3);
-        // the LDS rows of B are its columns in the order a lane keeps them
-        const int own = !IS_B ? r : (r & ~63) + (sizeof(T) == 1 ? column_at_8bit(r & 63) : column_at(r & 63));
-        const int64_t line = min((int64_t)own, lines - 1 - line0);
+        const int64_t line = min((int64_t)r, lines - 1 - line0);  // lines past the end: not stored
         off[i] = (uint32_t)(line * ld * (int64_t)sizeof(T)) + c * 16;
       } else {
         const int k = at_k(i), c = (lane % CHUNKS) ^ (k % PER_LOAD * 2);
@@ -468,7 +545,7 @@ struct Tile {
 // the tile before, so that a tile begins with what it needs in registers.
 template <typename T, int MI>
 struct Share {
-  static constexpr int ROWS = 16, GROUPS = MI, RUN = 16;  // rows of a matrix tile, tiles, adjacent columns of a lane
+  static constexpr int ROWS = 16, GROUPS = MI;  // rows of a matrix tile, tiles along m
   static constexpr int NB = 4, AHEAD = 2;
   using Frag = typename Mat<T>::Frag;
   f32x4 acc[GROUPS][NB] = {};
@@ -478,18 +555,29 @@ struct Share {
     Mat<T>::mul(fb, fa, c);
     acc[i][j] = c[0];
   }
-  __device__ __forceinline__ float at(int i, int c) const { return acc[i][c >> 2][c & 3]; }
+  __device__ __forceinline__ void put(int i, char* rows) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), acc[i][j]);
+  }
 };
 template <int MI>
 struct Share<e4m3, MI> {
-  static constexpr int ROWS = 32, GROUPS = MI / 2, RUN = 32;
+  static constexpr int ROWS = 32, GROUPS = MI / 2;
   static constexpr int NB = 2, AHEAD = 1;
   using Frag = i32x8;
   f32x16 acc[GROUPS][NB] = {};
   __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {  // block scales of 2^0
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
   }
-  __device__ __forceinline__ float at(int i, int c) const { return acc[i][c >> 4][c & 15]; }
+  __device__ __forceinline__ void put(int i, char* rows) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const f32x4 v = {acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]};
+        put_sums(rows, threadIdx.x & 31, j * 8 + a * 2 + (threadIdx.x >> 5 & 1), v);
+      }
+  }
 };
 template <typename S>
 struct Ahead {
@@ -553,8 +641,8 @@ template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
-  using TA = Tile<T, A_KC, false, BM, WAVES>;
-  using TB = Tile<T, B_KC, true, BN, WAVES>;
+  using TA = Tile<T, A_KC, BM, WAVES>;
+  using TB = Tile<T, B_KC, BN, WAVES>;
   constexpr int BK = TA::BK, LOADS = TA::LOADS + TB::LOADS;
   // The buffers are variables of their own: the compiler then sees that loads into
   // one do not touch the others, and does not wait for them before it reads.
@@ -601,33 +689,13 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   }
 #undef EEC_FOUR_TILES
 #undef EEC_TILE
-#pragma unroll
-  for (int i = 0; i < S::GROUPS; ++i) {
-    const int64_t m = m0 + wm + S::ROWS * i + (lane % S::ROWS);
-    if constexpr (B_KC) {
-      constexpr int L = S::RUN;
-      const int64_t n = n0 + wn + (lane / S::ROWS) * L;
-      float v[L];
-#pragma unroll
-      for (int j = 0; j < L; ++j) v[j] = c.at(i, j);
-      if (e.part) {
-        if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
-      } else {
-        finish_run<O>(e, m, n, v);
-      }
-    } else {  // columns in memory order: 4 adjacent ones a lane
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + wn + 16 * j + (lane >> 4) * 4;
-        float v[4] = {c.at(i, 4 * j), c.at(i, 4 * j + 1), c.at(i, 4 * j + 2), c.at(i, 4 * j + 3)};
-        if (e.part) {
-          if (m < e.M) store_run(e.part + ((int64_t)blockIdx.y * e.M + m) * e.N + n, e.N - n, v);
-        } else {
-          finish_run<O>(e, m, n, v);
-        }
-      }
-    }
-  }
+  tile_barrier<0>();  // nobody's loads or reads are left in the buffers
+  // 32 rows of a wave in 8 KB: two waves to an operand's buffer
+  static_assert(TA::BYTES * 4 >= WAVES * 8192, "room for 8 KB a wave");
+  const int of = WAVES == 4 ? wave : wave >> 1;
+  char* mine = (of == 0 ? a0 : of == 1 ? a1 : of == 2 ? a2 : a3) + (WAVES == 4 ? 0 : (wave & 1) * 8192);
+  finish_wave<O, S::GROUPS, S::ROWS, 32 / S::ROWS>(
+      e, mine, m0 + wm, n0 + wn, [&](int i, char* rows) { c.put(i, rows); });
 #endif
 }
 
@@ -727,7 +795,12 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
 #pragma unroll
     for (int i = 1; i < WAVES; ++i) v += join[i][wave][lane];
     float r[4] = {v[0], v[1], v[2], v[3]};
-    finish_run<O>(e, wave * 16 + (lane & 15), n0 + q * 4, r);
+    const int64_t m = wave * 16 + (lane & 15);
+    Columns<O, 4> c;
+    c.load(e, n0 + q * 4);
+    Residual<O, 4> res;
+    res.load(e, m, n0 + q * 4);
+    finish_run<O, 4>(e, m, c, res, r);
   }
 }
 
@@ -756,8 +829,7 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
     load_run((const T*)a.gy + r * a.ldgy + col, left, g);
     if (a.act != EEC_ACT_NONE) {
       load_run((const T*)a.preact + r * a.cols + col, left, z);
-#pragma unroll
-      for (int i = 0; i < V; ++i) g[i] *= act_slope(z[i], a.act);
+      act_slopes(g, z, a.act);
     }
     if (a.gz) store_run((T*)a.gz + r * a.cols + col, left, g);
 #pragma unroll

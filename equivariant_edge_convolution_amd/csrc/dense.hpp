@@ -39,6 +39,17 @@ __device__ __forceinline__ void load_run(const T* __restrict__ p, int64_t valid,
   }
 }
 
+// The same as they are stored.
+template <typename T, int N>
+__device__ __forceinline__ void load_raw(const T* __restrict__ p, int64_t valid, T (&v)[N]) {
+  if (valid >= N) {
+    __builtin_memcpy(v, p, sizeof(v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < valid ? p[i] : T(0);
+  }
+}
+
 // The first `valid` of N floats, each rounded once to T (to nearest even).
 template <typename T, int N>
 __device__ __forceinline__ void store_run(T* __restrict__ p, int64_t valid, const float (&v)[N]) {
@@ -80,22 +91,38 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
 
-// act(z) and its slope; the branch is uniform over the launch.
-__device__ __forceinline__ float act_value(float z, int act) {
-  if (act == EEC_ACT_SILU) return z * sigmoid(z);
-  if (act == EEC_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-  if (act == EEC_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
-  return z;
-}
-__device__ __forceinline__ float act_slope(float z, int act) {
+// act in place; the branch is uniform over the launch and taken once per run.
+template <int N>
+__device__ __forceinline__ void act_values(float (&z)[N], int act) {
   if (act == EEC_ACT_SILU) {
-    const float p = sigmoid(z);
-    return p * (1.f + z * (1.f - p));
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] *= sigmoid(z[i]);
+  } else if (act == EEC_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.f + erff(z[i] * 0.70710678118654752f));
+  } else if (act == EEC_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // a NaN stays one
   }
-  if (act == EEC_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-  if (act == EEC_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  return 1.f;
+}
+// g act'(z) in place of g.
+template <int N>
+__device__ __forceinline__ void act_slopes(float (&g)[N], const float (&z)[N], int act) {
+  if (act == EEC_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float p = sigmoid(z[i]);
+      g[i] *= p * (1.f + z[i] * (1.f - p));
+    }
+  } else if (act == EEC_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      g[i] *= 0.5f * (1.f + erff(z[i] * 0.70710678118654752f)) +
+              z[i] * expf(-0.5f * z[i] * z[i]) * 0.39894228040143268f;
+  } else if (act == EEC_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] *= z[i] > 0.f ? 1.f : 0.f;
+  }
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
