@@ -128,7 +128,7 @@ def lib() -> ctypes.CDLL:
     L.eec_add_rms_norm_backward.restype = ctypes.c_int
     L.eec_add_rms_norm_backward.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp, sz]
     L.eec_linear_workspace_bytes.restype = sz
-    L.eec_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.eec_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
     L.eec_linear.restype = ctypes.c_int
     L.eec_linear.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, i64, i32, vp, vp, vp, sz]
     L.eec_linear_backward_workspace_bytes.restype = sz
@@ -537,7 +537,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
         out["preact"] = torch.empty((rows, n), dtype=ot, device=dev)
     ws = workspace
     if ws is None:
-        need = lib().eec_linear_workspace_bytes(rows, n, k, DTYPES[dt])
+        need = lib().eec_linear_workspace_bytes(rows, n, k, DTYPES[dt], DTYPES[ot])
         ws = _workspace(need, dev) if need else None
     _check(lib().eec_linear(_raw_stream(dev), rows, n, k, DTYPES[dt], DTYPES[ot], x.data_ptr(), ldx, xs, w.data_ptr(),
                             ldw, wsc, b, _address(residual), ldr, ACTS[act], y.data_ptr(), _address(out.get("preact")),

@@ -617,9 +617,9 @@ static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
   return EEC_OK;
 }
 
-size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype) {
+size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
   if (bad_size(rows) || bad_size(outer) || bad_size(inner) || (!float_dtype(dtype) && dtype != EEC_E4M3)) return 0;
-  return linear_workspace(rows, outer, inner, dtype);
+  return linear_workspace(rows, outer, inner, dtype, out_dtype);
 }
 
 eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype,
@@ -644,7 +644,7 @@ eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, 
   TRY(check_optional(residual, rows, outer, ldr, out_dtype, "residual"));
   TRY(check_matrix(y, rows, outer, outer, out_dtype, "y"));
   TRY(check_optional(preact, rows, outer, outer, out_dtype, "preact"));
-  TRY(check_ws(workspace, workspace_bytes, linear_workspace(rows, outer, inner, dtype)));
+  TRY(check_ws(workspace, workspace_bytes, linear_workspace(rows, outer, inner, dtype, out_dtype)));
   TRY(check_alias({matrix(y, rows, outer, outer, out_dtype, "y"), matrix(preact, rows, outer, outer, out_dtype, "preact"),
                    span(workspace, workspace_bytes, "workspace")},
                   {matrix(x, rows, inner, ldx, dtype, "x"), matrix(w, outer, inner, ldw, dtype, "w"),

@@ -85,43 +85,25 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, 
   static_assert(ROWS % (TOGETHER * PER) == 0, "whole accesses");
   const int lane = threadIdx.x & 63;
   float* part = e.part ? e.part + (int64_t)blockIdx.y * e.M * e.N : nullptr;
-  if (n0 + 64 <= e.N) {
-    const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
-    Columns<O, L> c;
-    c.load(e, n0 + col);
+  const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
+  Columns<O, L> c;
+  c.load(e, n0 + col);
 #pragma unroll 1
-    for (int r = r0; r < ROWS; r += TOGETHER * PER) {
-      Residual<O, L> res[TOGETHER];
+  for (int r = r0; r < ROWS; r += TOGETHER * PER) {
+    Residual<O, L> res[TOGETHER];
 #pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) res[i].load(e, m0 + r + i * PER, n0 + col);
+    for (int i = 0; i < TOGETHER; ++i) res[i].load(e, m0 + r + i * PER, n0 + col);
 #pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        const int row = r + i * PER;
-        float v[L];
+    for (int i = 0; i < TOGETHER; ++i) {
+      const int row = r + i * PER;
+      float v[L];
 #pragma unroll
-        for (int u = 0; u < L; u += 4)
-          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
-        if (part == nullptr)
-          finish_run<O, L>(e, m0 + row, c, res[i], v);
-        else if (m0 + row < e.M)
-          __builtin_memcpy(part + (m0 + row) * e.N + n0 + col, v, sizeof(v));
-      }
-    }
-  } else {  // the last columns: one element a lane
-    const int64_t n = n0 + lane;
-    Columns<O, 1> c;
-    c.load(e, n);
-#pragma unroll 1
-    for (int row = 0; row < ROWS; ++row) {
-      const int64_t m = m0 + row;
-      Residual<O, 1> res;
-      if (n < e.N) res.load(e, m, n);
-      float v[1];
-      __builtin_memcpy(v, lds + (row * 256 + ((lane / 4) ^ (row & 15)) * 16 + lane % 4 * 4), 4);
+      for (int u = 0; u < L; u += 4)
+        __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
       if (part == nullptr)
-        finish_run<O, 1>(e, m, c, res, v);
-      else if (m < e.M && n < e.N)
-        part[m * e.N + n] = v[0];
+        finish_run<O, L>(e, m0 + row, c, res[i], v);
+      else if (m0 + row < e.M)
+        store_run(part + (m0 + row) * e.N + n0 + col, c.left, v);
     }
   }
 }
@@ -168,42 +150,46 @@ __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
 // ------------------------------------------------------------------ matrix instructions
 
 // float32 as the exact sum of three bf16 parts (8 + 8 + 8 significant bits, cut
-// towards zero, so that no part overflows; below 2^-109 the last parts end at
-// bf16's smallest step, 2^-133).  NaN and infinities stay in the first part, the
-// others are 0 then.
+// towards zero, so that no part overflows and all have the sign of x).  A part that
+// would be 0 beside a value that is not takes the smallest bf16, 2^-133: an
+// infinity times any part of the other operand is then an infinity of the right
+// sign, never the NaN of an infinity times 0, and the sums of part products need no
+// care.  So a value is held to 2^-131, exactly above 2^-100 but for that.
 __device__ __forceinline__ void split3(float x, bf16& h, bf16& m, bf16& l) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x), sign = u >> 16 & 0x8000u, least = x != 0.f ? 1u : 0u;
   const bool finite = (u & 0x7f800000u) != 0x7f800000u;
   const uint32_t hi = (u & 0xffff0000u) | (x != x ? 0x400000u : 0u);  // a NaN keeps a bit of its fraction
   const float r = finite ? x - __uint_as_float(hi) : 0.f;
   const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
-  const float rl = r - __uint_as_float(mid);
-  h = __builtin_bit_cast(bf16, (uint16_t)(hi >> 16));
-  m = __builtin_bit_cast(bf16, (uint16_t)(mid >> 16));
-  l = __builtin_bit_cast(bf16, (uint16_t)(__float_as_uint(rl) >> 16));
+  const uint32_t low = __float_as_uint(r - __uint_as_float(mid));
+  auto part = [&](uint32_t bits) {
+    const uint32_t size = max(bits >> 16 & 0x7fffu, least);
+    return __builtin_bit_cast(bf16, (uint16_t)(size | sign));
+  };
+  h = part(hi);
+  m = part(mid);
+  l = part(low);
 }
 
 template <typename T>
-struct Mat;  // operand planes in LDS (element type, count), and the product of 8-element fragments in ACCS sums
+struct Mat;  // operand planes in LDS (element type, count), and the product of 8-element fragments
 template <>
 struct Mat<f16> {
   using E = f16;
-  static constexpr int PLANES = 1, ACCS = 1;
+  static constexpr int PLANES = 1;
   using Frag = f16x8;
-  static __device__ __forceinline__ void mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 (&c)[1]) {
-    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0], a[0], c[0], 0, 0, 0);
+  static __device__ __forceinline__ f32x4 mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(b[0], a[0], c, 0, 0, 0);
   }
-  static __device__ __forceinline__ float total(const f32x4 (&c)[1], int i) { return c[0][i]; }
 };
 template <>
 struct Mat<bf16> {
   using E = bf16;
-  static constexpr int PLANES = 1, ACCS = 1;
+  static constexpr int PLANES = 1;
   using Frag = bf16x8;
-  static __device__ __forceinline__ void mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 (&c)[1]) {
-    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[0], c[0], 0, 0, 0);
+  static __device__ __forceinline__ f32x4 mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[0], c, 0, 0, 0);
   }
-  static __device__ __forceinline__ float total(const f32x4 (&c)[1], int i) { return c[0][i]; }
 };
 // The 8-bit instructions align a sum's products before they add them: over all
 // bit patterns their result was up to 9e-5 of sum |a||b| off (1e-5 for normally
@@ -213,12 +199,11 @@ struct Mat<bf16> {
 template <>
 struct Mat<e4m3> {
   using E = e4m3;
-  static constexpr int PLANES = 1, ACCS = 1;
+  static constexpr int PLANES = 1;
   using Frag = long;
-  static __device__ __forceinline__ void mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 (&c)[1]) {
-    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b[0], a[0], c[0], 0, 0, 0);
+  static __device__ __forceinline__ f32x4 mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b[0], a[0], c, 0, 0, 0);
   }
-  static __device__ __forceinline__ float total(const f32x4 (&c)[1], int i) { return c[0][i]; }
 };
 struct e4m3_wide : e4m3 {};
 template <>
@@ -226,22 +211,16 @@ struct Mat<e4m3_wide> : Mat<bf16> {};
 template <>
 struct Mat<float> {
   using E = bf16;
-  static constexpr int PLANES = 3, ACCS = 2;
+  static constexpr int PLANES = 3;
   using Frag = bf16x8;
-  // The products of the first parts in one sum, the five next in size in another;
-  // the three left out are below 2^-24 of the whole.  The sums are kept apart
-  // because an infinity times a part that is 0 makes the second a NaN: a first
-  // sum that is not finite is the result by itself.
-  static __device__ __forceinline__ void mul(const Frag (&b)[3], const Frag (&a)[3], f32x4 (&c)[2]) {
-    c[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[0], c[0], 0, 0, 0);
-    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[1], a[1], c[1], 0, 0, 0);
-    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[2], a[0], c[1], 0, 0, 0);
-    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[2], c[1], 0, 0, 0);
-    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[1], a[0], c[1], 0, 0, 0);
-    c[1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[1], c[1], 0, 0, 0);
-  }
-  static __device__ __forceinline__ float total(const f32x4 (&c)[2], int i) {
-    return (__float_as_uint(c[0][i]) & 0x7f800000u) == 0x7f800000u ? c[0][i] : c[0][i] + c[1][i];
+  // The part products in rising size; the three left out are below 2^-24 of the whole.
+  static __device__ __forceinline__ f32x4 mul(const Frag (&b)[3], const Frag (&a)[3], f32x4 c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[2], a[0], c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[2], c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[1], a[1], c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[1], a[0], c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[1], c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[0], a[0], c, 0, 0, 0);
   }
 };
 
@@ -284,7 +263,8 @@ struct Product {
   const void *a, *b;
   int64_t lda, ldb;
   int64_t M, N, K;
-  int64_t k_split;  // k of one split, a multiple of GBK
+  int64_t k_split;           // k of one split, a multiple of 128
+  int64_t a_plane, b_plane;  // bytes between an operand's parts (float32 in planes)
 };
 
 constexpr int GBM = 128, GBN = 128, GBK = 32;
@@ -375,7 +355,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   n0 *= GBN;
   const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x4 acc[4][4][M_::ACCS] = {};
+  f32x4 acc[4][4] = {};
   SA sa;
   SB sb;
   if (kb < ke) {
@@ -406,19 +386,14 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
         __builtin_memcpy(&fb[p], __builtin_assume_aligned(lds_b + p * SB::PLANE + (wn + 16 * j) * SB::ROW + at, 8),
                          sizeof(fb[p]));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) M_::mul(fb, fa[i], acc[i][j]);
+      for (int i = 0; i < 4; ++i) acc[i][j] = M_::mul(fb, fa[i], acc[i][j]);
     }
   }
   __syncthreads();
   constexpr int PER = sizeof(lds) >= 2 * SUMS ? 2 : 1;
   finish_wave<O, 4, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, [&](int i, char* rows) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f32x4 v;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = M_::total(acc[i][j], c);
-      put_sums(rows, lane & 15, j * 4 + (lane >> 4), v);
-    }
+    for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
   });
 }
 
@@ -443,7 +418,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 //       banks.  Only the low bits of a chunk's place depend on the lane, so a few
 //       address registers serve all fragments.
 // Neither has a bank conflict by the counter.
-template <typename T, bool KC, int LINES, int WAVES>
+template <typename T, bool KC, int LINES, int WAVES, int PARTS>
 struct Tile {
   static constexpr int BK = 64 / (int)sizeof(T);          // k of a tile
   static constexpr int LOADS = LINES / 16 / WAVES;        // direct loads of one wave
@@ -453,9 +428,15 @@ struct Tile {
   static constexpr int BYTES = LINES / 16 * STRIDE;
   static constexpr int READS = KC && sizeof(T) == 2 ? 1 : 2;  // LDS reads of one fragment
   static constexpr uint32_t NOWHERE = 0x80000000u;        // past every buffer: reads as zero
+  static constexpr int RUNS = 6;
   const char* base;  // of the next tile, uniform
   int64_t step;      // bytes from tile to tile
   uint32_t off[LOADS];
+  // PARTS: the operand's order of parts, two bits each, over as many runs through k
+  // of `tiles` tiles each.
+  const char* first;
+  int64_t plane;
+  int tile, tiles, run;
 
   // Load i of this wave: its place among the tile's loads.
   static __device__ __forceinline__ int place(int i) { return wave_id() * LOADS + i; }
@@ -473,9 +454,17 @@ struct Tile {
   static __device__ __forceinline__ int block_of(int u) {
     return PER_LOAD == 2 ? (u & 9) | (u & 2) << 1 | (u >> 1 & 2) : (u & 4) | (u & 1) << 1 | (u >> 1 & 1);
   }
-  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0) {
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0, int64_t k1,
+                                       int64_t plane_) {
     const int lane = threadIdx.x & 63;
     base = (const char*)p + (KC ? (line0 * ld + k0) : (k0 * ld + line0)) * (int64_t)sizeof(T);
+    if constexpr (PARTS != 0) {
+      first = base;
+      plane = plane_;
+      tile = run = 0;
+      tiles = (int)((k1 - k0) / BK);
+      base += (PARTS & 3) * plane;
+    }
     step = (KC ? (int64_t)BK : (int64_t)BK * ld) * (int64_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -492,8 +481,8 @@ struct Tile {
   // Loads the next tile; with TAIL only `left` of its k exist (none, perhaps).
   template <bool TAIL>
   __device__ __forceinline__ void load(char* lds, int64_t left) {
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)0x7fffffff, 0x00020000);
+    const int size = PARTS != 0 && run >= RUNS ? 0 : 0x7fffffff;  // after the last run, nothing: reads as zero
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, size, 0x00020000);
     if constexpr (TAIL) {  // what lies past the end reads as zero from here on
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) off[i] = at_k(i) < left ? off[i] : NOWHERE;
@@ -503,6 +492,12 @@ struct Tile {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           rsrc, (__attribute__((address_space(3))) void*)(lds + place(i) * STRIDE), 16, off[i], 0, 0, 0);
     base += step;
+    if constexpr (PARTS != 0) {
+      const bool last = ++tile == tiles;
+      tile = last ? 0 : tile;
+      run += last ? 1 : 0;
+      base = last ? first + (PARTS >> 2 * run & 3) * plane : base;
+    }
   }
   // Fragment i of the lines from `line` (a multiple of 64).  Each address is one
   // addition to the buffer: through a longer chain the compiler loses sight of the
@@ -550,10 +545,8 @@ struct Share {
   using Frag = typename Mat<T>::Frag;
   f32x4 acc[GROUPS][NB] = {};
   __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {
-    f32x4 c[1] = {acc[i][j]};
     const Frag fb[1] = {b}, fa[1] = {a};
-    Mat<T>::mul(fb, fa, c);
-    acc[i][j] = c[0];
+    acc[i][j] = Mat<T>::mul(fb, fa, acc[i][j]);
   }
   __device__ __forceinline__ void put(int i, char* rows) const {
 #pragma unroll
@@ -637,12 +630,16 @@ __device__ __forceinline__ void tile_barrier() {
 // from, the one after is on its way, and a third is started into the buffer that
 // everybody left at that barrier.
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
-template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
+// PARTED: float32 operands as planes of bf16 parts (k_pack, k in whole groups of
+// four tiles, zeros past the end).  The six part products are six runs through k,
+// in rising size, of the one bf16 kernel.
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, bool PARTED>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
-  using TA = Tile<T, A_KC, BM, WAVES>;
-  using TB = Tile<T, B_KC, BN, WAVES>;
+  // the parts h, m, l as 0, 1, 2: (l, h), (h, l), (m, m), (m, h), (h, m), (h, h)
+  using TA = Tile<T, A_KC, BM, WAVES, PARTED ? 2 | 0 << 2 | 1 << 4 | 1 << 6 | 0 << 8 | 0 << 10 : 0>;
+  using TB = Tile<T, B_KC, BN, WAVES, PARTED ? 0 | 2 << 2 | 1 << 4 | 0 << 6 | 1 << 8 | 0 << 10 : 0>;
   constexpr int BK = TA::BK, LOADS = TA::LOADS + TB::LOADS;
   // The buffers are variables of their own: the compiler then sees that loads into
   // one do not touch the others, and does not wait for them before it reads.
@@ -650,7 +647,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   __shared__ __attribute__((aligned(1024))) char b0[TB::BYTES], b1[TB::BYTES], b2[TB::BYTES], b3[TB::BYTES];
   const int lane = threadIdx.x & 63, wave = wave_id();
   int64_t m0, n0;
-  tile_of((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, m0, n0);
+  tile_of((e.M + BM - 1) / BM, (e.N + BN - 1) / BN, m0, n0);
   m0 *= BM;
   n0 *= BN;
   const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
@@ -660,14 +657,14 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   Ahead<S> f0, f1;
   TA ta;
   TB tb;
-  ta.init(g.a, g.lda, m0, g.M, kb);
-  tb.init(g.b, g.ldb, n0, g.N, kb);
-  ta.template load<true>(a0, ke - kb);
-  tb.template load<true>(b0, ke - kb);
-  ta.template load<true>(a1, ke - kb - BK);
-  tb.template load<true>(b1, ke - kb - BK);
-  ta.template load<true>(a2, ke - kb - 2 * BK);
-  tb.template load<true>(b2, ke - kb - 2 * BK);
+  ta.init(g.a, g.lda, m0, g.M, kb, ke, g.a_plane);
+  tb.init(g.b, g.ldb, n0, g.N, kb, ke, g.b_plane);
+  ta.template load<!PARTED>(a0, ke - kb);
+  tb.template load<!PARTED>(b0, ke - kb);
+  ta.template load<!PARTED>(a1, ke - kb - BK);
+  tb.template load<!PARTED>(b1, ke - kb - BK);
+  ta.template load<!PARTED>(a2, ke - kb - 2 * BK);
+  tb.template load<!PARTED>(b2, ke - kb - 2 * BK);
   tile_barrier<2 * LOADS>();
   read_ahead<S, TA, TB>(f0, a0, b0, wm, wn);
   int64_t k = kb;
@@ -681,11 +678,17 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   EEC_TILE(TAIL, 1, f1, a1, f0, a2, b2, a0, b0);   \
   EEC_TILE(TAIL, 2, f0, a2, f1, a3, b3, a1, b1);   \
   EEC_TILE(TAIL, 3, f1, a3, f0, a0, b0, a2, b2)
-  for (; k + 7 * BK <= ke; k += 4 * BK) {  // every tile it loads is whole
-    EEC_FOUR_TILES(false);
-  }
-  for (; k < ke; k += 4 * BK) {  // tiles past the end are zeros, read from nowhere
-    EEC_FOUR_TILES(true);
+  if constexpr (PARTED) {
+    for (int64_t end = kb + (ke - kb) * TA::RUNS; k < end; k += 4 * BK) {
+      EEC_FOUR_TILES(false);
+    }
+  } else {
+    for (; k + 7 * BK <= ke; k += 4 * BK) {  // every tile it loads is whole
+      EEC_FOUR_TILES(false);
+    }
+    for (; k < ke; k += 4 * BK) {  // tiles past the end are zeros, read from nowhere
+      EEC_FOUR_TILES(true);
+    }
   }
 #undef EEC_FOUR_TILES
 #undef EEC_TILE
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   const T* x[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = (const T*)g.a + min((int64_t)(t * 16 + (lane & 15)), g.M - 1) * g.lda;
-  f32x4 acc[MT][M_::ACCS] = {};
+  f32x4 acc[MT] = {};
   // A run of CHUNK k: lane group q holds STEPS * 8 adjacent ones, of which step s
   // multiplies the s-th 8 (the same k of both operands meet, which is all a sum asks).
   struct Run {
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         parts(xr[t].v[s], fx);
-        M_::mul(fw, fx, acc[t]);
+        acc[t] = M_::mul(fw, fx, acc[t]);
       }
     }
   };
@@ -784,10 +787,7 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   }
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    f32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = M_::total(acc[t], i);
-    join[wave][t][lane] = v;
+    join[wave][t][lane] = acc[t];
   }
   __syncthreads();
   if (wave < MT) {
@@ -849,11 +849,75 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
   }
 }
 
+// ------------------------------------------------------------------ packing
+
+// A matrix laid out for the tiled product: rows padded to a stride of whole 16-byte
+// chunks with zeros; float32 as three planes of bf16 parts, rows and columns padded
+// to multiples of 128 (either may be k).
+struct Packing {
+  const void* from;
+  int64_t ld, rows, cols;        // of the source
+  char* to;                      // NULL: nothing to do
+  int64_t to_ld, to_rows;        // elements
+  int64_t plane;                 // bytes
+};
+struct Packings {
+  Packing p[3];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_pack(Packings all) {
+  constexpr int V = sizeof(T) == 1 ? 16 : 8;
+  const Packing p = all.p[blockIdx.y];
+  if (p.to == nullptr) return;
+  const uint32_t chunks = (uint32_t)(p.to_ld / V), per = max(1u, 512u / chunks);  // rows of a workgroup's turn
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.to_rows; r0 += (int64_t)gridDim.x * per) {
+    const uint32_t total = chunks * (uint32_t)min((int64_t)per, p.to_rows - r0);
+    for (uint32_t i = threadIdx.x; i < total; i += 256) {
+      const int64_t row = r0 + i / chunks, col = (int64_t)(i % chunks) * V;
+      T v[V];
+      load_raw((const T*)p.from + row * p.ld + col, row < p.rows ? p.cols - col : 0, v);
+      if constexpr (std::is_same<T, float>::value) {
+        bf16 q[3][V];
+#pragma unroll
+        for (int c = 0; c < V; ++c) split3(v[c], q[0][c], q[1][c], q[2][c]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          __builtin_memcpy(__builtin_assume_aligned(p.to + k * p.plane + (row * p.to_ld + col) * 2, 16), q[k], 16);
+      } else {
+        __builtin_memcpy(__builtin_assume_aligned(p.to + (row * p.to_ld + col) * (int64_t)sizeof(T), 16), v, 16);
+      }
+    }
+  }
+}
+
+constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+// Element size of `dtype`'s packed form, its stride, rows and bytes.
+int packed_size(int32_t dtype) { return dtype == EEC_E4M3 ? 1 : 2; }
+Packing packing(int32_t dtype, const void* from, int64_t ld, int64_t rows, int64_t cols, char* to) {
+  Packing p{from, ld, rows, cols, to, 0, 0, 0};
+  p.to_ld = dtype == EEC_F32 ? up(cols, 128) : up(cols, 16 / packed_size(dtype));
+  p.to_rows = dtype == EEC_F32 ? up(rows, 128) : rows;
+  p.plane = p.to_rows * p.to_ld * packed_size(dtype);
+  return p;
+}
+size_t packed_bytes(int32_t dtype, int64_t rows, int64_t cols) {
+  return align256((size_t)packing(dtype, nullptr, 0, rows, cols, nullptr).plane * (dtype == EEC_F32 ? 3 : 1));
+}
+template <typename T>
+void pack(hipStream_t st, const Packings& all) {
+  int64_t most = 0;
+  for (const Packing& p : all.p)
+    if (p.to) most = std::max(most, p.to_rows * p.to_ld);
+  if (most > 0) k_pack<T><<<dim3((unsigned)std::min<int64_t>((most + 4095) / 4096, 4096), 3), 256, 0, st>>>(all);
+}
+
 // ------------------------------------------------------------------ plans
 
 enum Kind { GENERAL, TILE128, TILE256, FEW };
 struct Plan {
   Kind kind;
+  bool packed;  // operands through k_pack
   int64_t tiles, splits, k_split;
 };
 
@@ -864,10 +928,20 @@ int64_t tiles_of(int64_t M, int64_t N, int b) { return ((M + b - 1) / b) * ((N +
 // at 64, where they take 18 us).
 constexpr int64_t FEW_ROWS = 32;
 
-// How a product is run: a rule on its sizes and on whether its operands take the
-// tiled kernel.  k is split where the tiles alone leave most of the 256 CUs idle,
-// into at least 512 k each.
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool forward) {
+// Whether a product is worth packing for.  Packing reads and writes the operands
+// once, in proportion to (M + N) K, and what it gains over the general kernel goes
+// with M N K.
+bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype) {
+  if (M <= FEW_ROWS || N <= FEW_ROWS) return false;
+  if (M > 1 << 20 || N > 1 << 20 || K > 1 << 20) return false;  // lanes' offsets within a tile fit 31 bits
+  const double least = dtype == EEC_F32 ? 192 : 128;
+  return (double)M * N >= least * (M + N) && (double)M * N * K >= 4e8;
+}
+
+// How a product is run: a rule on sizes, type and (aligned) whether the operands
+// take the tiled kernel as they are.  k is split where the tiles alone leave most of
+// the 256 CUs idle, into at least 128 (tiled: 256) k each.
+Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool aligned, bool packed, bool forward) {
   Plan p{};
   if (forward && M <= FEW_ROWS) {
     p.kind = FEW;
@@ -875,17 +949,21 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool forward) {
     return p;
   }
   const int64_t t256 = tiles_of(M, N, 256);
-  p.kind = !tiled ? GENERAL : t256 >= 192 ? TILE256 : TILE128;
+  p.packed = packed;
+  p.kind = !(aligned || packed) ? GENERAL : t256 >= 192 ? TILE256 : TILE128;
   p.tiles = p.kind == TILE256 ? t256 : tiles_of(M, N, 128);
-  const int64_t step = 128;  // k of a split is a multiple of every kernel's tile
-  int64_t s = std::min<int64_t>((p.kind == TILE256 ? 256 : 512) / std::max<int64_t>(1, p.tiles), K / 512);
+  const int64_t step = 128;  // k of a split is a multiple of every kernel's tiles
+  int64_t s = std::min<int64_t>((p.kind == TILE256 ? 256 : 512) / std::max<int64_t>(1, p.tiles),
+                                K / (p.kind == GENERAL ? 128 : 256));
   s = std::max<int64_t>(1, s);
-  p.k_split = std::max<int64_t>(step, ((K + s - 1) / s + step - 1) / step * step);
+  p.k_split = std::max<int64_t>(step, up((K + s - 1) / s, step));
   p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);
   return p;
 }
-size_t product_workspace(int64_t M, int64_t N, int64_t K, bool forward) {
-  const int64_t s = std::max(plan_product(M, N, K, false, forward).splits, plan_product(M, N, K, true, forward).splits);
+// Room for the split sums, however the operands turn out to be aligned.
+size_t split_workspace(int64_t M, int64_t N, int64_t K, int32_t dtype, bool packed, bool forward) {
+  int64_t s = plan_product(M, N, K, dtype, true, packed, forward).splits;
+  if (!packed) s = std::max(s, plan_product(M, N, K, dtype, false, packed, forward).splits);
   return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
 }
 
@@ -896,22 +974,29 @@ bool tiled_operand(const void* p, int64_t ld, int64_t along, int size) {
   return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && along * size % 16 == 0 && ld * size < (1 << 22);
 }
 
+// One product; `packed`: the operands are as k_pack leaves them.
 template <typename T, typename O, bool A_KC, bool B_KC>
-void product(hipStream_t st, Product g, Epilogue e, float* ws) {
+void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bool packed) {
   if (g.M == 0 || g.N == 0) return;
-  bool tiled = false;
-  if constexpr (!std::is_same<T, float>::value && !std::is_same<T, e4m3_wide>::value)
-    tiled = tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
-            tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
-  const Plan p = plan_product(g.M, g.N, g.K, tiled, A_KC && B_KC);
+  const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value && !packed &&
+                       tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
+                       tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
+  const Plan p = plan_product(g.M, g.N, g.K, dtype, aligned, packed, A_KC && B_KC);
   g.k_split = p.k_split;
   e.M = g.M;
   e.N = g.N;
   e.part = p.splits > 1 ? ws : nullptr;
   const dim3 grid((unsigned)p.tiles, (unsigned)p.splits);
-  if constexpr (!std::is_same<T, float>::value && !std::is_same<T, e4m3_wide>::value) {
-    if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8><<<grid, 512, 0, st>>>(g, e);
-    if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4><<<grid, 256, 0, st>>>(g, e);
+  if constexpr (!std::is_same<T, e4m3_wide>::value) {
+    constexpr bool PARTED = std::is_same<T, float>::value;
+    using E = std::conditional_t<PARTED, bf16, T>;
+    Product t = g;
+    if (PARTED) t.K = up(g.K, 128);
+    // what is loaded along memory may run into the padding, which is there and zero
+    if (packed && !A_KC) t.M = t.lda;
+    if (packed && !B_KC) t.N = t.ldb;
+    if (p.kind == TILE256) k_tiled<E, O, A_KC, B_KC, 2, 4, 8, PARTED><<<grid, 512, 0, st>>>(t, e);
+    if (p.kind == TILE128) k_tiled<E, O, A_KC, B_KC, 2, 2, 4, PARTED><<<grid, 256, 0, st>>>(t, e);
   }
   if constexpr (A_KC && B_KC) {
     const dim3 columns((unsigned)((g.N + 15) / 16));
@@ -932,44 +1017,87 @@ void by_type(int32_t dtype, F&& f) {
   f(bf16());
 }
 
+// The forward's workspace: x and w packed, split sums.
+struct FwdPlan {
+  bool packed;
+  size_t off_x, off_w, off_split, bytes;
+};
+FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
+  FwdPlan p{};
+  const bool exact = dtype == EEC_E4M3 && out_dtype == EEC_F32;  // widened by the general kernel
+  p.packed = !exact && worth_packing(rows, outer, inner, dtype) &&
+             (dtype == EEC_F32 || inner * packed_size(dtype) % 16 != 0);
+  size_t at = 0;
+  p.off_x = at;
+  if (p.packed) at += packed_bytes(dtype, rows, inner);
+  p.off_w = at;
+  if (p.packed) at += packed_bytes(dtype, outer, inner);
+  p.off_split = at;
+  p.bytes = at + split_workspace(rows, outer, inner, dtype, p.packed, true);
+  return p;
+}
+
 constexpr int STRIP_ROWS = 4;  // rows of a strip at least, one for each wave
 int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
   const int64_t per = 64 * (dtype == EEC_F32 ? 4 : 8), wide = (cols + per - 1) / per;
-  return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 2048 / std::max<int64_t>(1, wide)));
+  return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 1024 / std::max<int64_t>(1, wide)));
 }
 
+// The backward's: gz, column sums, gz, x and w packed, split sums.
 struct BwdPlan {
-  size_t off_gz, off_part, off_split, bytes;
+  bool packed;
+  size_t off_gz, off_part, off_gzp, off_xp, off_wp, off_split, bytes;
 };
 BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
   BwdPlan p{};
+  p.packed = worth_packing(rows, inner, outer, dtype) && worth_packing(outer, inner, rows, dtype) &&
+             (dtype == EEC_F32 || outer % 8 != 0 || inner % 8 != 0);
   size_t at = 0;
   p.off_gz = at;
   if (act != EEC_ACT_NONE) at += align256((size_t)rows * (size_t)outer * (dtype == EEC_F32 ? 4 : 2));
   p.off_part = at;
   at += align256(4 * (size_t)act_grad_strips(rows, outer, dtype) * (size_t)outer);
+  p.off_gzp = at;
+  if (p.packed) at += packed_bytes(dtype, rows, outer);
+  p.off_xp = at;
+  if (p.packed) at += packed_bytes(dtype, rows, inner);
+  p.off_wp = at;
+  if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  at += std::max(product_workspace(rows, inner, outer, false), product_workspace(outer, inner, rows, false));
+  at += std::max(split_workspace(rows, inner, outer, dtype, p.packed, false),
+                 split_workspace(outer, inner, rows, dtype, p.packed, false));
   p.bytes = at;
   return p;
 }
 
 }  // namespace
 
-size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype) {
-  return product_workspace(rows, outer, inner, true);
+size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
+  return fwd_plan(rows, outer, inner, dtype, out_dtype).bytes;
 }
 
 void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) {
-  const Product g{a.x, a.w, a.ldx, a.ldw, a.rows, a.outer, a.inner, 0};
+  const FwdPlan p = fwd_plan(a.rows, a.outer, a.inner, a.dtype, a.out_dtype);
   const Epilogue e{a.bias, a.residual, a.ldr, a.x_scale, a.w_scale, a.act, a.y, a.preact, 0, 0, nullptr};
   by_type(a.out_dtype, [&](auto zero) {
     using O = decltype(zero);
     using E = std::conditional_t<std::is_same<O, float>::value, e4m3_wide, e4m3>;
+    Product g{a.x, a.w, a.ldx, a.ldw, a.rows, a.outer, a.inner, 0, 0, 0};
+    if (p.packed) {
+      const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, ws + p.off_x);
+      const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, ws + p.off_w);
+      const Packings both{{x, w, Packing{}}};
+      if (a.dtype == EEC_E4M3)
+        pack<e4m3>(st, both);
+      else
+        pack<O>(st, both);
+      g = Product{x.to, w.to, x.to_ld, w.to_ld, a.rows, a.outer, a.inner, 0, x.plane, w.plane};
+    }
+    float* split = (float*)(ws + p.off_split);
     if (a.dtype == EEC_E4M3)
-      product<E, O, true, true>(st, g, e, (float*)ws);
+      product<E, O, true, true>(st, g, e, split, a.dtype, p.packed);
     else
-      product<O, O, true, true>(st, g, e, (float*)ws);
+      product<O, O, true, true>(st, g, e, split, a.dtype, p.packed);
   });
 }
 
@@ -991,15 +1119,25 @@ void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
       k_act_grad<T><<<dim3((unsigned)((a.outer + cols - 1) / cols), (unsigned)strips), 256, 0, st>>>(q);
       if (a.gbias) launch_column_sum(st, a.dtype, (const float*)(ws + p.off_part), (int)strips, a.outer, a.gbias);
     }
+    Product gx{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0, 0, 0};
+    Product gw{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0, 0, 0};
+    if (p.packed && products) {
+      const Packing z = packing(a.dtype, gz, ldgz, a.rows, a.outer, ws + p.off_gzp);
+      const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, a.gw ? ws + p.off_xp : nullptr);
+      const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, a.gx ? ws + p.off_wp : nullptr);
+      pack<T>(st, Packings{{z, x, w}});
+      gx = Product{z.to, w.to, z.to_ld, w.to_ld, a.rows, a.inner, a.outer, 0, z.plane, w.plane};
+      gw = Product{z.to, x.to, z.to_ld, x.to_ld, a.outer, a.inner, a.rows, 0, z.plane, x.plane};
+    }
     float* split = (float*)(ws + p.off_split);
     Epilogue e{};
     if (a.gx) {
       e.y = a.gx;
-      product<T, T, true, false>(st, Product{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0}, e, split);
+      product<T, T, true, false>(st, gx, e, split, a.dtype, p.packed);
     }
     if (a.gw) {
       e.y = a.gw;
-      product<T, T, false, false>(st, Product{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0}, e, split);
+      product<T, T, false, false>(st, gw, e, split, a.dtype, p.packed);
     }
   });
 }

@@ -46,7 +46,7 @@ __device__ __forceinline__ void load_raw(const T* __restrict__ p, int64_t valid,
     __builtin_memcpy(v, p, sizeof(v));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = i < valid ? p[i] : T(0);
+    for (int i = 0; i < N; ++i) v[i] = i < valid ? p[i] : T{};
   }
 }
 

@@ -187,7 +187,7 @@ struct LinearArgs {
   int32_t dtype, out_dtype, act;
   void *y, *preact;
 };
-size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
+size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype);
 void launch_linear(hipStream_t s, const LinearArgs& a, char* ws);
 struct LinearBwdArgs {
   int64_t rows, outer, inner;

@@ -315,22 +315,30 @@ __global__ void __launch_bounds__(1024) k_norm_bwd_wide(NormBwd a) {
   }
 }
 
-// Column sums of the partial rows [parts][n], in row order: 64 columns per
-// workgroup, its waves dealing the rows in turn and joined in wave order.
+// Column sums of the partial rows [parts][n]: 64 columns per workgroup, whose 16
+// waves deal the rows in turn, eight of them on their way at a time (one by one
+// each would wait for memory), and are joined in wave order.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_column_sum(const float* __restrict__ part, int parts, int64_t n,
                                                      T* __restrict__ out) {
-  __shared__ float join[16][64];
+  constexpr int WAVES = 16, TOGETHER = 8;
+  __shared__ float join[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + lane;
   float v = 0.f;
   if (col < n)
-    for (int p = wave; p < parts; p += 16) v += part[(int64_t)p * n + col];
+    for (int p = wave; p < parts; p += WAVES * TOGETHER) {
+      float t[TOGETHER];
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) t[i] = p + WAVES * i < parts ? part[(int64_t)(p + WAVES * i) * n + col] : 0.f;
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) v += t[i];
+    }
   join[wave][lane] = v;
   __syncthreads();
   if (wave == 0 && col < n) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) v += join[i][lane];
+    for (int i = 1; i < WAVES; ++i) v += join[i][lane];
     out[col] = (T)v;
   }
 }

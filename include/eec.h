@@ -448,10 +448,10 @@ EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t w
  *   x_scale [rows], w_scale [outer] float32: EEC_E4M3 only, and required there
  *   y       [rows][outer] out_dtype
  *   preact  [rows][outer] z in out_dtype, or NULL (what the backward reads)
- *   workspace >= eec_linear_workspace_bytes(rows, outer, inner, dtype); may be
- *   NULL where that is 0
+ *   workspace >= eec_linear_workspace_bytes(rows, outer, inner, dtype, out_dtype);
+ *   may be NULL where that is 0
  * float32 operands keep float32's accuracy on the bf16 matrix cores: each is
- * the sum of three bf16 parts (exact above 2^-109, to within 2^-133 below), and
+ * the sum of three bf16 parts (exact above 2^-100, to within 2^-131 below), and
  * the six part products down to 2^-16 of the largest are taken.  e4m3 products
  * with a 16-bit output are summed by the 8-bit matrix instructions, whose sums
  * are good to about 1e-5 of sum |x||w|; with a float32 output, in float32. */
@@ -459,7 +459,8 @@ EEC_API eec_status eec_linear(void *stream, int64_t rows, int64_t outer, int64_t
                       int32_t out_dtype, const void *x, int64_t ldx, const float *x_scale, const void *w,
                       int64_t ldw, const float *w_scale, const void *bias, const void *residual, int64_t ldr,
                       int32_t act, void *y, void *preact, void *workspace, size_t workspace_bytes);
-EEC_API size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
+EEC_API size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                                          int32_t out_dtype);
 
 /* eec_linear_backward -- with gz = gy act'(preact), rounded once to dtype for
  * the products (EEC_ACT_NONE: gz = gy):

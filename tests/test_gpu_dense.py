@@ -194,6 +194,38 @@ def test_linear_and_backward(rows, inner, outer, dt):
                (2 * rows + 32) * EPS * az.sum(axis=0) + U[dt] * np.abs(ref["gbias"]) + TINY[dt], f"{act} gbias")
 
 
+PACKED_SHAPES = [(640, 1100, 601), (700, 901, 777), (1031, 640, 643), (517, 1543, 521)]
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", PACKED_SHAPES)
+def test_linear_and_backward_packed(rows, inner, outer, dt):
+    """Sizes whose operands are packed first (float32 into its parts, odd rows to aligned ones)."""
+    test_linear_and_backward(rows, inner, outer, dt)
+
+
+def test_linear_packed_special_values():
+    """An infinity or NaN in a packed float32 product reaches its own row alone, also beside values whose parts are zero."""
+    rows, inner, outer = 640, 1100, 601
+    x = torch.full((rows, inner), 2.0, device=DEV)
+    w = torch.full((outer, inner), 0.5, device=DEV)
+    w[3] = -0.5
+    x[1, 5], x[2, 7], x[4, 9] = float("inf"), float("nan"), -float("inf")
+    x[4, 10], w[5, 9] = float("inf"), 0.0
+    y = np_(B.linear(x, w)["y"])
+    assert np.all(np.isposinf(np.delete(y[1], 3))) and np.isneginf(y[1, 3])
+    assert np.all(np.isnan(y[2])) and np.all(np.isnan(np.delete(y[4], 5))) and np.isnan(y[4, 5])
+    rest = np.delete(y, (1, 2, 4), axis=0)
+    ref = np.full(outer, float(inner))
+    ref[3], ref[5] = -inner, inner - 1
+    np.testing.assert_allclose(rest, np.broadcast_to(ref, rest.shape), rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("rows,inner,outer", [(640, 1100, 601), (517, 1543, 521), (300, 4097, 1000)])
+def test_linear_e4m3_packed(rows, inner, outer):
+    test_linear_e4m3(rows, inner, outer, torch.bfloat16)
+
+
 @pytest.mark.parametrize("ot", TYPES, ids=ids)
 @pytest.mark.parametrize("rows,inner,outer", [(1, 64, 64), (3, 16, 5), (17, 1000, 65), (129, 257, 130), (300, 4096, 40),
                                               (256, 512, 512), (1, 4096, 1024), (40, 130, 300), (0, 8, 8), (4, 0, 4)])
