@@ -625,15 +625,18 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// BM x BN of C per workgroup of WM x WN waves, MI * 16 x 64 of it per wave.  Four
+// BM x BN of C per workgroup of WM x WN waves, MI * 16 x 64 of it per wave.  BUFS
 // LDS buffers: at the barrier before a tile the next one is there, to be read ahead
-// from, the one after is on its way, and a third is started into the buffer that
-// everybody left at that barrier.
+// from, BUFS - 3 more are on their way, and another is started into the buffer that
+// everybody left at that barrier.  A load takes about 1900 cycles, a tile's products
+// 1030 at 256 x 256, where two on their way do, and 258 at 128 x 128, where it takes
+// six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, XXX with
+// eight).
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
 // PARTED: float32 operands as planes of bf16 parts (k_pack, k in whole groups of
 // four tiles, zeros past the end).  The six part products are six runs through k,
 // in rising size, of the one bf16 kernel.
-template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, bool PARTED>
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS, bool PARTED>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
@@ -643,8 +646,10 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   constexpr int BK = TA::BK, LOADS = TA::LOADS + TB::LOADS;
   // The buffers are variables of their own: the compiler then sees that loads into
   // one do not touch the others, and does not wait for them before it reads.
+  constexpr int A2 = BUFS == 8 ? TA::BYTES : 16, B2 = BUFS == 8 ? TB::BYTES : 16;
   __shared__ __attribute__((aligned(1024))) char a0[TA::BYTES], a1[TA::BYTES], a2[TA::BYTES], a3[TA::BYTES];
   __shared__ __attribute__((aligned(1024))) char b0[TB::BYTES], b1[TB::BYTES], b2[TB::BYTES], b3[TB::BYTES];
+  __shared__ __attribute__((aligned(16))) char a4[A2], a5[A2], a6[A2], a7[A2], b4[B2], b5[B2], b6[B2], b7[B2];
   const int lane = threadIdx.x & 63, wave = wave_id();
   int64_t m0, n0;
   tile_of((e.M + BM - 1) / BM, (e.N + BN - 1) / BN, m0, n0);
@@ -659,39 +664,63 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   TB tb;
   ta.init(g.a, g.lda, m0, g.M, kb, ke, g.a_plane);
   tb.init(g.b, g.ldb, n0, g.N, kb, ke, g.b_plane);
-  ta.template load<!PARTED>(a0, ke - kb);
-  tb.template load<!PARTED>(b0, ke - kb);
-  ta.template load<!PARTED>(a1, ke - kb - BK);
-  tb.template load<!PARTED>(b1, ke - kb - BK);
-  ta.template load<!PARTED>(a2, ke - kb - 2 * BK);
-  tb.template load<!PARTED>(b2, ke - kb - 2 * BK);
-  tile_barrier<2 * LOADS>();
-  read_ahead<S, TA, TB>(f0, a0, b0, wm, wn);
   int64_t k = kb;
-#define EEC_TILE(TAIL, T, F, A, NEXT, NA, NB, FREE_A, FREE_B)   \
-  tile_barrier<LOADS>();                                        \
-  ta.template load<TAIL>(FREE_A, ke - k - (T + 3) * BK);        \
-  tb.template load<TAIL>(FREE_B, ke - k - (T + 3) * BK);        \
+#define EEC_LOAD(TAIL, T, A, B)                   \
+  ta.template load<TAIL>(A, ke - k - (T) * BK);   \
+  tb.template load<TAIL>(B, ke - k - (T) * BK)
+#define EEC_TILE(TAIL, T, F, A, NEXT, NA, NB, FREE_A, FREE_B) \
+  tile_barrier<(BUFS - 3) * LOADS>();                         \
+  EEC_LOAD(TAIL, T + BUFS - 1, FREE_A, FREE_B);               \
   multiply<S, TA, TB>(c, F, A, wm, NEXT, NA, NB, wn)
-#define EEC_FOUR_TILES(TAIL)                       \
+#define EEC_FOUR(TAIL)                             \
   EEC_TILE(TAIL, 0, f0, a0, f1, a1, b1, a3, b3);   \
   EEC_TILE(TAIL, 1, f1, a1, f0, a2, b2, a0, b0);   \
   EEC_TILE(TAIL, 2, f0, a2, f1, a3, b3, a1, b1);   \
   EEC_TILE(TAIL, 3, f1, a3, f0, a0, b0, a2, b2)
-  if constexpr (PARTED) {
-    for (int64_t end = kb + (ke - kb) * TA::RUNS; k < end; k += 4 * BK) {
-      EEC_FOUR_TILES(false);
-    }
-  } else {
-    for (; k + 7 * BK <= ke; k += 4 * BK) {  // every tile it loads is whole
-      EEC_FOUR_TILES(false);
-    }
-    for (; k < ke; k += 4 * BK) {  // tiles past the end are zeros, read from nowhere
-      EEC_FOUR_TILES(true);
+#define EEC_EIGHT(TAIL)                            \
+  EEC_TILE(TAIL, 0, f0, a0, f1, a1, b1, a7, b7);   \
+  EEC_TILE(TAIL, 1, f1, a1, f0, a2, b2, a0, b0);   \
+  EEC_TILE(TAIL, 2, f0, a2, f1, a3, b3, a1, b1);   \
+  EEC_TILE(TAIL, 3, f1, a3, f0, a4, b4, a2, b2);   \
+  EEC_TILE(TAIL, 4, f0, a4, f1, a5, b5, a3, b3);   \
+  EEC_TILE(TAIL, 5, f1, a5, f0, a6, b6, a4, b4);   \
+  EEC_TILE(TAIL, 6, f0, a6, f1, a7, b7, a5, b5);   \
+  EEC_TILE(TAIL, 7, f1, a7, f0, a0, b0, a6, b6)
+  EEC_LOAD(!PARTED, 0, a0, b0);
+  EEC_LOAD(!PARTED, 1, a1, b1);
+  EEC_LOAD(!PARTED, 2, a2, b2);
+  if constexpr (BUFS == 8) {
+    EEC_LOAD(!PARTED, 3, a3, b3);
+    EEC_LOAD(!PARTED, 4, a4, b4);
+    EEC_LOAD(!PARTED, 5, a5, b5);
+    EEC_LOAD(!PARTED, 6, a6, b6);
+  }
+  tile_barrier<(BUFS - 2) * LOADS>();
+  read_ahead<S, TA, TB>(f0, a0, b0, wm, wn);
+  // Whole groups of tiles; with PARTED every tile is whole, otherwise those past the
+  // end are zeros, read from nowhere.
+  const int64_t whole = PARTED ? kb + (ke - kb) * TA::RUNS : ke - (2 * BUFS - 1) * BK + 1;
+  const int64_t end = PARTED ? whole : ke;
+  for (; k < whole; k += BUFS * BK) {
+    if constexpr (BUFS == 8) {
+      EEC_EIGHT(false);
+    } else {
+      EEC_FOUR(false);
     }
   }
-#undef EEC_FOUR_TILES
+  if constexpr (!PARTED) {
+    for (; k < end; k += BUFS * BK) {
+      if constexpr (BUFS == 8) {
+        EEC_EIGHT(true);
+      } else {
+        EEC_FOUR(true);
+      }
+    }
+  }
+#undef EEC_EIGHT
+#undef EEC_FOUR
 #undef EEC_TILE
+#undef EEC_LOAD
   tile_barrier<0>();  // nobody's loads or reads are left in the buffers
   // 32 rows of a wave in 8 KB: two waves to an operand's buffer
   static_assert(TA::BYTES * 4 >= WAVES * 8192, "room for 8 KB a wave");
@@ -953,7 +982,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool aligned, 
   p.kind = !(aligned || packed) ? GENERAL : t256 >= 192 ? TILE256 : TILE128;
   p.tiles = p.kind == TILE256 ? t256 : tiles_of(M, N, 128);
   const int64_t step = 128;  // k of a split is a multiple of every kernel's tiles
-  int64_t s = std::min<int64_t>((p.kind == TILE256 ? 256 : 512) / std::max<int64_t>(1, p.tiles),
+  int64_t s = std::min<int64_t>((p.kind == GENERAL ? 512 : 256) / std::max<int64_t>(1, p.tiles),
                                 K / (p.kind == GENERAL ? 128 : 256));
   s = std::max<int64_t>(1, s);
   p.k_split = std::max<int64_t>(step, up((K + s - 1) / s, step));
@@ -995,8 +1024,8 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
     // what is loaded along memory may run into the padding, which is there and zero
     if (packed && !A_KC) t.M = t.lda;
     if (packed && !B_KC) t.N = t.ldb;
-    if (p.kind == TILE256) k_tiled<E, O, A_KC, B_KC, 2, 4, 8, PARTED><<<grid, 512, 0, st>>>(t, e);
-    if (p.kind == TILE128) k_tiled<E, O, A_KC, B_KC, 2, 2, 4, PARTED><<<grid, 256, 0, st>>>(t, e);
+    if (p.kind == TILE256) k_tiled<E, O, A_KC, B_KC, 2, 4, 8, 4, PARTED><<<grid, 512, 0, st>>>(t, e);
+    if (p.kind == TILE128) k_tiled<E, O, A_KC, B_KC, 2, 2, 4, 8, PARTED><<<grid, 256, 0, st>>>(t, e);
   }
   if constexpr (A_KC && B_KC) {
     const dim3 columns((unsigned)((g.N + 15) / 16));
