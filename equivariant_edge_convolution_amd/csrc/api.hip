@@ -612,8 +612,8 @@ static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
   if (bad_size(rows) || bad_size(outer) || bad_size(inner)) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
   // output tiles of one product, counted as the kernels launch them
   const int64_t r = rows / 128 + 1, o = outer / 128 + 1, i = inner / 128 + 1;
-  if (r * o >= (1 << 23) || r * i >= (1 << 23) || o * i >= (1 << 23))
-    return fail(EEC_ERR_SHAPE, "a product of more than 2^37 outputs");
+  if (r * o >= (1 << 22) || r * i >= (1 << 22) || o * i >= (1 << 22))
+    return fail(EEC_ERR_SHAPE, "a product of more than 2^36 outputs");
   return EEC_OK;
 }
 

@@ -64,7 +64,7 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
     for (int i = 0; i < L; ++i) v[i] += c.bias[i];
   }
   if (e.preact) store_run((O*)e.preact + m * e.N + c.n, c.left, v);
-  act_values(v, e.act);
+  act_values<O>(v, e.act);
   if (e.residual) {
 #pragma unroll
     for (int i = 0; i < L; ++i) v[i] += (float)r.v[i];
@@ -267,7 +267,7 @@ struct Product {
   int64_t a_plane, b_plane;  // bytes between an operand's parts (float32 in planes)
 };
 
-constexpr int GBM = 128, GBN = 128, GBK = 32;
+constexpr int GBK = 32;  // k of a step of the general kernel
 
 // Tile of a workgroup.  Workgroups go to the 8 XCDs in turn, each with an L2 of
 // its own: an XCD takes a contiguous share of the tiles, in strips of 8 tiles of m
@@ -281,81 +281,72 @@ __device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_
   tn = in / high;
 }
 
-// A tile of 128 lines x 32 k of one operand, two 8-element chunks per thread.
-// KC: k runs along memory (a chunk is one run), otherwise the lines do (a chunk
-// is 8 runs of 2 lines).
-template <typename T, bool KC>
+// A tile of LINES lines x 32 k of one operand, an 8-element chunk per thread (two
+// with 128 lines).  KC: k runs along memory (a chunk is one run), otherwise the
+// lines do (a chunk is 8 runs of R lines).
+template <typename T, bool KC, int LINES>
 struct Stage {
+  static constexpr int R = LINES / 64;
   static constexpr int ROW = GBK * sizeof(typename Mat<T>::E) + 8 * sizeof(typename Mat<T>::E);
-  static constexpr int PLANE = GBM * ROW;
-  Raw<T> r[2];
+  static constexpr int PLANE = LINES * ROW;
+  Raw<T> r[R];
 
   __device__ __forceinline__ void load(const T* __restrict__ p, int64_t ld, int64_t line0, int64_t lines, int64_t k0,
                                        int64_t k_end) {
     if constexpr (KC) {
       const int64_t k = k0 + (threadIdx.x & 3) * 8, left = k_end - k;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < R; ++i) {
         const int64_t line = min(line0 + (threadIdx.x >> 2) + 64 * i, lines - 1);  // lines past the end: not stored
-        const T* s = p + line * ld + k;
-        if (left >= 8) {
-          __builtin_memcpy(&r[i], s, sizeof(r[i]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) r[i].v[j] = j < left ? s[j] : T{};
-        }
+        load_raw(p + line * ld + k, left, r[i].v);
       }
     } else {
-      const int64_t line = line0 + (threadIdx.x & 63) * 2;
+      const int64_t line = line0 + (threadIdx.x & 63) * R;
       const int64_t k = k0 + (threadIdx.x >> 6) * 8;
       const T* s = p + k * ld + line;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        T two[2] = {};
-        if (k + j < k_end) {
-          if (line + 2 <= lines)
-            __builtin_memcpy(two, s + j * ld, sizeof(two));
-          else if (line < lines)
-            two[0] = s[j * ld];
-        }
-        r[0].v[j] = two[0];
-        r[1].v[j] = two[1];
+        T some[R];
+        load_raw(s + j * ld, k + j < k_end ? lines - line : 0, some);
+#pragma unroll
+        for (int i = 0; i < R; ++i) r[i].v[j] = some[i];
       }
     }
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int line = KC ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x & 63) * 2 + i;
+    for (int i = 0; i < R; ++i) {
+      const int line = KC ? (threadIdx.x >> 2) + 64 * i : (threadIdx.x & 63) * R + i;
       const int kc = KC ? threadIdx.x & 3 : threadIdx.x >> 6;
       put_chunk<T>(lds + line * ROW + kc * 8 * sizeof(typename Mat<T>::E), PLANE, r[i]);
     }
   }
 };
 
-// 128 x 128 of C per workgroup, 64 x 64 per wave, any size, stride and alignment.
+// Any size, stride and alignment: WM x WN waves with MI * 16 x 64 of C each.
 // Operands pass through registers (where float32 is split into its parts and
 // k-major ones are turned) into LDS rows of 32 k; the next tile's loads are in
-// flight while the present one is multiplied.  B is the first factor of the
-// matrix instruction, so a lane holds one row of C and, by the column order in
-// LDS, 16 adjacent columns.
-template <typename T, typename O, bool A_KC, bool B_KC>
+// flight while the present one is multiplied.  B is the first factor of the matrix
+// instruction, so a lane holds four adjacent columns of one row of C.
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
 __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
+  static_assert(WM * WN == 4, "four waves");
+  constexpr int BM = WM * MI * 16, BN = WN * 64;
   using M_ = Mat<T>;
   constexpr int P = M_::PLANES;
-  using SA = Stage<T, A_KC>;
-  using SB = Stage<T, B_KC>;
+  using SA = Stage<T, A_KC, BM>;
+  using SB = Stage<T, B_KC, BN>;
   constexpr int TILES = P * (SA::PLANE + SB::PLANE), SUMS = 4 * 4096;  // 4 KB of each wave for a matrix tile's sums
   __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
   char* lds_b = lds + P * SA::PLANE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t m0, n0;
-  tile_of((g.M + GBM - 1) / GBM, (g.N + GBN - 1) / GBN, m0, n0);
-  m0 *= GBM;
-  n0 *= GBN;
+  tile_of((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, m0, n0);
+  m0 *= BM;
+  n0 *= BN;
   const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-  f32x4 acc[4][4] = {};
+  const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
+  f32x4 acc[MI][4] = {};
   SA sa;
   SB sb;
   if (kb < ke) {
@@ -371,10 +362,10 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
       sa.load((const T*)g.a, g.lda, m0, g.M, k + GBK, ke);
       sb.load((const T*)g.b, g.ldb, n0, g.N, k + GBK, ke);
     }
-    typename M_::Frag fa[4][P], fb[P];
+    typename M_::Frag fa[MI][P], fb[P];
     const int at = (lane & 15) * SA::ROW + (lane >> 4) * 8 * (int)sizeof(typename M_::E);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int p = 0; p < P; ++p)
         __builtin_memcpy(&fa[i][p], __builtin_assume_aligned(lds + p * SA::PLANE + (wm + 16 * i) * SA::ROW + at, 8),
@@ -386,12 +377,12 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
         __builtin_memcpy(&fb[p], __builtin_assume_aligned(lds_b + p * SB::PLANE + (wn + 16 * j) * SB::ROW + at, 8),
                          sizeof(fb[p]));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i][j] = M_::mul(fb, fa[i], acc[i][j]);
+      for (int i = 0; i < MI; ++i) acc[i][j] = M_::mul(fb, fa[i], acc[i][j]);
     }
   }
   __syncthreads();
-  constexpr int PER = sizeof(lds) >= 2 * SUMS ? 2 : 1;
-  finish_wave<O, 4, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, [&](int i, char* rows) {
+  constexpr int PER = MI > 1 && sizeof(lds) >= 2 * SUMS ? 2 : 1;
+  finish_wave<O, MI, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, [&](int i, char* rows) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
   });
@@ -630,7 +621,7 @@ __device__ __forceinline__ void tile_barrier() {
 // from, BUFS - 3 more are on their way, and another is started into the buffer that
 // everybody left at that barrier.  A load takes about 1900 cycles, a tile's products
 // 1030 at 256 x 256, where two on their way do, and 258 at 128 x 128, where it takes
-// six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, XXX with
+// six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, 43 with
 // eight).
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
 // PARTED: float32 operands as planes of bf16 parts (k_pack, k in whole groups of
@@ -858,7 +849,7 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
     load_run((const T*)a.gy + r * a.ldgy + col, left, g);
     if (a.act != EEC_ACT_NONE) {
       load_run((const T*)a.preact + r * a.cols + col, left, z);
-      act_slopes(g, z, a.act);
+      act_slopes<T>(g, z, a.act);
     }
     if (a.gz) store_run((T*)a.gz + r * a.cols + col, left, g);
 #pragma unroll
@@ -943,7 +934,7 @@ void pack(hipStream_t st, const Packings& all) {
 
 // ------------------------------------------------------------------ plans
 
-enum Kind { GENERAL, TILE128, TILE256, FEW };
+enum Kind { SMALL, GENERAL, TILE128, TILE256, FEW };  // SMALL: the general kernel in 64 x 64 tiles
 struct Plan {
   Kind kind;
   bool packed;  // operands through k_pack
@@ -967,32 +958,35 @@ bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype) {
   return (double)M * N >= least * (M + N) && (double)M * N * K >= 4e8;
 }
 
-// How a product is run: a rule on sizes, type and (aligned) whether the operands
-// take the tiled kernel as they are.  k is split where the tiles alone leave most of
-// the 256 CUs idle, into at least 128 (tiled: 256) k each.
-Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool aligned, bool packed, bool forward) {
+// How a product is run: a rule on sizes and on whether the operands take the tiled
+// kernel (aligned, or packed).  k is split where the tiles alone leave most of the
+// 256 CUs idle: joining the sums costs about 5 us, in which a 128 x 128 tile gets
+// through 1200 k and the general kernel, which waits for memory at every step,
+// through some 200.
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool packed, bool forward) {
   Plan p{};
   if (forward && M <= FEW_ROWS) {
     p.kind = FEW;
     p.splits = 1;
     return p;
   }
-  const int64_t t256 = tiles_of(M, N, 256);
+  const int64_t t256 = tiles_of(M, N, 256), t128 = tiles_of(M, N, 128);
   p.packed = packed;
-  p.kind = !(aligned || packed) ? GENERAL : t256 >= 192 ? TILE256 : TILE128;
-  p.tiles = p.kind == TILE256 ? t256 : tiles_of(M, N, 128);
+  p.kind = tiled || packed ? (t256 >= 192 ? TILE256 : TILE128) : t128 >= 256 ? GENERAL : SMALL;
+  p.tiles = p.kind == TILE256 ? t256 : p.kind == SMALL ? tiles_of(M, N, 64) : t128;
+  const bool general = p.kind == GENERAL || p.kind == SMALL;
   const int64_t step = 128;  // k of a split is a multiple of every kernel's tiles
-  int64_t s = std::min<int64_t>((p.kind == GENERAL ? 512 : 256) / std::max<int64_t>(1, p.tiles),
-                                K / (p.kind == GENERAL ? 128 : 256));
+  int64_t s = K < (general ? 512 : 2048) ? 1 : std::min<int64_t>((general ? 512 : 256) / p.tiles, K / (general ? 128 : 512));
   s = std::max<int64_t>(1, s);
   p.k_split = std::max<int64_t>(step, up((K + s - 1) / s, step));
   p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);
   return p;
 }
 // Room for the split sums, however the operands turn out to be aligned.
-size_t split_workspace(int64_t M, int64_t N, int64_t K, int32_t dtype, bool packed, bool forward) {
-  int64_t s = plan_product(M, N, K, dtype, true, packed, forward).splits;
-  if (!packed) s = std::max(s, plan_product(M, N, K, dtype, false, packed, forward).splits);
+size_t split_workspace(int64_t M, int64_t N, int64_t K, bool packed, bool forward) {
+  if (M == 0 || N == 0) return 0;
+  int64_t s = plan_product(M, N, K, true, packed, forward).splits;
+  if (!packed) s = std::max(s, plan_product(M, N, K, false, packed, forward).splits);
   return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
 }
 
@@ -1010,7 +1004,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value && !packed &&
                        tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
                        tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
-  const Plan p = plan_product(g.M, g.N, g.K, dtype, aligned, packed, A_KC && B_KC);
+  const Plan p = plan_product(g.M, g.N, g.K, aligned, packed, A_KC && B_KC);
   g.k_split = p.k_split;
   e.M = g.M;
   e.N = g.N;
@@ -1032,7 +1026,8 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
     if (p.kind == FEW && g.M <= 16) k_few<T, O, 1><<<columns, 512, 0, st>>>(g, e);
     if (p.kind == FEW && g.M > 16) k_few<T, O, 2><<<columns, 512, 0, st>>>(g, e);
   }
-  if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC><<<grid, 256, 0, st>>>(g, e);
+  if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC, 2, 2, 4><<<grid, 256, 0, st>>>(g, e);
+  if (p.kind == SMALL) k_product<T, O, A_KC, B_KC, 4, 1, 1><<<grid, 256, 0, st>>>(g, e);
   if (p.splits > 1) {
     const int64_t runs = g.M * ((g.N + 3) / 4);
     k_join_splits<O><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)p.splits);
@@ -1062,7 +1057,7 @@ FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_w = at;
   if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  p.bytes = at + split_workspace(rows, outer, inner, dtype, p.packed, true);
+  p.bytes = at + split_workspace(rows, outer, inner, p.packed, true);
   return p;
 }
 
@@ -1093,8 +1088,8 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_wp = at;
   if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  at += std::max(split_workspace(rows, inner, outer, dtype, p.packed, false),
-                 split_workspace(outer, inner, rows, dtype, p.packed, false));
+  at += std::max(split_workspace(rows, inner, outer, p.packed, false),
+                 split_workspace(outer, inner, rows, p.packed, false));
   p.bytes = at;
   return p;
 }

@@ -91,22 +91,37 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
 
-// act in place; the branch is uniform over the launch and taken once per run.
-template <int N>
+// erf(x) to 1.5e-7 (the rational times a Gaussian of Abramowitz and Stegun, 7.1.26):
+// enough beside a 16-bit output, and a third of erff's work.
+__device__ __forceinline__ float erf_short(float x) {
+  const float a = fabsf(x), t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * a);
+  const float p = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+  return copysignf(1.f - p * __builtin_amdgcn_exp2f(a * a * -1.44269504088896341f), x);
+}
+template <typename O>
+__device__ __forceinline__ float erf_of(float x) {
+  if constexpr (sizeof(O) == 4)
+    return erff(x);
+  else
+    return erf_short(x);
+}
+
+// act in place, for an output of type O; the branch is uniform over the launch and taken once per run.
+template <typename O, int N>
 __device__ __forceinline__ void act_values(float (&z)[N], int act) {
   if (act == EEC_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] *= sigmoid(z[i]);
   } else if (act == EEC_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.f + erff(z[i] * 0.70710678118654752f));
+    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.f + erf_of<O>(z[i] * 0.70710678118654752f));
   } else if (act == EEC_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];  // a NaN stays one
   }
 }
 // g act'(z) in place of g.
-template <int N>
+template <typename O, int N>
 __device__ __forceinline__ void act_slopes(float (&g)[N], const float (&z)[N], int act) {
   if (act == EEC_ACT_SILU) {
 #pragma unroll
@@ -117,8 +132,8 @@ __device__ __forceinline__ void act_slopes(float (&g)[N], const float (&z)[N], i
   } else if (act == EEC_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      g[i] *= 0.5f * (1.f + erff(z[i] * 0.70710678118654752f)) +
-              z[i] * expf(-0.5f * z[i] * z[i]) * 0.39894228040143268f;
+      g[i] *= 0.5f * (1.f + erf_of<O>(z[i] * 0.70710678118654752f)) +
+              z[i] * __builtin_amdgcn_exp2f(z[i] * z[i] * -0.72134752044448170f) * 0.39894228040143268f;
   } else if (act == EEC_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) g[i] *= z[i] > 0.f ? 1.f : 0.f;
