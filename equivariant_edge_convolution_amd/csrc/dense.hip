@@ -79,12 +79,12 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
 // fits the instruction cache (8192 x 8192 x 32 bf16: 64 us, this 46 us).
 // Up to four rows' residuals a lane are on their way together.
 template <typename O, int ROWS>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, int64_t m0, int64_t n0) {
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, int64_t m0, int64_t n0, int split) {
   constexpr int L = 16 / (int)sizeof(O), PER = L;              // columns of a lane, rows of one access
   constexpr int TOGETHER = ROWS / PER < 4 ? ROWS / PER : 4;
   static_assert(ROWS % (TOGETHER * PER) == 0, "whole accesses");
   const int lane = threadIdx.x & 63;
-  float* part = e.part ? e.part + (int64_t)blockIdx.y * e.M * e.N : nullptr;
+  float* part = e.part ? e.part + split * e.M * e.N : nullptr;
   const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
   Columns<O, L> c;
   c.load(e, n0 + col);
@@ -110,14 +110,14 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, 
 // All of a wave's GROUPS matrix tiles of HIGH rows, PER of them at a time through
 // its own LDS; put(i, chunk(c)) writes the c-th four adjacent columns of tile i.
 template <typename O, int GROUPS, int HIGH, int PER, typename Put>
-__device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, Put put) {
+__device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split, Put put) {
 #pragma unroll 1
   for (int g = 0; g < GROUPS; g += PER) {
 #pragma unroll
     for (int i = 0; i < GROUPS; ++i)
       if (i / PER * PER == g) put(i, lds + i % PER * HIGH * 256);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    finish_rows<O, PER * HIGH>(e, lds, m0 + g * HIGH, n0);
+    finish_rows<O, PER * HIGH>(e, lds, m0 + g * HIGH, n0, split);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
@@ -269,16 +269,25 @@ struct Product {
 
 constexpr int GBK = 32;  // k of a step of the general kernel
 
-// Tile of a workgroup.  Workgroups go to the 8 XCDs in turn, each with an L2 of
-// its own: an XCD takes a contiguous share of the tiles, in strips of 8 tiles of m
-// that run along n, so that what its CUs hold at one time reuses few rows of A and B.
-__device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
-  const uint32_t total = (uint32_t)(tiles_m * tiles_n), b = blockIdx.x, xcd = b & 7;
-  const uint32_t t = xcd * (total >> 3) + min(xcd, total & 7) + (b >> 3);
-  const uint32_t strip = t / (8 * (uint32_t)tiles_n), first = strip * 8;
-  const uint32_t high = min(8u, (uint32_t)tiles_m - first), in = t - first * (uint32_t)tiles_n;
-  tm = first + in % high;
-  tn = in / high;
+// Tile and split of k of a workgroup.  Workgroups go to the 8 XCDs in turn, each
+// with an L2 of its own: an XCD takes a contiguous share of the work, split after
+// split (the tiles of a split read the same k), each in strips of 8 tiles of m that
+// run along n, so that what its CUs hold at one time reuses few rows of A and B.
+// (32768 x 512 x 512 gw in float32, 16 splits of 16 tiles: 190 us with a split's
+// tiles dealt over all XCDs, XXX so.)
+struct Place {
+  int64_t m, n;
+  int split;
+};
+template <int BM, int BN>
+__device__ __forceinline__ Place place_of(int64_t M, int64_t N) {
+  const uint32_t tiles_m = (uint32_t)((M + BM - 1) / BM), tiles_n = (uint32_t)((N + BN - 1) / BN);
+  const uint32_t total = gridDim.x, b = blockIdx.x, xcd = b & 7;
+  const uint32_t all = xcd * (total >> 3) + min(xcd, total & 7) + (b >> 3);
+  const uint32_t split = all / (tiles_m * tiles_n), t = all - split * tiles_m * tiles_n;
+  const uint32_t first = t / (8 * tiles_n) * 8, in = t - first * tiles_n;
+  const uint32_t high = min(8u, tiles_m - first);
+  return Place{(int64_t)(first + in % high) * BM, (int64_t)(in / high) * BN, (int)split};
 }
 
 // A tile of LINES lines x 32 k of one operand, an 8-element chunk per thread (two
@@ -340,11 +349,9 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
   char* lds_b = lds + P * SA::PLANE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t m0, n0;
-  tile_of((g.M + BM - 1) / BM, (g.N + BN - 1) / BN, m0, n0);
-  m0 *= BM;
-  n0 *= BN;
-  const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
+  const Place place = place_of<BM, BN>(e.M, e.N);
+  const int64_t m0 = place.m, n0 = place.n;
+  const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
   f32x4 acc[MI][4] = {};
   SA sa;
@@ -382,7 +389,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   }
   __syncthreads();
   constexpr int PER = MI > 1 && sizeof(lds) >= 2 * SUMS ? 2 : 1;
-  finish_wave<O, MI, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, [&](int i, char* rows) {
+  finish_wave<O, MI, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
   });
@@ -469,19 +476,16 @@ struct Tile {
       }
     }
   }
-  // Loads the next tile; with TAIL only `left` of its k exist (none, perhaps).
-  template <bool TAIL>
-  __device__ __forceinline__ void load(char* lds, int64_t left) {
-    const int size = PARTS != 0 && run >= RUNS ? 0 : 0x7fffffff;  // after the last run, nothing: reads as zero
+  // Loads the next tile, of which `left` k exist (none, perhaps): what lies past the
+  // end reads as zero.
+  __device__ __forceinline__ void load(char* lds, int left) {
+    const int size = PARTS != 0 && run >= RUNS ? 0 : 0x7fffffff;  // after the last run, nothing
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, size, 0x00020000);
-    if constexpr (TAIL) {  // what lies past the end reads as zero from here on
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) off[i] = at_k(i) < left ? off[i] : NOWHERE;
-    }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void*)(lds + place(i) * STRIDE), 16, off[i], 0, 0, 0);
+          rsrc, (__attribute__((address_space(3))) void*)(lds + place(i) * STRIDE), 16,
+          PARTS != 0 || at_k(i) < left ? off[i] : NOWHERE, 0, 0, 0);
     base += step;
     if constexpr (PARTS != 0) {
       const bool last = ++tile == tiles;
@@ -642,11 +646,9 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   __shared__ __attribute__((aligned(1024))) char b0[TB::BYTES], b1[TB::BYTES], b2[TB::BYTES], b3[TB::BYTES];
   __shared__ __attribute__((aligned(16))) char a4[A2], a5[A2], a6[A2], a7[A2], b4[B2], b5[B2], b6[B2], b7[B2];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  int64_t m0, n0;
-  tile_of((e.M + BM - 1) / BM, (e.N + BN - 1) / BN, m0, n0);
-  m0 *= BM;
-  n0 *= BN;
-  const int64_t kb = (int64_t)blockIdx.y * g.k_split, ke = min(g.K, kb + g.k_split);
+  const Place place = place_of<BM, BN>(e.M, e.N);
+  const int64_t m0 = place.m, n0 = place.n;
+  const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
   using S = Share<T, MI>;
   S c;
@@ -655,61 +657,46 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   TB tb;
   ta.init(g.a, g.lda, m0, g.M, kb, ke, g.a_plane);
   tb.init(g.b, g.ldb, n0, g.N, kb, ke, g.b_plane);
-  int64_t k = kb;
-#define EEC_LOAD(TAIL, T, A, B)                   \
-  ta.template load<TAIL>(A, ke - k - (T) * BK);   \
-  tb.template load<TAIL>(B, ke - k - (T) * BK)
-#define EEC_TILE(TAIL, T, F, A, NEXT, NA, NB, FREE_A, FREE_B) \
-  tile_barrier<(BUFS - 3) * LOADS>();                         \
-  EEC_LOAD(TAIL, T + BUFS - 1, FREE_A, FREE_B);               \
+  // k left from the present tile; groups of BUFS tiles, of which those past the end
+  // are zeros, read from nowhere.  There is one copy of the loop: a second one for
+  // the end would run from a cold instruction cache (1536 x 2768 x 1032 bf16: 37 us
+  // with it, XXX without).
+  int left = (int)(ke - kb) * (PARTED ? TA::RUNS : 1);
+#define EEC_LOAD(T, A, B)         \
+  ta.load(A, left - (T) * BK);    \
+  tb.load(B, left - (T) * BK)
+#define EEC_TILE(T, F, A, NEXT, NA, NB, FREE_A, FREE_B) \
+  tile_barrier<(BUFS - 3) * LOADS>();                   \
+  EEC_LOAD(T + BUFS - 1, FREE_A, FREE_B);               \
   multiply<S, TA, TB>(c, F, A, wm, NEXT, NA, NB, wn)
-#define EEC_FOUR(TAIL)                             \
-  EEC_TILE(TAIL, 0, f0, a0, f1, a1, b1, a3, b3);   \
-  EEC_TILE(TAIL, 1, f1, a1, f0, a2, b2, a0, b0);   \
-  EEC_TILE(TAIL, 2, f0, a2, f1, a3, b3, a1, b1);   \
-  EEC_TILE(TAIL, 3, f1, a3, f0, a0, b0, a2, b2)
-#define EEC_EIGHT(TAIL)                            \
-  EEC_TILE(TAIL, 0, f0, a0, f1, a1, b1, a7, b7);   \
-  EEC_TILE(TAIL, 1, f1, a1, f0, a2, b2, a0, b0);   \
-  EEC_TILE(TAIL, 2, f0, a2, f1, a3, b3, a1, b1);   \
-  EEC_TILE(TAIL, 3, f1, a3, f0, a4, b4, a2, b2);   \
-  EEC_TILE(TAIL, 4, f0, a4, f1, a5, b5, a3, b3);   \
-  EEC_TILE(TAIL, 5, f1, a5, f0, a6, b6, a4, b4);   \
-  EEC_TILE(TAIL, 6, f0, a6, f1, a7, b7, a5, b5);   \
-  EEC_TILE(TAIL, 7, f1, a7, f0, a0, b0, a6, b6)
-  EEC_LOAD(!PARTED, 0, a0, b0);
-  EEC_LOAD(!PARTED, 1, a1, b1);
-  EEC_LOAD(!PARTED, 2, a2, b2);
+  EEC_LOAD(0, a0, b0);
+  EEC_LOAD(1, a1, b1);
+  EEC_LOAD(2, a2, b2);
   if constexpr (BUFS == 8) {
-    EEC_LOAD(!PARTED, 3, a3, b3);
-    EEC_LOAD(!PARTED, 4, a4, b4);
-    EEC_LOAD(!PARTED, 5, a5, b5);
-    EEC_LOAD(!PARTED, 6, a6, b6);
+    EEC_LOAD(3, a3, b3);
+    EEC_LOAD(4, a4, b4);
+    EEC_LOAD(5, a5, b5);
+    EEC_LOAD(6, a6, b6);
   }
   tile_barrier<(BUFS - 2) * LOADS>();
   read_ahead<S, TA, TB>(f0, a0, b0, wm, wn);
-  // Whole groups of tiles; with PARTED every tile is whole, otherwise those past the
-  // end are zeros, read from nowhere.
-  const int64_t whole = PARTED ? kb + (ke - kb) * TA::RUNS : ke - (2 * BUFS - 1) * BK + 1;
-  const int64_t end = PARTED ? whole : ke;
-  for (; k < whole; k += BUFS * BK) {
+  for (; left > 0; left -= BUFS * BK) {
     if constexpr (BUFS == 8) {
-      EEC_EIGHT(false);
+      EEC_TILE(0, f0, a0, f1, a1, b1, a7, b7);
+      EEC_TILE(1, f1, a1, f0, a2, b2, a0, b0);
+      EEC_TILE(2, f0, a2, f1, a3, b3, a1, b1);
+      EEC_TILE(3, f1, a3, f0, a4, b4, a2, b2);
+      EEC_TILE(4, f0, a4, f1, a5, b5, a3, b3);
+      EEC_TILE(5, f1, a5, f0, a6, b6, a4, b4);
+      EEC_TILE(6, f0, a6, f1, a7, b7, a5, b5);
+      EEC_TILE(7, f1, a7, f0, a0, b0, a6, b6);
     } else {
-      EEC_FOUR(false);
+      EEC_TILE(0, f0, a0, f1, a1, b1, a3, b3);
+      EEC_TILE(1, f1, a1, f0, a2, b2, a0, b0);
+      EEC_TILE(2, f0, a2, f1, a3, b3, a1, b1);
+      EEC_TILE(3, f1, a3, f0, a0, b0, a2, b2);
     }
   }
-  if constexpr (!PARTED) {
-    for (; k < end; k += BUFS * BK) {
-      if constexpr (BUFS == 8) {
-        EEC_EIGHT(true);
-      } else {
-        EEC_FOUR(true);
-      }
-    }
-  }
-#undef EEC_EIGHT
-#undef EEC_FOUR
 #undef EEC_TILE
 #undef EEC_LOAD
   tile_barrier<0>();  // nobody's loads or reads are left in the buffers
@@ -718,7 +705,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   const int of = WAVES == 4 ? wave : wave >> 1;
   char* mine = (of == 0 ? a0 : of == 1 ? a1 : of == 2 ? a2 : a3) + (WAVES == 4 ? 0 : (wave & 1) * 8192);
   finish_wave<O, S::GROUPS, S::ROWS, 32 / S::ROWS>(
-      e, mine, m0 + wm, n0 + wn, [&](int i, char* rows) { c.put(i, rows); });
+      e, mine, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) { c.put(i, rows); });
 #endif
 }
 
@@ -871,9 +858,10 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
 
 // ------------------------------------------------------------------ packing
 
-// A matrix laid out for the tiled product: rows padded to a stride of whole 16-byte
-// chunks with zeros; float32 as three planes of bf16 parts, rows and columns padded
-// to multiples of 128 (either may be k).
+// A matrix laid out for the tiled product: rows padded with zeros to a multiple of
+// 128 elements, whole cache lines (at a stride of 2064 bytes a tile's 64-byte pieces
+// cross lines: 1536 x 2768 x 1032 bf16 37 us, 29 us at 4096); float32 as three planes
+// of bf16 parts, the number of rows padded alike (either may be k).
 struct Packing {
   const void* from;
   int64_t ld, rows, cols;        // of the source
@@ -916,7 +904,7 @@ constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int packed_size(int32_t dtype) { return dtype == EEC_E4M3 ? 1 : 2; }
 Packing packing(int32_t dtype, const void* from, int64_t ld, int64_t rows, int64_t cols, char* to) {
   Packing p{from, ld, rows, cols, to, 0, 0, 0};
-  p.to_ld = dtype == EEC_F32 ? up(cols, 128) : up(cols, 16 / packed_size(dtype));
+  p.to_ld = up(cols, 128);
   p.to_rows = dtype == EEC_F32 ? up(rows, 128) : rows;
   p.plane = p.to_rows * p.to_ld * packed_size(dtype);
   return p;
@@ -1009,7 +997,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   e.M = g.M;
   e.N = g.N;
   e.part = p.splits > 1 ? ws : nullptr;
-  const dim3 grid((unsigned)p.tiles, (unsigned)p.splits);
+  const dim3 grid((unsigned)(p.tiles * p.splits));
   if constexpr (!std::is_same<T, e4m3_wide>::value) {
     constexpr bool PARTED = std::is_same<T, float>::value;
     using E = std::conditional_t<PARTED, bf16, T>;
