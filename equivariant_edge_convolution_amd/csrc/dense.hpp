@@ -57,7 +57,15 @@ __device__ __forceinline__ void store_run(T* __restrict__ p, int64_t valid, cons
     T t[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) t[i] = (T)v[i];
-    __builtin_memcpy(p, t, sizeof(t));
+    if constexpr (sizeof(t) == 16) {
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      typedef i32x4 i32x4_any __attribute__((aligned(1)));
+      i32x4 q;
+      __builtin_memcpy(&q, t, 16);
+      __builtin_nontemporal_store(q, (i32x4_any*)p);
+    } else {
+      __builtin_memcpy(p, t, sizeof(t));
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i)
