@@ -27,14 +27,12 @@ struct Epilogue {
   float* part;  // split sums [split][M][N] instead of all of the above, or NULL
 };
 
-// What L adjacent columns have in common over the rows.
+// What L adjacent columns, `left` of which exist, have in common over the rows.
 template <typename O, int L>
 struct Columns {
   int64_t n, left;
   float bias[L], scale[L];
-  __device__ __forceinline__ void load(const Epilogue& e, int64_t n_) {
-    n = n_;
-    left = e.N - n_;
+  __device__ __forceinline__ Columns(const Epilogue& e, int64_t n_, int64_t left_) : n(n_), left(left_) {
     if (e.bias) load_run((const O*)e.bias + n, left, bias);
     if (e.w_scale) load_run(e.w_scale + n, left, scale);
   }
@@ -42,8 +40,8 @@ struct Columns {
 template <typename O, int L>
 struct Residual {
   O v[L];  // as it comes from memory
-  __device__ __forceinline__ void load(const Epilogue& e, int64_t m, int64_t n) {
-    if (e.residual && m < e.M) load_raw((const O*)e.residual + m * e.ldr + n, e.N - n, v);
+  __device__ __forceinline__ void load(const Epilogue& e, int64_t m, const Columns<O, L>& c) {
+    if (e.residual && m < e.M) load_raw<true>((const O*)e.residual + m * e.ldr + c.n, c.left, v);
   }
 };
 
@@ -53,7 +51,7 @@ struct Residual {
 template <typename O, int L>
 __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const Columns<O, L>& c, const Residual<O, L>& r,
                                            float (&v)[L]) {
-  if (m >= e.M || c.left <= 0) return;
+  if (m >= e.M) return;
   if (e.x_scale) {
     const float xs = e.x_scale[m];
 #pragma unroll
@@ -77,33 +75,50 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
 // there each access takes 16 bytes a lane of whole rows, and the code is short
 // whatever a lane's registers hold: written out for every register it no longer
 // fits the instruction cache (8192 x 8192 x 32 bf16: 64 us, this 46 us).
-// Up to four rows' residuals a lane are on their way together.
+// Up to eight rows' residuals a lane are on their way together.
 template <typename O, int ROWS>
 __device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, int64_t m0, int64_t n0, int split) {
   constexpr int L = 16 / (int)sizeof(O), PER = L;              // columns of a lane, rows of one access
-  constexpr int TOGETHER = ROWS / PER < 4 ? ROWS / PER : 4;
+  constexpr int TOGETHER = ROWS / PER < 8 ? ROWS / PER : 8;
   static_assert(ROWS % (TOGETHER * PER) == 0, "whole accesses");
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, columns = (int)min((int64_t)64, e.N - n0);
   float* part = e.part ? e.part + split * e.M * e.N : nullptr;
   const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
-  Columns<O, L> c;
-  c.load(e, n0 + col);
+  if (col + L <= columns) {
+    const Columns<O, L> c(e, n0 + col, L);
 #pragma unroll 1
-  for (int r = r0; r < ROWS; r += TOGETHER * PER) {
-    Residual<O, L> res[TOGETHER];
+    for (int r = r0; r < ROWS; r += TOGETHER * PER) {
+      Residual<O, L> res[TOGETHER];
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) res[i].load(e, m0 + r + i * PER, n0 + col);
+      for (int i = 0; i < TOGETHER; ++i) res[i].load(e, m0 + r + i * PER, c);
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) {
-      const int row = r + i * PER;
-      float v[L];
+      for (int i = 0; i < TOGETHER; ++i) {
+        const int row = r + i * PER;
+        float v[L];
 #pragma unroll
-      for (int u = 0; u < L; u += 4)
-        __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
+        for (int u = 0; u < L; u += 4)
+          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
+        if (part == nullptr)
+          finish_run<O, L>(e, m0 + row, c, res[i], v);
+        else if (m0 + row < e.M)
+          store_run(part + (m0 + row) * e.N + n0 + col, L, v);
+      }
+    }
+  }
+  // the last columns of C that make no whole run: a row a lane, a column at a time
+  if (columns % L > 0 && lane < ROWS) {
+    const int64_t m = m0 + lane;
+#pragma unroll 1
+    for (int at = columns / L * L; at < columns; ++at) {
+      const Columns<O, 1> c(e, n0 + at, 1);
+      Residual<O, 1> res;
+      res.load(e, m, c);
+      float v[1];
+      __builtin_memcpy(v, lds + (lane * 256 + ((at / 4) ^ (lane & 15)) * 16 + at % 4 * 4), 4);
       if (part == nullptr)
-        finish_run<O, L>(e, m0 + row, c, res[i], v);
-      else if (m0 + row < e.M)
-        store_run(part + (m0 + row) * e.N + n0 + col, c.left, v);
+        finish_run<O, 1>(e, m, c, res, v);
+      else if (m < e.M)
+        part[m * e.N + n0 + at] = v[0];
     }
   }
 }
@@ -139,10 +154,9 @@ __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) v[c] += t[c];
     }
-    Columns<O, 4> c;
-    c.load(e, n);
+    const Columns<O, 4> c(e, n, e.N - n);
     Residual<O, 4> r;
-    r.load(e, m, n);
+    r.load(e, m, c);
     finish_run<O, 4>(e, m, c, r, v);
   }
 }
@@ -700,12 +714,13 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #undef EEC_TILE
 #undef EEC_LOAD
   tile_barrier<0>();  // nobody's loads or reads are left in the buffers
-  // 32 rows of a wave in 8 KB: two waves to an operand's buffer
-  static_assert(TA::BYTES * 4 >= WAVES * 8192, "room for 8 KB a wave");
-  const int of = WAVES == 4 ? wave : wave >> 1;
-  char* mine = (of == 0 ? a0 : of == 1 ? a1 : of == 2 ? a2 : a3) + (WAVES == 4 ? 0 : (wave & 1) * 8192);
-  finish_wave<O, S::GROUPS, S::ROWS, 32 / S::ROWS>(
-      e, mine, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) { c.put(i, rows); });
+  // a buffer of its own for each wave: 64 rows of sums in 16 KB, or 32 in 8
+  constexpr int SUMS = TA::BYTES >= 16384 && TB::BYTES >= 16384 ? 64 : 32;
+  static_assert(TA::BYTES >= SUMS * 256 && TB::BYTES >= SUMS * 256 && WAVES <= 8, "room for the sums");
+  const int pair = wave >> 1;
+  char *even = pair == 0 ? a0 : pair == 1 ? a1 : pair == 2 ? a2 : a3, *odd = pair == 0 ? b0 : pair == 1 ? b1 : pair == 2 ? b2 : b3;
+  finish_wave<O, S::GROUPS, S::ROWS, SUMS / S::ROWS>(
+      e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) { c.put(i, rows); });
 #endif
 }
 
@@ -803,11 +818,12 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
     for (int i = 1; i < WAVES; ++i) v += join[i][wave][lane];
     float r[4] = {v[0], v[1], v[2], v[3]};
     const int64_t m = wave * 16 + (lane & 15);
-    Columns<O, 4> c;
-    c.load(e, n0 + q * 4);
-    Residual<O, 4> res;
-    res.load(e, m, n0 + q * 4);
-    finish_run<O, 4>(e, m, c, res, r);
+    if (n0 + q * 4 < e.N) {
+      const Columns<O, 4> c(e, n0 + q * 4, e.N - n0 - q * 4);
+      Residual<O, 4> res;
+      res.load(e, m, c);
+      finish_run<O, 4>(e, m, c, res, r);
+    }
   }
 }
 
@@ -833,9 +849,9 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
   float sum[V] = {};
   for (int64_t r = r0 + wave; r < r1; r += 4) {
     float g[V], z[V];
-    load_run((const T*)a.gy + r * a.ldgy + col, left, g);
+    load_run<true>((const T*)a.gy + r * a.ldgy + col, left, g);
     if (a.act != EEC_ACT_NONE) {
-      load_run((const T*)a.preact + r * a.cols + col, left, z);
+      load_run<true>((const T*)a.preact + r * a.cols + col, left, z);
       act_slopes<T>(g, z, a.act);
     }
     if (a.gz) store_run((T*)a.gz + r * a.cols + col, left, g);
@@ -951,7 +967,7 @@ bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype) {
 // 256 CUs idle: joining the sums costs about 5 us, in which a 128 x 128 tile gets
 // through 1200 k and the general kernel, which waits for memory at every step,
 // through some 200.
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool packed, bool forward) {
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool f32, bool tiled, bool packed, bool forward) {
   Plan p{};
   if (forward && M <= FEW_ROWS) {
     p.kind = FEW;
@@ -960,7 +976,14 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool packed, bool
   }
   const int64_t t256 = tiles_of(M, N, 256), t128 = tiles_of(M, N, 128);
   p.packed = packed;
-  p.kind = tiled || packed ? (t256 >= 192 ? TILE256 : TILE128) : t128 >= 256 ? GENERAL : SMALL;
+  // One round of the 256 CUs takes 128 x 128 tiles about 10 us and 0.25 us for every
+  // 32 k, 256 x 256 tiles 20 us and 0.49 us (bf16 with bias, GELU and residual:
+  // 1536 x 2768 x 1024 36 us in 264 small tiles, 41 us in 66 large ones; 4096 x 4096 x
+  // 1024 43 us in 256 large ones).
+  const double steps = (double)K / 32 * (packed && f32 ? 6 : 1);
+  const double us128 = (double)((t128 + 255) / 256) * (10 + 0.25 * steps);
+  const double us256 = (double)((t256 + 255) / 256) * (20 + 0.49 * steps);
+  p.kind = tiled || packed ? (us256 < us128 ? TILE256 : TILE128) : t128 >= 256 ? GENERAL : SMALL;
   p.tiles = p.kind == TILE256 ? t256 : p.kind == SMALL ? tiles_of(M, N, 64) : t128;
   const bool general = p.kind == GENERAL || p.kind == SMALL;
   const int64_t step = 128;  // k of a split is a multiple of every kernel's tiles
@@ -971,10 +994,10 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool tiled, bool packed, bool
   return p;
 }
 // Room for the split sums, however the operands turn out to be aligned.
-size_t split_workspace(int64_t M, int64_t N, int64_t K, bool packed, bool forward) {
+size_t split_workspace(int64_t M, int64_t N, int64_t K, bool f32, bool packed, bool forward) {
   if (M == 0 || N == 0) return 0;
-  int64_t s = plan_product(M, N, K, true, packed, forward).splits;
-  if (!packed) s = std::max(s, plan_product(M, N, K, false, packed, forward).splits);
+  int64_t s = plan_product(M, N, K, f32, true, packed, forward).splits;
+  if (!packed) s = std::max(s, plan_product(M, N, K, f32, false, packed, forward).splits);
   return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
 }
 
@@ -992,7 +1015,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value && !packed &&
                        tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
                        tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
-  const Plan p = plan_product(g.M, g.N, g.K, aligned, packed, A_KC && B_KC);
+  const Plan p = plan_product(g.M, g.N, g.K, dtype == EEC_F32, aligned, packed, A_KC && B_KC);
   g.k_split = p.k_split;
   e.M = g.M;
   e.N = g.N;
@@ -1045,7 +1068,7 @@ FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_w = at;
   if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  p.bytes = at + split_workspace(rows, outer, inner, p.packed, true);
+  p.bytes = at + split_workspace(rows, outer, inner, dtype == EEC_F32, p.packed, true);
   return p;
 }
 
@@ -1076,8 +1099,8 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_wp = at;
   if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  at += std::max(split_workspace(rows, inner, outer, p.packed, false),
-                 split_workspace(outer, inner, rows, p.packed, false));
+  at += std::max(split_workspace(rows, inner, outer, dtype == EEC_F32, p.packed, false),
+                 split_workspace(outer, inner, rows, dtype == EEC_F32, p.packed, false));
   p.bytes = at;
   return p;
 }

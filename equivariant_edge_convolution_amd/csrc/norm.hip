@@ -73,10 +73,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(NormIn in, NormO
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int at = (c * TPR + t) * V;
-      load_run(x + at, n - at, s[c]);
+      load_run<true>(x + at, n - at, s[c]);
       if (r) {
         float b[V];
-        load_run(r + at, n - at, b);
+        load_run<true>(r + at, n - at, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[c][i] += b[i];
       }
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(1024) k_norm_wide(NormIn in, NormOut out) {
       load_run(x + at, n - at, s);
       if (r) {
         float b[V];
-        load_run(r + at, n - at, b);
+        load_run<true>(r + at, n - at, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) s[i] += b[i];
       }
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm_bwd(NormBwd a) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int at = (c * TPR + t) * V;
-      load_run(s + at, n - at, xh[c]);
-      load_run(gy + at, n - at, q[c]);
+      load_run<true>(s + at, n - at, xh[c]);
+      load_run<true>(gy + at, n - at, q[c]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         xh[c][i] *= rstd;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm_bwd(NormBwd a) {
     for (int c = 0; c < CH; ++c) {
       const int at = (c * TPR + t) * V;
       float b[V];
-      if (gs) load_run(gs + at, n - at, b);
+      if (gs) load_run<true>(gs + at, n - at, b);
 #pragma unroll
       for (int i = 0; i < V; ++i) q[c][i] = rstd * (q[c][i] - xh[c][i] * dot) + (gs ? b[i] : 0.f);
       if (a.gx) store_run((T*)a.gx + row * n + at, n - at, q[c]);
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(1024) k_norm_bwd_wide(NormBwd a) {
       load_run(s + at, n - at, xh);
       load_run(gy + at, n - at, q);
       if (w) load_run(w + at, n - at, g);
-      if (gs) load_run(gs + at, n - at, b);
+      if (gs) load_run<true>(gs + at, n - at, b);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         q[i] = rstd * (q[i] * (w ? g[i] : 1.f) - xh[i] * rstd * dot) + (gs ? b[i] : 0.f);
