@@ -430,7 +430,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 //       banks.  Only the low bits of a chunk's place depend on the lane, so a few
 //       address registers serve all fragments.
 // Neither has a bank conflict by the counter.
-template <typename T, bool KC, int LINES, int WAVES, int PARTS>
+template <typename T, bool KC, int LINES, int WAVES>
 struct Tile {
   static constexpr int BK = 64 / (int)sizeof(T);          // k of a tile
   static constexpr int LOADS = LINES / 16 / WAVES;        // direct loads of one wave
@@ -440,15 +440,9 @@ struct Tile {
   static constexpr int BYTES = LINES / 16 * STRIDE;
   static constexpr int READS = KC && sizeof(T) == 2 ? 1 : 2;  // LDS reads of one fragment
   static constexpr uint32_t NOWHERE = 0x80000000u;        // past every buffer: reads as zero
-  static constexpr int RUNS = 6;
   const char* base;  // of the next tile, uniform
   int64_t step;      // bytes from tile to tile
   uint32_t off[LOADS];
-  // PARTS: the operand's order of parts, two bits each, over as many runs through k
-  // of `tiles` tiles each.
-  const char* first;
-  int64_t plane;
-  int tile, tiles, run;
 
   // Load i of this wave: its place among the tile's loads.
   static __device__ __forceinline__ int place(int i) { return wave_id() * LOADS + i; }
@@ -466,17 +460,9 @@ struct Tile {
   static __device__ __forceinline__ int block_of(int u) {
     return PER_LOAD == 2 ? (u & 9) | (u & 2) << 1 | (u >> 1 & 2) : (u & 4) | (u & 1) << 1 | (u >> 1 & 1);
   }
-  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0, int64_t k1,
-                                       int64_t plane_) {
+  __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0) {
     const int lane = threadIdx.x & 63;
     base = (const char*)p + (KC ? (line0 * ld + k0) : (k0 * ld + line0)) * (int64_t)sizeof(T);
-    if constexpr (PARTS != 0) {
-      first = base;
-      plane = plane_;
-      tile = run = 0;
-      tiles = (int)((k1 - k0) / BK);
-      base += (PARTS & 3) * plane;
-    }
     step = (KC ? (int64_t)BK : (int64_t)BK * ld) * (int64_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
@@ -493,20 +479,22 @@ struct Tile {
   // Loads the next tile, of which `left` k exist (none, perhaps): what lies past the
   // end reads as zero.
   __device__ __forceinline__ void load(char* lds, int left) {
-    const int size = PARTS != 0 && run >= RUNS ? 0 : 0x7fffffff;  // after the last run, nothing
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, size, 0x00020000);
+    load_from(lds, base, left);
+    base += step;
+  }
+  // The next tile of all three planes (BYTES apart in LDS), of a whole number of tiles.
+  __device__ __forceinline__ void load_planes(char* lds, int64_t plane, int left) {
+#pragma unroll
+    for (int p = 0; p < 3; ++p) load_from(lds + p * BYTES, base + p * plane, left);
+    base += step;
+  }
+  __device__ __forceinline__ void load_from(char* lds, const char* from, int left) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0x7fffffff, 0x00020000);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void*)(lds + place(i) * STRIDE), 16,
-          PARTS != 0 || at_k(i) < left ? off[i] : NOWHERE, 0, 0, 0);
-    base += step;
-    if constexpr (PARTS != 0) {
-      const bool last = ++tile == tiles;
-      tile = last ? 0 : tile;
-      run += last ? 1 : 0;
-      base = last ? first + (PARTS >> 2 * run & 3) * plane : base;
-    }
+          rsrc, (__attribute__((address_space(3))) void*)(lds + place(i) * STRIDE), 16, at_k(i) < left ? off[i] : NOWHERE,
+          0, 0, 0);
   }
   // Fragment i of the lines from `line` (a multiple of 64).  Each address is one
   // addition to the buffer: through a longer chain the compiler loses sight of the
@@ -642,16 +630,12 @@ __device__ __forceinline__ void tile_barrier() {
 // six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, 43 with
 // eight).
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
-// PARTED: float32 operands as planes of bf16 parts (k_pack, k in whole groups of
-// four tiles, zeros past the end).  The six part products are six runs through k,
-// in rising size, of the one bf16 kernel.
-template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS, bool PARTED>
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
-  // the parts h, m, l as 0, 1, 2: (l, h), (h, l), (m, m), (m, h), (h, m), (h, h)
-  using TA = Tile<T, A_KC, BM, WAVES, PARTED ? 2 | 0 << 2 | 1 << 4 | 1 << 6 | 0 << 8 | 0 << 10 : 0>;
-  using TB = Tile<T, B_KC, BN, WAVES, PARTED ? 0 | 2 << 2 | 1 << 4 | 0 << 6 | 1 << 8 | 0 << 10 : 0>;
+  using TA = Tile<T, A_KC, BM, WAVES>;
+  using TB = Tile<T, B_KC, BN, WAVES>;
   constexpr int BK = TA::BK, LOADS = TA::LOADS + TB::LOADS;
   // The buffers are variables of their own: the compiler then sees that loads into
   // one do not touch the others, and does not wait for them before it reads.
@@ -669,13 +653,13 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   Ahead<S> f0, f1;
   TA ta;
   TB tb;
-  ta.init(g.a, g.lda, m0, g.M, kb, ke, g.a_plane);
-  tb.init(g.b, g.ldb, n0, g.N, kb, ke, g.b_plane);
+  ta.init(g.a, g.lda, m0, g.M, kb);
+  tb.init(g.b, g.ldb, n0, g.N, kb);
   // k left from the present tile; groups of BUFS tiles, of which those past the end
   // are zeros, read from nowhere.  There is one copy of the loop: a second one for
   // the end would run from a cold instruction cache (1536 x 2768 x 1032 bf16: 37 us
   // with it, XXX without).
-  int left = (int)(ke - kb) * (PARTED ? TA::RUNS : 1);
+  int left = (int)(ke - kb);
 #define EEC_LOAD(T, A, B)         \
   ta.load(A, left - (T) * BK);    \
   tb.load(B, left - (T) * BK)
@@ -721,6 +705,72 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   char *even = pair == 0 ? a0 : pair == 1 ? a1 : pair == 2 ? a2 : a3, *odd = pair == 0 ? b0 : pair == 1 ? b1 : pair == 2 ? b2 : b3;
   finish_wave<O, S::GROUPS, S::ROWS, SUMS / S::ROWS>(
       e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) { c.put(i, rows); });
+#endif
+}
+
+// ------------------------------------------------------------------ tiled product (float32 in parts)
+
+// 256 x 128 of C per workgroup, 64 x 64 per wave, from planes of bf16 parts
+// (k_pack: k in whole groups of four tiles).  A step is 32 k of all six planes,
+// 72 KB of LDS, and does all six part products, so a plane is loaded once; two
+// buffers: a step's 96 products a wave take 3100 cycles, the next one's loads 1900.
+template <bool A_KC, bool B_KC>
+__global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
+#ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
+  using TA = Tile<bf16, A_KC, 256, 8>;
+  using TB = Tile<bf16, B_KC, 128, 8>;
+  __shared__ __attribute__((aligned(1024))) char a0[3 * TA::BYTES], a1[3 * TA::BYTES], b0[3 * TB::BYTES], b1[3 * TB::BYTES];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const Place place = place_of<256, 128>(e.M, e.N);
+  const int64_t m0 = place.m, n0 = place.n;
+  const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
+  const int wm = wave / 2 * 64, wn = wave % 2 * 64;
+  f32x4 acc[4][4] = {};
+  TA ta;
+  TB tb;
+  ta.init(g.a, g.lda, m0, g.M, kb);
+  tb.init(g.b, g.ldb, n0, g.N, kb);
+  auto step = [&](const char* la, const char* lb) {
+    bf16x8 b[3][4];
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) TB::fragment(b[p][j], lb + p * TB::BYTES, wn, j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bf16x8 a[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) TA::fragment(a[p], la + p * TA::BYTES, wm, i);
+      // in rising size: (l, h), (h, l), (m, m), (m, h), (h, m), (h, h)
+      constexpr int pa[6] = {2, 0, 1, 1, 0, 0}, pb[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+      for (int t = 0; t < 6; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[pb[t]][j], a[pa[t]], acc[i][j], 0, 0, 0);
+    }
+  };
+#define EEC_LOAD(A, B, LEFT)                          \
+  ta.load_planes(A, g.a_plane, LEFT);                 \
+  tb.load_planes(B, g.b_plane, LEFT)
+  int left = (int)(ke - kb);
+  EEC_LOAD(a0, b0, left);
+  for (; left > 0; left -= 2 * TA::BK) {  // two steps; k is whole groups of four
+    tile_barrier<0>();
+    EEC_LOAD(a1, b1, left - TA::BK);
+    step(a0, b0);
+    tile_barrier<0>();
+    EEC_LOAD(a0, b0, left - 2 * TA::BK);
+    step(a1, b1);
+  }
+#undef EEC_LOAD
+  tile_barrier<0>();
+  // 64 rows of sums in 16 KB for each wave: three in an A buffer, one in a B buffer
+  char* mine = wave < 3 ? a0 + wave * 16384 : wave < 6 ? a1 + (wave - 3) * 16384 : wave == 6 ? b0 : b1;
+  finish_wave<float, 4, 16, 4>(e, mine, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
+  });
 #endif
 }
 
@@ -938,7 +988,7 @@ void pack(hipStream_t st, const Packings& all) {
 
 // ------------------------------------------------------------------ plans
 
-enum Kind { SMALL, GENERAL, TILE128, TILE256, FEW };  // SMALL: the general kernel in 64 x 64 tiles
+enum Kind { SMALL, GENERAL, TILE128, TILE256, PARTED, FEW };  // SMALL: the general kernel in 64 x 64 tiles
 struct Plan {
   Kind kind;
   bool packed;  // operands through k_pack
@@ -980,14 +1030,21 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool f32, bool tiled, bool pa
   // 32 k, 256 x 256 tiles 20 us and 0.49 us (bf16 with bias, GELU and residual:
   // 1536 x 2768 x 1024 36 us in 264 small tiles, 41 us in 66 large ones; 4096 x 4096 x
   // 1024 43 us in 256 large ones).
-  const double steps = (double)K / 32 * (packed && f32 ? 6 : 1);
+  const double steps = (double)K / 32;
   const double us128 = (double)((t128 + 255) / 256) * (10 + 0.25 * steps);
   const double us256 = (double)((t256 + 255) / 256) * (20 + 0.49 * steps);
-  p.kind = tiled || packed ? (us256 < us128 ? TILE256 : TILE128) : t128 >= 256 ? GENERAL : SMALL;
-  p.tiles = p.kind == TILE256 ? t256 : p.kind == SMALL ? tiles_of(M, N, 64) : t128;
+  p.kind = packed && f32       ? PARTED
+           : tiled || packed   ? (us256 < us128 ? TILE256 : TILE128)
+           : t128 >= 256       ? GENERAL
+                               : SMALL;
+  p.tiles = p.kind == TILE256  ? t256
+            : p.kind == PARTED ? ((M + 255) / 256) * ((N + 127) / 128)
+            : p.kind == SMALL  ? tiles_of(M, N, 64)
+                               : t128;
   const bool general = p.kind == GENERAL || p.kind == SMALL;
   const int64_t step = 128;  // k of a split is a multiple of every kernel's tiles
-  int64_t s = K < (general ? 512 : 2048) ? 1 : std::min<int64_t>((general ? 512 : 256) / p.tiles, K / (general ? 128 : 512));
+  const int64_t least = general ? 128 : p.kind == PARTED ? 256 : 512;  // k of a split
+  int64_t s = K < 4 * least ? 1 : std::min<int64_t>((general ? 512 : 256) / p.tiles, K / least);
   s = std::max<int64_t>(1, s);
   p.k_split = std::max<int64_t>(step, up((K + s - 1) / s, step));
   p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);
@@ -1021,16 +1078,16 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   e.N = g.N;
   e.part = p.splits > 1 ? ws : nullptr;
   const dim3 grid((unsigned)(p.tiles * p.splits));
-  if constexpr (!std::is_same<T, e4m3_wide>::value) {
-    constexpr bool PARTED = std::is_same<T, float>::value;
-    using E = std::conditional_t<PARTED, bf16, T>;
-    Product t = g;
-    if (PARTED) t.K = up(g.K, 128);
-    // what is loaded along memory may run into the padding, which is there and zero
-    if (packed && !A_KC) t.M = t.lda;
-    if (packed && !B_KC) t.N = t.ldb;
-    if (p.kind == TILE256) k_tiled<E, O, A_KC, B_KC, 2, 4, 8, 4, PARTED><<<grid, 512, 0, st>>>(t, e);
-    if (p.kind == TILE128) k_tiled<E, O, A_KC, B_KC, 2, 2, 4, 8, PARTED><<<grid, 256, 0, st>>>(t, e);
+  Product t = g;
+  // what is loaded along memory may run into the padding, which is there and zero
+  if (packed && !A_KC) t.M = t.lda;
+  if (packed && !B_KC) t.N = t.ldb;
+  if constexpr (std::is_same<T, float>::value) {
+    t.K = up(g.K, 128);
+    if (p.kind == PARTED) k_parted<A_KC, B_KC><<<grid, 512, 0, st>>>(t, e);
+  } else if constexpr (!std::is_same<T, e4m3_wide>::value) {
+    if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8, 4><<<grid, 512, 0, st>>>(t, e);
+    if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 8><<<grid, 256, 0, st>>>(t, e);
   }
   if constexpr (A_KC && B_KC) {
     const dim3 columns((unsigned)((g.N + 15) / 16));
