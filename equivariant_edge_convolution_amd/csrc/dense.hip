@@ -147,12 +147,16 @@ __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
   const int64_t per_row = (e.N + 3) / 4, total = e.M * per_row;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / per_row, n = i % per_row * 4;
-    float v[4], t[4];
-    load_run(e.part + m * e.N + n, e.N - n, v);
-    for (int s = 1; s < splits; ++s) {
-      load_run(e.part + ((int64_t)s * e.M + m) * e.N + n, e.N - n, t);
+    float v[4] = {};
+    for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads on their way
+      float t[8][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += t[c];
+      for (int s = 0; s < 8; ++s)
+        load_run(e.part + ((int64_t)(s0 + s) * e.M + m) * e.N + n, s0 + s < splits ? e.N - n : 0, t[s]);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] += t[s][c];
     }
     const Columns<O, 4> c(e, n, e.N - n);
     Residual<O, 4> r;
@@ -750,9 +754,11 @@ __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[pb[t]][j], a[pa[t]], acc[i][j], 0, 0, 0);
     }
   };
-#define EEC_LOAD(A, B, LEFT)                          \
-  ta.load_planes(A, g.a_plane, LEFT);                 \
-  tb.load_planes(B, g.b_plane, LEFT)
+// The scheduler would put the loads next to the wait at the step's end.
+#define EEC_LOAD(A, B, LEFT)          \
+  ta.load_planes(A, g.a_plane, LEFT); \
+  tb.load_planes(B, g.b_plane, LEFT); \
+  __builtin_amdgcn_sched_barrier(0)
   int left = (int)(ke - kb);
   EEC_LOAD(a0, b0, left);
   for (; left > 0; left -= 2 * TA::BK) {  // two steps; k is whole groups of four
@@ -877,51 +883,6 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   }
 }
 
-// ------------------------------------------------------------------ gradient of the activation
-
-struct ActGrad {
-  const void *gy, *preact;
-  int64_t ldgy, rows, cols, per;  // rows of one strip
-  int32_t act;
-  void* gz;     // [rows][cols], or NULL
-  float* part;  // [strips][cols] column sums of gz before its rounding, or NULL
-};
-
-// gz = gy act'(preact) and its column sums: a wave takes 64 x 8 (float32: 4)
-// columns, a workgroup's waves deal the rows of a strip in turn.
-template <typename T>
-__global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
-  constexpr int V = VEC<T>;
-  __shared__ float join[3][64 * V];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = ((int64_t)blockIdx.x * 64 + lane) * V, left = a.cols - col;
-  const int64_t r0 = (int64_t)blockIdx.y * a.per, r1 = min(a.rows, r0 + a.per);
-  float sum[V] = {};
-  for (int64_t r = r0 + wave; r < r1; r += 4) {
-    float g[V], z[V];
-    load_run<true>((const T*)a.gy + r * a.ldgy + col, left, g);
-    if (a.act != EEC_ACT_NONE) {
-      load_run<true>((const T*)a.preact + r * a.cols + col, left, z);
-      act_slopes<T>(g, z, a.act);
-    }
-    if (a.gz) store_run((T*)a.gz + r * a.cols + col, left, g);
-#pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] += g[i];
-  }
-  if (a.part == nullptr) return;
-  if (wave > 0) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) join[wave - 1][lane * V + i] = sum[i];
-  }
-  __syncthreads();
-  if (wave == 0) {
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] += join[k][lane * V + i];
-    store_run(a.part + (int64_t)blockIdx.y * a.cols + col, left, sum);
-  }
-}
-
 // ------------------------------------------------------------------ packing
 
 // A matrix laid out for the tiled product: rows padded with zeros to a multiple of
@@ -936,7 +897,7 @@ struct Packing {
   int64_t plane;                 // bytes
 };
 struct Packings {
-  Packing p[3];
+  Packing p[2];
 };
 
 template <typename T>
@@ -983,7 +944,66 @@ void pack(hipStream_t st, const Packings& all) {
   int64_t most = 0;
   for (const Packing& p : all.p)
     if (p.to) most = std::max(most, p.to_rows * p.to_ld);
-  if (most > 0) k_pack<T><<<dim3((unsigned)std::min<int64_t>((most + 4095) / 4096, 4096), 3), 256, 0, st>>>(all);
+  if (most > 0) k_pack<T><<<dim3((unsigned)std::min<int64_t>((most + 4095) / 4096, 4096), 2), 256, 0, st>>>(all);
+}
+
+// ------------------------------------------------------------------ gradient of the activation
+
+struct ActGrad {
+  const void *gy, *preact;
+  int64_t ldgy, rows, cols, per;  // rows of one strip
+  int32_t act;
+  void* gz;        // [rows][cols], or NULL
+  Packing packed;  // or gz packed (packed.to not NULL)
+  float* part;     // [strips][cols] column sums of gz before its rounding, or NULL
+};
+
+// gz = gy act'(preact), as it is or packed, and its column sums: a wave takes 64 x 8
+// (float32: 4) columns, a workgroup's waves deal the rows of a strip in turn.
+template <typename T>
+__global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
+  constexpr int V = VEC<T>;
+  __shared__ float join[3][64 * V];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = ((int64_t)blockIdx.x * 64 + lane) * V, left = a.cols - col;
+  const int64_t r0 = (int64_t)blockIdx.y * a.per, r1 = min(a.packed.to ? a.packed.to_rows : a.rows, r0 + a.per);
+  float sum[V] = {};
+  for (int64_t r = r0 + wave; r < r1; r += 4) {
+    float g[V], z[V];
+    const int64_t here = r < a.rows ? left : 0;  // rows and columns of the padding are zeros
+    load_run<true>((const T*)a.gy + r * a.ldgy + col, here, g);
+    if (a.act != EEC_ACT_NONE) {
+      load_run<true>((const T*)a.preact + r * a.cols + col, here, z);
+      act_slopes<T>(g, z, a.act);
+    }
+    if (a.gz) store_run((T*)a.gz + r * a.cols + col, left, g);
+    if (a.packed.to && col < a.packed.to_ld) {
+      char* to = a.packed.to + (r * a.packed.to_ld + col) * 2;
+      if constexpr (std::is_same<T, float>::value) {
+        bf16 q[3][V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) split3(g[i], q[0][i], q[1][i], q[2][i]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) __builtin_memcpy(__builtin_assume_aligned(to + k * a.packed.plane, 8), q[k], 2 * V);
+      } else {
+        store_run((T*)to, V, g);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] += g[i];
+  }
+  if (a.part == nullptr) return;
+  if (wave > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) join[wave - 1][lane * V + i] = sum[i];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] += join[k][lane * V + i];
+    store_run(a.part + (int64_t)blockIdx.y * a.cols + col, left, sum);
+  }
 }
 
 // ------------------------------------------------------------------ plans
@@ -1135,7 +1155,7 @@ int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
   return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 1024 / std::max<int64_t>(1, wide)));
 }
 
-// The backward's: gz, column sums, gz, x and w packed, split sums.
+// The backward's: gz (packed or not), column sums, x and w packed, split sums.
 struct BwdPlan {
   bool packed;
   size_t off_gz, off_part, off_gzp, off_xp, off_wp, off_split, bytes;
@@ -1146,7 +1166,7 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
              (dtype == EEC_F32 || outer % 8 != 0 || inner % 8 != 0);
   size_t at = 0;
   p.off_gz = at;
-  if (act != EEC_ACT_NONE) at += align256((size_t)rows * (size_t)outer * (dtype == EEC_F32 ? 4 : 2));
+  if (act != EEC_ACT_NONE && !p.packed) at += align256((size_t)rows * (size_t)outer * (dtype == EEC_F32 ? 4 : 2));
   p.off_part = at;
   at += align256(4 * (size_t)act_grad_strips(rows, outer, dtype) * (size_t)outer);
   p.off_gzp = at;
@@ -1178,7 +1198,7 @@ void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) {
     if (p.packed) {
       const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, ws + p.off_x);
       const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, ws + p.off_w);
-      const Packings both{{x, w, Packing{}}};
+      const Packings both{{x, w}};
       if (a.dtype == EEC_E4M3)
         pack<e4m3>(st, both);
       else
@@ -1201,23 +1221,25 @@ void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
   const BwdPlan p = bwd_plan(a.rows, a.outer, a.inner, a.dtype, a.act);
   by_type(a.dtype, [&](auto zero) {
     using T = decltype(zero);
-    const bool products = a.gx != nullptr || a.gw != nullptr, shaped = a.act != EEC_ACT_NONE && products;
-    const void* gz = shaped ? (const void*)(ws + p.off_gz) : a.gy;
-    const int64_t ldgz = shaped ? a.outer : a.ldgy;
-    if (a.outer > 0 && ((shaped && a.rows > 0) || a.gbias)) {
+    const bool products = a.gx != nullptr || a.gw != nullptr;
+    const bool packed = p.packed && products, shaped = a.act != EEC_ACT_NONE && products && !packed;
+    const Packing z = packing(a.dtype, nullptr, 0, a.rows, a.outer, packed ? ws + p.off_gzp : nullptr);
+    if (a.outer > 0 && ((shaped && a.rows > 0) || a.gbias || packed)) {
       const int64_t strips = act_grad_strips(a.rows, a.outer, a.dtype), cols = 64 * VEC<T>;
-      const ActGrad q{a.gy,  a.preact, a.ldgy, a.rows, a.outer, (a.rows + strips - 1) / strips,
-                      a.act, shaped ? ws + p.off_gz : nullptr, a.gbias ? (float*)(ws + p.off_part) : nullptr};
-      k_act_grad<T><<<dim3((unsigned)((a.outer + cols - 1) / cols), (unsigned)strips), 256, 0, st>>>(q);
+      const int64_t rows = packed ? z.to_rows : a.rows, width = packed ? z.to_ld : a.outer;
+      const ActGrad q{a.gy,  a.preact, a.ldgy, a.rows, a.outer, (rows + strips - 1) / strips,
+                      a.act, shaped ? ws + p.off_gz : nullptr, z, a.gbias ? (float*)(ws + p.off_part) : nullptr};
+      k_act_grad<T><<<dim3((unsigned)((width + cols - 1) / cols), (unsigned)strips), 256, 0, st>>>(q);
       if (a.gbias) launch_column_sum(st, a.dtype, (const float*)(ws + p.off_part), (int)strips, a.outer, a.gbias);
     }
+    const void* gz = shaped ? (const void*)(ws + p.off_gz) : a.gy;
+    const int64_t ldgz = shaped ? a.outer : a.ldgy;
     Product gx{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0, 0, 0};
     Product gw{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0, 0, 0};
-    if (p.packed && products) {
-      const Packing z = packing(a.dtype, gz, ldgz, a.rows, a.outer, ws + p.off_gzp);
+    if (packed) {
       const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, a.gw ? ws + p.off_xp : nullptr);
       const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, a.gx ? ws + p.off_wp : nullptr);
-      pack<T>(st, Packings{{z, x, w}});
+      pack<T>(st, Packings{{x, w}});
       gx = Product{z.to, w.to, z.to_ld, w.to_ld, a.rows, a.inner, a.outer, 0, z.plane, w.plane};
       gw = Product{z.to, x.to, z.to_ld, x.to_ld, a.outer, a.inner, a.rows, 0, z.plane, x.plane};
     }
