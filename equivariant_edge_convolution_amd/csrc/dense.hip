@@ -956,6 +956,7 @@ struct ActGrad {
   void* gz;        // [rows][cols], or NULL
   Packing packed;  // or gz packed (packed.to not NULL)
   float* part;     // [strips][cols] column sums of gz before its rounding, or NULL
+  void* gbias;     // with one strip the sums themselves instead, or NULL
 };
 
 // gz = gy act'(preact), as it is or packed, and its column sums: a wave takes 64 x 8
@@ -992,7 +993,7 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] += g[i];
   }
-  if (a.part == nullptr) return;
+  if (a.part == nullptr && a.gbias == nullptr) return;
   if (wave > 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i) join[wave - 1][lane * V + i] = sum[i];
@@ -1002,7 +1003,10 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
     for (int k = 0; k < 3; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] += join[k][lane * V + i];
-    store_run(a.part + (int64_t)blockIdx.y * a.cols + col, left, sum);
+    if (a.gbias)
+      store_run((T*)a.gbias + col, left, sum);
+    else
+      store_run(a.part + (int64_t)blockIdx.y * a.cols + col, left, sum);
   }
 }
 
@@ -1149,7 +1153,9 @@ FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   return p;
 }
 
-constexpr int STRIP_ROWS = 4;  // rows of a strip at least, one for each wave
+// Rows of a strip at least: four for each wave, so that a few rows are one strip and
+// their column sums need no second launch.
+constexpr int STRIP_ROWS = 16;
 int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
   const int64_t per = 64 * (dtype == EEC_F32 ? 4 : 8), wide = (cols + per - 1) / per;
   return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 1024 / std::max<int64_t>(1, wide)));
@@ -1228,9 +1234,11 @@ void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
       const int64_t strips = act_grad_strips(a.rows, a.outer, a.dtype), cols = 64 * VEC<T>;
       const int64_t rows = packed ? z.to_rows : a.rows, width = packed ? z.to_ld : a.outer;
       const ActGrad q{a.gy,  a.preact, a.ldgy, a.rows, a.outer, (rows + strips - 1) / strips,
-                      a.act, shaped ? ws + p.off_gz : nullptr, z, a.gbias ? (float*)(ws + p.off_part) : nullptr};
+                      a.act, shaped ? ws + p.off_gz : nullptr, z,
+                      a.gbias && strips > 1 ? (float*)(ws + p.off_part) : nullptr, strips == 1 ? a.gbias : nullptr};
       k_act_grad<T><<<dim3((unsigned)((width + cols - 1) / cols), (unsigned)strips), 256, 0, st>>>(q);
-      if (a.gbias) launch_column_sum(st, a.dtype, (const float*)(ws + p.off_part), (int)strips, a.outer, a.gbias);
+      if (a.gbias && strips > 1)
+        launch_column_sum(st, a.dtype, (const float*)(ws + p.off_part), (int)strips, a.outer, a.gbias);
     }
     const void* gz = shaped ? (const void*)(ws + p.off_gz) : a.gy;
     const int64_t ldgz = shaped ? a.outer : a.ldgy;

@@ -189,7 +189,8 @@ struct NormBwd {
   int64_t rows;
   int width;
   void* gx;
-  float* part;  // [gridDim.x][width] sums of gy xhat, or NULL
+  float* part;    // [gridDim.x][width] sums of gy xhat, or NULL
+  void* gweight;  // with one workgroup the sums themselves instead, or NULL
 };
 
 // TPR threads per row, rows dealt in turn to all row groups of the grid; each
@@ -247,8 +248,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm_bwd(NormBwd a) {
       if (a.gx) store_run((T*)a.gx + row * n + at, n - at, q[c]);
     }
   }
-  if (a.part == nullptr) return;
-  float* o = a.part + (int64_t)blockIdx.x * n;
+  if (a.part == nullptr && a.gweight == nullptr) return;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int at = (c * TPR + t) * V;
@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm_bwd(NormBwd a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[c][i] += join[k][t * V + i];
     }
-    store_run(o + at, n - at, acc[c]);
+    if (a.gweight)
+      store_run((T*)a.gweight + at, n - at, acc[c]);
+    else
+      store_run(a.part + (int64_t)blockIdx.x * n + at, n - at, acc[c]);
   }
 }
 
@@ -370,8 +373,10 @@ void by_type(int32_t dtype, F&& f) {
 }
 
 // Workgroups of the backward: enough to fill the chip twice over, and few enough
-// that the partial sums of the weight gradient stay a small share of the rows.
-int64_t norm_bwd_groups(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, 512)); }
+// that the partial sums of the weight gradient stay a small share of the rows.  A few
+// rows take one, which needs no second launch for the sums (about 4 us).
+constexpr int64_t ONE_GROUP_ROWS = 8;
+int64_t norm_bwd_groups(int64_t rows) { return rows <= ONE_GROUP_ROWS ? 1 : std::min<int64_t>(rows, 512); }
 
 }  // namespace
 
@@ -403,19 +408,25 @@ void launch_norm_bwd(hipStream_t st, int32_t dtype, int64_t rows, int64_t width,
                      const void* s, int64_t lds, const void* weight, const float* rstd, const void* gsum,
                      int64_t ldgs, void* gx, void* gweight, char* ws) {
   const int64_t groups = norm_bwd_groups(rows);
-  float* part = gweight ? (float*)ws : nullptr;
-  const NormBwd a{gy, s, weight, gsum, rstd, ldgy, lds, ldgs, rows, (int)width, gx, part};
+  NormBwd a{gy, s, weight, gsum, rstd, ldgy, lds, ldgs, rows, (int)width, gx, gweight ? (float*)ws : nullptr, nullptr};
+  bool summed = gweight == nullptr;
   by_type(dtype, [&](auto zero) {
     using T = decltype(zero);
     by_width<T>(width, [&](auto tpr, auto ch) {
       constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-      if constexpr (CH == 0)
+      if constexpr (CH == 0) {
         k_norm_bwd_wide<T><<<dim3((unsigned)groups), 1024, 0, st>>>(a);
-      else
+      } else {
+        if (groups == 1 && gweight) {
+          a.part = nullptr;
+          a.gweight = gweight;
+          summed = true;
+        }
         k_norm_bwd<T, TPR, CH><<<dim3((unsigned)groups), TPR < 256 ? 256 : TPR, 0, st>>>(a);
+      }
     });
   });
-  if (gweight) launch_column_sum(st, dtype, (const float*)ws, (int)groups, width, gweight);
+  if (!summed) launch_column_sum(st, dtype, (const float*)ws, (int)groups, width, gweight);
 }
 
 void launch_column_sum(hipStream_t st, int32_t dtype, const float* part, int parts, int64_t n, void* out) {
