@@ -525,6 +525,7 @@ eec_status eec_radial_table_build(void* stream, const eec_model* m, int32_t log2
 namespace {
 
 constexpr int64_t MAX_SIZE = INT32_MAX;
+constexpr int64_t MAX_WIDTH = int64_t(1) << 27;  // columns: a launch counts its threads in 32 bits
 
 size_t dtype_bytes(int32_t t) { return t == EEC_F32 ? 4 : t == EEC_E4M3 ? 1 : 2; }
 bool float_dtype(int32_t t) { return t == EEC_F32 || t == EEC_F16 || t == EEC_BF16; }
@@ -546,6 +547,7 @@ Span matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int32_t dtyp
   return span(p, n * dtype_bytes(dtype), name);
 }
 bool bad_size(int64_t n) { return n < 0 || n > MAX_SIZE; }
+bool bad_width(int64_t n) { return n < 0 || n > MAX_WIDTH; }
 
 eec_status check_act(int32_t act) {
   if (act < EEC_ACT_NONE || act > EEC_ACT_GELU) return fail(EEC_ERR_SHAPE, "unknown activation");
@@ -558,7 +560,7 @@ eec_status eec_add_rms_norm(void* stream, int64_t rows, int64_t width, int32_t d
                             const void* residual, int64_t ldr, const void* weight, double eps, void* sum, void* y,
                             float* scale, float* rstd) {
   if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
-  if (bad_size(rows) || width < 1 || bad_size(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
+  if (bad_size(rows) || width < 1 || bad_width(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
   if (!(isfinite(eps) && eps >= 0.0)) return fail(EEC_ERR_SHAPE, "eps must be finite and >= 0");
   const int32_t ytype = scale != nullptr ? (int32_t)EEC_E4M3 : dtype;
   TRY(check_matrix(x, rows, width, ldx, dtype, "x"));
@@ -578,7 +580,7 @@ eec_status eec_add_rms_norm(void* stream, int64_t rows, int64_t width, int32_t d
 }
 
 size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t width) {
-  if (bad_size(rows) || width < 1 || bad_size(width)) return 0;
+  if (bad_size(rows) || width < 1 || bad_width(width)) return 0;
   return norm_bwd_workspace(rows, width);
 }
 
@@ -587,7 +589,7 @@ eec_status eec_add_rms_norm_backward(void* stream, int64_t rows, int64_t width, 
                                      const float* rstd, const void* gsum, int64_t ldgs, void* gx, void* gweight,
                                      void* workspace, size_t workspace_bytes) {
   if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
-  if (bad_size(rows) || width < 1 || bad_size(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
+  if (bad_size(rows) || width < 1 || bad_width(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
   TRY(check_matrix(gy, rows, width, ldgy, dtype, "gy"));
   TRY(check_matrix(sum, rows, width, lds, dtype, "sum"));
   TRY(check_matrix(rstd, rows, 1, 1, EEC_F32, "rstd"));
@@ -609,7 +611,7 @@ eec_status eec_add_rms_norm_backward(void* stream, int64_t rows, int64_t width, 
 }
 
 static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
-  if (bad_size(rows) || bad_size(outer) || bad_size(inner)) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
+  if (bad_size(rows) || bad_width(outer) || bad_width(inner)) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
   // output tiles of one product, counted as the kernels launch them
   const int64_t r = rows / 128 + 1, o = outer / 128 + 1, i = inner / 128 + 1;
   if (r * o >= (1 << 22) || r * i >= (1 << 22) || o * i >= (1 << 22))
@@ -618,7 +620,7 @@ static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
 }
 
 size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
-  if (bad_size(rows) || bad_size(outer) || bad_size(inner) || (!float_dtype(dtype) && dtype != EEC_E4M3)) return 0;
+  if (bad_size(rows) || bad_width(outer) || bad_width(inner) || (!float_dtype(dtype) && dtype != EEC_E4M3)) return 0;
   return linear_workspace(rows, outer, inner, dtype, out_dtype);
 }
 
@@ -659,7 +661,7 @@ eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, 
 }
 
 size_t eec_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
-  if (bad_size(rows) || bad_size(outer) || bad_size(inner) || !float_dtype(dtype)) return 0;
+  if (bad_size(rows) || bad_width(outer) || bad_width(inner) || !float_dtype(dtype)) return 0;
   return linear_bwd_workspace(rows, outer, inner, dtype, act);
 }
 

@@ -292,7 +292,7 @@ constexpr int GBK = 32;  // k of a step of the general kernel
 // split (the tiles of a split read the same k), each in strips of 8 tiles of m that
 // run along n, so that what its CUs hold at one time reuses few rows of A and B.
 // (32768 x 512 x 512 gw in float32, 16 splits of 16 tiles: 190 us with a split's
-// tiles dealt over all XCDs, XXX so.)
+// tiles dealt over all XCDs, 169 us so.)
 struct Place {
   int64_t m, n;
   int split;
@@ -660,9 +660,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   ta.init(g.a, g.lda, m0, g.M, kb);
   tb.init(g.b, g.ldb, n0, g.N, kb);
   // k left from the present tile; groups of BUFS tiles, of which those past the end
-  // are zeros, read from nowhere.  There is one copy of the loop: a second one for
-  // the end would run from a cold instruction cache (1536 x 2768 x 1032 bf16: 37 us
-  // with it, XXX without).
+  // are zeros, read from nowhere.
   int left = (int)(ke - kb);
 #define EEC_LOAD(T, A, B)         \
   ta.load(A, left - (T) * BK);    \

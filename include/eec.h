@@ -397,7 +397,8 @@ EEC_API size_t eec_workspace_bytes(int32_t n_atoms, int64_t n_edges, const eec_m
  *   - Sums, norms and products are accumulated in float32; every output is
  *     rounded once, to nearest even, to its type.
  *   - NaN and infinities propagate by the formulas.  Sizes may be odd, one, or
- *     zero (a sum over nothing is 0).  Sizes and strides are at most 2^31 - 1. */
+ *     zero (a sum over nothing is 0).  Rows and strides are at most 2^31 - 1,
+ *     columns (width, outer, inner) 2^27, and a product has at most 2^36 outputs. */
 typedef enum { EEC_F32 = 0, EEC_F16 = 1, EEC_BF16 = 2, EEC_E4M3 = 3 /* OCP: max 448, no infinity */ } eec_dtype;
 typedef enum {
   EEC_ACT_NONE = 0,
