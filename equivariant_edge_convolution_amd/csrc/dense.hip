@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
 
 // ------------------------------------------------------------------ plans
 
-enum Kind { SMALL, GENERAL, TILE128, TILE256, PARTED, FEW };  // SMALL: the general kernel in 64 x 64 tiles
+enum Kind { SMALL, GENERAL, TILE128, TILE128X2, TILE256, PARTED, FEW };  // SMALL: the general kernel in 64 x 64 tiles
 struct Plan {
   Kind kind;
   bool packed;  // operands through k_pack
@@ -1039,7 +1039,7 @@ bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype) {
 // 256 CUs idle: joining the sums costs about 5 us, in which a 128 x 128 tile gets
 // through 1200 k and the general kernel, which waits for memory at every step,
 // through some 200.
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool f32, bool tiled, bool packed, bool forward) {
+Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool tiled, bool packed, bool forward) {
   Plan p{};
   if (forward && M <= FEW_ROWS) {
     p.kind = FEW;
@@ -1049,16 +1049,18 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool f32, bool tiled, bool pa
   const int64_t t256 = tiles_of(M, N, 256), t128 = tiles_of(M, N, 128);
   p.packed = packed;
   // One round of the 256 CUs takes 128 x 128 tiles about 10 us and 0.25 us for every
-  // 32 k, 256 x 256 tiles 20 us and 0.49 us (bf16 with bias, GELU and residual:
-  // 1536 x 2768 x 1024 36 us in 264 small tiles, 41 us in 66 large ones; 4096 x 4096 x
-  // 1024 43 us in 256 large ones).
-  const double steps = (double)K / 32;
+  // 64 bytes of k, 256 x 256 tiles 20 us and 0.49 us.  Between one and two rounds of
+  // the small ones, two workgroups with four buffers share a CU instead: bf16 with
+  // bias, GELU and residual, 1536 x 2816 x 1024 24 us (large tiles 35), 2048 x 4096 x
+  // 1024 31 (38), x 4096 87 (99, split); beyond, split large tiles are even.
+  const double steps = (double)K * (dtype == EEC_E4M3 ? 1 : 2) / 64;
   const double us128 = (double)((t128 + 255) / 256) * (10 + 0.25 * steps);
   const double us256 = (double)((t256 + 255) / 256) * (20 + 0.49 * steps);
-  p.kind = packed && f32       ? PARTED
-           : tiled || packed   ? (us256 < us128 ? TILE256 : TILE128)
-           : t128 >= 256       ? GENERAL
-                               : SMALL;
+  const bool shared = t128 > 256 && t128 <= 512 && steps <= 128;
+  p.kind = packed && dtype == EEC_F32 ? PARTED
+           : tiled || packed ? (shared ? TILE128X2 : us256 < us128 ? TILE256 : TILE128)
+           : t128 >= 256     ? GENERAL
+                             : SMALL;
   p.tiles = p.kind == TILE256  ? t256
             : p.kind == PARTED ? ((M + 255) / 256) * ((N + 127) / 128)
             : p.kind == SMALL  ? tiles_of(M, N, 64)
@@ -1073,10 +1075,10 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool f32, bool tiled, bool pa
   return p;
 }
 // Room for the split sums, however the operands turn out to be aligned.
-size_t split_workspace(int64_t M, int64_t N, int64_t K, bool f32, bool packed, bool forward) {
+size_t split_workspace(int64_t M, int64_t N, int64_t K, int32_t dtype, bool packed, bool forward) {
   if (M == 0 || N == 0) return 0;
-  int64_t s = plan_product(M, N, K, f32, true, packed, forward).splits;
-  if (!packed) s = std::max(s, plan_product(M, N, K, f32, false, packed, forward).splits);
+  int64_t s = plan_product(M, N, K, dtype, true, packed, forward).splits;
+  if (!packed) s = std::max(s, plan_product(M, N, K, dtype, false, packed, forward).splits);
   return s > 1 ? align256(4 * (size_t)s * (size_t)M * (size_t)N) : 0;
 }
 
@@ -1094,7 +1096,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value && !packed &&
                        tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
                        tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
-  const Plan p = plan_product(g.M, g.N, g.K, dtype == EEC_F32, aligned, packed, A_KC && B_KC);
+  const Plan p = plan_product(g.M, g.N, g.K, dtype, aligned, packed, A_KC && B_KC);
   g.k_split = p.k_split;
   e.M = g.M;
   e.N = g.N;
@@ -1109,6 +1111,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
     if (p.kind == PARTED) k_parted<A_KC, B_KC><<<grid, 512, 0, st>>>(t, e);
   } else if constexpr (!std::is_same<T, e4m3_wide>::value) {
     if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8, 4><<<grid, 512, 0, st>>>(t, e);
+    if (p.kind == TILE128X2) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 4><<<grid, 256, 0, st>>>(t, e);
     if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 8><<<grid, 256, 0, st>>>(t, e);
   }
   if constexpr (A_KC && B_KC) {
@@ -1147,7 +1150,7 @@ FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_w = at;
   if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  p.bytes = at + split_workspace(rows, outer, inner, dtype == EEC_F32, p.packed, true);
+  p.bytes = at + split_workspace(rows, outer, inner, dtype, p.packed, true);
   return p;
 }
 
@@ -1180,8 +1183,8 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   p.off_wp = at;
   if (p.packed) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  at += std::max(split_workspace(rows, inner, outer, dtype == EEC_F32, p.packed, false),
-                 split_workspace(outer, inner, rows, dtype == EEC_F32, p.packed, false));
+  at += std::max(split_workspace(rows, inner, outer, dtype, p.packed, false),
+                 split_workspace(outer, inner, rows, dtype, p.packed, false));
   p.bytes = at;
   return p;
 }
