@@ -363,7 +363,9 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   constexpr int P = M_::PLANES;
   using SA = Stage<T, A_KC, BM>;
   using SB = Stage<T, B_KC, BN>;
-  constexpr int TILES = P * (SA::PLANE + SB::PLANE), SUMS = 4 * 4096;  // 4 KB of each wave for a matrix tile's sums
+  // sums: 4 KB of each wave for a matrix tile, two tiles at a time (one at a time the
+  // compiler picks the tile by a runtime index and keeps all of acc in scratch memory)
+  constexpr int PER = MI > 1 ? 2 : 1, TILES = P * (SA::PLANE + SB::PLANE), SUMS = 4 * PER * 4096;
   __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
   char* lds_b = lds + P * SA::PLANE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -406,7 +408,6 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
     }
   }
   __syncthreads();
-  constexpr int PER = MI > 1 && sizeof(lds) >= 2 * SUMS ? 2 : 1;
   finish_wave<O, MI, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
