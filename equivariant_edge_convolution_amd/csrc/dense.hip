@@ -61,13 +61,15 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
 #pragma unroll
     for (int i = 0; i < L; ++i) v[i] += c.bias[i];
   }
-  if (e.preact) store_run((O*)e.preact + m * e.N + c.n, c.left, v);
+  // rows that do not start on cache lines leave parts of lines for the L2 to join
+  const bool once = e.N * (int64_t)sizeof(O) % 128 == 0;
+  if (e.preact) store_run((O*)e.preact + m * e.N + c.n, c.left, v, once);
   act_values<O>(v, e.act);
   if (e.residual) {
 #pragma unroll
     for (int i = 0; i < L; ++i) v[i] += (float)r.v[i];
   }
-  store_run((O*)e.y + m * e.N + c.n, c.left, v);
+  store_run((O*)e.y + m * e.N + c.n, c.left, v, once);
 }
 
 // Finishes (or, split, stores) the ROWS x 64 sums of a wave, which it has put in

@@ -57,9 +57,10 @@ __device__ __forceinline__ void load_run(const T* __restrict__ p, int64_t valid,
   for (int i = 0; i < N; ++i) v[i] = (float)t[i];
 }
 
-// The first `valid` of N floats, each rounded once to T (to nearest even).
+// The first `valid` of N floats, each rounded once to T (to nearest even); past the
+// L2 unless `once` (uniform) is false.
 template <typename T, int N>
-__device__ __forceinline__ void store_run(T* __restrict__ p, int64_t valid, const float (&v)[N]) {
+__device__ __forceinline__ void store_run(T* __restrict__ p, int64_t valid, const float (&v)[N], bool once = true) {
   if (valid >= N) {
     T t[N];
 #pragma unroll
@@ -67,7 +68,10 @@ __device__ __forceinline__ void store_run(T* __restrict__ p, int64_t valid, cons
     if constexpr (sizeof(t) == 16) {
       i32x4 q;
       __builtin_memcpy(&q, t, 16);
-      __builtin_nontemporal_store(q, (i32x4_any*)p);
+      if (once)
+        __builtin_nontemporal_store(q, (i32x4_any*)p);
+      else
+        *(i32x4_any*)p = q;
     } else {
       __builtin_memcpy(p, t, sizeof(t));
     }
