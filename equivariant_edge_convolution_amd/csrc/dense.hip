@@ -354,7 +354,7 @@ struct Stage {
 
 // Any size, stride and alignment: WM x WN waves with MI * 16 x 64 of C each.
 // Operands pass through registers (where float32 is split into its parts and
-// k-major ones are turned) into LDS rows of 32 k; the next tile's loads are in
+// k-major ones are turned) into LDS rows of 32 k; the next two steps' loads are in
 // flight while the present one is multiplied.  B is the first factor of the matrix
 // instruction, so a lane holds four adjacent columns of one row of C.
 template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
@@ -376,21 +376,20 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
   f32x4 acc[MI][4] = {};
-  SA sa;
-  SB sb;
-  if (kb < ke) {
-    sa.load((const T*)g.a, g.lda, m0, g.M, kb, ke);
-    sb.load((const T*)g.b, g.ldb, n0, g.N, kb, ke);
-  }
-  for (int64_t k = kb; k < ke; k += GBK) {
+  SA sa[2];
+  SB sb[2];
+  auto load = [&](int s, int64_t k) {
+    if (k >= ke) return;
+    sa[s].load((const T*)g.a, g.lda, m0, g.M, k, ke);
+    sb[s].load((const T*)g.b, g.ldb, n0, g.N, k, ke);
+  };
+  // the step from k, staged in registers s; then s is loaded for the step after the next
+  auto step = [&](int s, int64_t k) {
     __syncthreads();
-    sa.store(lds);
-    sb.store(lds_b);
+    sa[s].store(lds);
+    sb[s].store(lds_b);
     __syncthreads();
-    if (k + GBK < ke) {
-      sa.load((const T*)g.a, g.lda, m0, g.M, k + GBK, ke);
-      sb.load((const T*)g.b, g.ldb, n0, g.N, k + GBK, ke);
-    }
+    load(s, k + 2 * GBK);
     typename M_::Frag fa[MI][P], fb[P];
     const int at = (lane & 15) * SA::ROW + (lane >> 4) * 8 * (int)sizeof(typename M_::E);
 #pragma unroll
@@ -408,6 +407,12 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
 #pragma unroll
       for (int i = 0; i < MI; ++i) acc[i][j] = M_::mul(fb, fa[i], acc[i][j]);
     }
+  };
+  load(0, kb);
+  load(1, kb + GBK);
+  for (int64_t k = kb; k < ke; k += 2 * GBK) {
+    step(0, k);
+    if (k + GBK < ke) step(1, k + GBK);
   }
   __syncthreads();
   finish_wave<O, MI, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) {
@@ -1029,11 +1034,15 @@ constexpr int64_t FEW_ROWS = 32;
 
 // Whether a product is worth packing for.  Packing reads and writes the operands
 // once, in proportion to (M + N) K, and what it gains over the general kernel goes
-// with M N K.
+// with M N K; in float32 the kernel behind it needs enough of its 256 x 128 tiles.
 bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype) {
   if (M <= FEW_ROWS || N <= FEW_ROWS) return false;
   if (M > 1 << 20 || N > 1 << 20 || K > 1 << 20) return false;  // lanes' offsets within a tile fit 31 bits
-  const double least = dtype == EEC_F32 ? 192 : 128;
+  if (dtype == EEC_F32) {
+    const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
+    if (tiles * (K >= 1024 ? K / 256 : 1) < 100) return false;
+  }
+  const double least = dtype == EEC_F32 ? 96 : 128;
   return (double)M * N >= least * (M + N) && (double)M * N * K >= 4e8;
 }
 
@@ -1092,13 +1101,14 @@ bool tiled_operand(const void* p, int64_t ld, int64_t along, int size) {
   return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && along * size % 16 == 0 && ld * size < (1 << 22);
 }
 
-// One product; `packed`: the operands are as k_pack leaves them.
+// One product; packed_*: the operand is as k_pack leaves it.
 template <typename T, typename O, bool A_KC, bool B_KC>
-void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bool packed) {
+void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bool packed_a, bool packed_b) {
   if (g.M == 0 || g.N == 0) return;
-  const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value && !packed &&
-                       tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T)) &&
-                       tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T));
+  const bool packed = packed_a && packed_b;
+  const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value &&
+                       (packed_a || tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T))) &&
+                       (packed_b || tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T)));
   const Plan p = plan_product(g.M, g.N, g.K, dtype, aligned, packed, A_KC && B_KC);
   g.k_split = p.k_split;
   e.M = g.M;
@@ -1107,8 +1117,8 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   const dim3 grid((unsigned)(p.tiles * p.splits));
   Product t = g;
   // what is loaded along memory may run into the padding, which is there and zero
-  if (packed && !A_KC) t.M = t.lda;
-  if (packed && !B_KC) t.N = t.ldb;
+  if (packed_a && !A_KC) t.M = t.lda;
+  if (packed_b && !B_KC) t.N = t.ldb;
   if constexpr (std::is_same<T, float>::value) {
     t.K = up(g.K, 128);
     if (p.kind == PARTED) k_parted<A_KC, B_KC><<<grid, 512, 0, st>>>(t, e);
@@ -1167,27 +1177,35 @@ int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
 
 // The backward's: gz (packed or not), column sums, x and w packed, split sums.
 struct BwdPlan {
-  bool packed;
-  size_t off_gz, off_part, off_gzp, off_xp, off_wp, off_split, bytes;
+  bool gz, others;  // packed
+  size_t off_gz, off_part, off_xp, off_wp, off_split, bytes;
 };
 BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
   BwdPlan p{};
-  p.packed = worth_packing(rows, inner, outer, dtype) && worth_packing(outer, inner, rows, dtype) &&
-             (dtype == EEC_F32 || outer % 8 != 0 || inner % 8 != 0);
+  if (dtype == EEC_F32) {
+    p.gz = p.others = worth_packing(rows, inner, outer, dtype) && worth_packing(outer, inner, rows, dtype);
+  } else {
+    p.others = inner % 8 != 0 && worth_packing(rows, inner, outer, dtype) && worth_packing(outer, inner, rows, dtype);
+    // gz passes through k_act_grad anyway, or is small beside what gx and gw take
+    p.gz = outer % 8 != 0 && (p.others || inner % 8 == 0) && rows > FEW_ROWS && outer < 1 << 20 &&
+           (act != EEC_ACT_NONE || (double)rows * outer * inner >= 4e8);
+  }
   size_t at = 0;
   p.off_gz = at;
-  if (act != EEC_ACT_NONE && !p.packed) at += align256((size_t)rows * (size_t)outer * (dtype == EEC_F32 ? 4 : 2));
+  if (p.gz)
+    at += packed_bytes(dtype, rows, outer);
+  else if (act != EEC_ACT_NONE)
+    at += align256((size_t)rows * (size_t)outer * (dtype == EEC_F32 ? 4 : 2));
   p.off_part = at;
   at += align256(4 * (size_t)act_grad_strips(rows, outer, dtype) * (size_t)outer);
-  p.off_gzp = at;
-  if (p.packed) at += packed_bytes(dtype, rows, outer);
   p.off_xp = at;
-  if (p.packed) at += packed_bytes(dtype, rows, inner);
+  if (p.others) at += packed_bytes(dtype, rows, inner);
   p.off_wp = at;
-  if (p.packed) at += packed_bytes(dtype, outer, inner);
+  if (p.others) at += packed_bytes(dtype, outer, inner);
   p.off_split = at;
-  at += std::max(split_workspace(rows, inner, outer, dtype, p.packed, false),
-                 split_workspace(outer, inner, rows, dtype, p.packed, false));
+  const bool both = p.gz && p.others;
+  at += std::max(split_workspace(rows, inner, outer, dtype, both, false),
+                 split_workspace(outer, inner, rows, dtype, both, false));
   p.bytes = at;
   return p;
 }
@@ -1217,9 +1235,9 @@ void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) {
     }
     float* split = (float*)(ws + p.off_split);
     if (a.dtype == EEC_E4M3)
-      product<E, O, true, true>(st, g, e, split, a.dtype, p.packed);
+      product<E, O, true, true>(st, g, e, split, a.dtype, p.packed, p.packed);
     else
-      product<O, O, true, true>(st, g, e, split, a.dtype, p.packed);
+      product<O, O, true, true>(st, g, e, split, a.dtype, p.packed, p.packed);
   });
 }
 
@@ -1232,8 +1250,8 @@ void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
   by_type(a.dtype, [&](auto zero) {
     using T = decltype(zero);
     const bool products = a.gx != nullptr || a.gw != nullptr;
-    const bool packed = p.packed && products, shaped = a.act != EEC_ACT_NONE && products && !packed;
-    const Packing z = packing(a.dtype, nullptr, 0, a.rows, a.outer, packed ? ws + p.off_gzp : nullptr);
+    const bool packed = p.gz && products, shaped = a.act != EEC_ACT_NONE && products && !packed;
+    const Packing z = packing(a.dtype, nullptr, 0, a.rows, a.outer, packed ? ws + p.off_gz : nullptr);
     if (a.outer > 0 && ((shaped && a.rows > 0) || a.gbias || packed)) {
       const int64_t strips = act_grad_strips(a.rows, a.outer, a.dtype), cols = 64 * VEC<T>;
       const int64_t rows = packed ? z.to_rows : a.rows, width = packed ? z.to_ld : a.outer;
@@ -1244,26 +1262,30 @@ void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
       if (a.gbias && strips > 1)
         launch_column_sum(st, a.dtype, (const float*)(ws + p.off_part), (int)strips, a.outer, a.gbias);
     }
-    const void* gz = shaped ? (const void*)(ws + p.off_gz) : a.gy;
-    const int64_t ldgz = shaped ? a.outer : a.ldgy;
-    Product gx{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0, 0, 0};
-    Product gw{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0, 0, 0};
-    if (packed) {
+    const void* gz = packed ? z.to : shaped ? ws + p.off_gz : (const char*)a.gy;
+    const int64_t ldgz = packed ? z.to_ld : shaped ? a.outer : a.ldgy;
+    Product gx{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0, z.plane, 0};
+    Product gw{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0, z.plane, 0};
+    if (p.others && products) {
       const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, a.gw ? ws + p.off_xp : nullptr);
       const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, a.gx ? ws + p.off_wp : nullptr);
       pack<T>(st, Packings{{x, w}});
-      gx = Product{z.to, w.to, z.to_ld, w.to_ld, a.rows, a.inner, a.outer, 0, z.plane, w.plane};
-      gw = Product{z.to, x.to, z.to_ld, x.to_ld, a.outer, a.inner, a.rows, 0, z.plane, x.plane};
+      gx.b = w.to;
+      gx.ldb = w.to_ld;
+      gx.b_plane = w.plane;
+      gw.b = x.to;
+      gw.ldb = x.to_ld;
+      gw.b_plane = x.plane;
     }
     float* split = (float*)(ws + p.off_split);
     Epilogue e{};
     if (a.gx) {
       e.y = a.gx;
-      product<T, T, true, false>(st, gx, e, split, a.dtype, p.packed);
+      product<T, T, true, false>(st, gx, e, split, a.dtype, packed, p.others);
     }
     if (a.gw) {
       e.y = a.gw;
-      product<T, T, false, false>(st, gw, e, split, a.dtype, p.packed);
+      product<T, T, false, false>(st, gw, e, split, a.dtype, packed, p.others);
     }
   });
 }
