@@ -11,6 +11,7 @@ so nothing can silently fall back to another implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -467,6 +468,16 @@ def _address(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace(rows: int, outer: int, inner: int, dtype: int, out_dtype: int) -> int:
+    return lib().eec_linear_workspace_bytes(rows, outer, inner, dtype, out_dtype)
+
+
+def _new_rows(like: torch.Tensor, rows: int, n: int) -> torch.Tensor:
+    """A contiguous [rows][n] of the same type (empty_like, where it serves, is the quickest way to one)."""
+    return torch.empty_like(like) if like.is_contiguous() else like.new_empty((rows, n))
+
+
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                  eps: float = 1e-6, quantize: bool = False, save_rstd: bool = False) -> dict:
     """eec_add_rms_norm on rows of ``x`` (any row stride): ``y``, ``sum`` (x +
@@ -476,16 +487,17 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: 
     ldx = _matrix(x, "x", rows, n, dt, dev)
     ldr = _matrix(residual, "residual", rows, n, dt, dev) if residual is not None else 0
     w = _vector(weight, "weight", n, dt, dev)
-    out = dict(y=torch.empty((rows, n), dtype=torch.float8_e4m3fn if quantize else dt, device=dev), sum=x)
+    y = torch.empty((rows, n), dtype=torch.float8_e4m3fn, device=dev) if quantize else _new_rows(x, rows, n)
+    out = dict(y=y, sum=x)
     total = scale = rstd = None
     if residual is not None:
-        total = out["sum"] = torch.empty((rows, n), dtype=dt, device=dev)
+        total = out["sum"] = _new_rows(x, rows, n)
     if quantize:
         scale = out["scale"] = torch.empty(rows, dtype=torch.float32, device=dev)
     if save_rstd:
         rstd = out["rstd"] = torch.empty(rows, dtype=torch.float32, device=dev)
     _check(lib().eec_add_rms_norm(_raw_stream(dev), rows, n, DTYPES[dt], x.data_ptr(), ldx, _address(residual), ldr, w,
-                                  float(eps), _address(total), out["y"].data_ptr(), _address(scale), _address(rstd)),
+                                  float(eps), _address(total), y.data_ptr(), _address(scale), _address(rstd)),
            "add_rms_norm")
     return out
 
@@ -500,7 +512,7 @@ def add_rms_norm_backward(gy: torch.Tensor, sum: torch.Tensor, weight: torch.Ten
     ldgs = _matrix(gsum, "gsum", rows, n, dt, dev) if gsum is not None else 0
     w = _vector(weight, "weight", n, dt, dev)
     rs = _vector(rstd, "rstd", rows, torch.float32, dev)
-    gx = torch.empty((rows, n), dtype=dt, device=dev)
+    gx = _new_rows(sum, rows, n)
     gw = ws = None
     if weight is not None:
         gw = torch.empty(n, dtype=dt, device=dev)
@@ -531,15 +543,16 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     xs = _vector(x_scale, "x_scale", rows, torch.float32, dev)
     wsc = _vector(w_scale, "w_scale", n, torch.float32, dev)
     b = _vector(bias, "bias", n, ot, dev)
-    y = torch.empty((rows, n), dtype=ot, device=dev)
+    y = x.new_empty((rows, n)) if ot == dt else torch.empty((rows, n), dtype=ot, device=dev)
     out = dict(y=y)
     if save_preact:
         out["preact"] = torch.empty((rows, n), dtype=ot, device=dev)
     ws = workspace
+    dt, ot = DTYPES[dt], DTYPES[ot]
     if ws is None:
-        need = lib().eec_linear_workspace_bytes(rows, n, k, DTYPES[dt], DTYPES[ot])
+        need = _linear_workspace(rows, n, k, dt, ot)
         ws = _workspace(need, dev) if need else None
-    _check(lib().eec_linear(_raw_stream(dev), rows, n, k, DTYPES[dt], DTYPES[ot], x.data_ptr(), ldx, xs, w.data_ptr(),
+    _check(lib().eec_linear(_raw_stream(dev), rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(),
                             ldw, wsc, b, _address(residual), ldr, ACTS[act], y.data_ptr(), _address(out.get("preact")),
                             _address(ws), ws.numel() if ws is not None else 0), "linear")
     return out
@@ -561,8 +574,7 @@ def linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: 
             raise ValueError("an activation's backward needs preact")
         if _matrix(preact, "preact", rows, n, dt, dev) != n:
             raise ValueError("preact must be contiguous")
-    gx = torch.empty((rows, k), dtype=dt, device=dev)
-    gw = torch.empty((n, k), dtype=dt, device=dev)
+    gx, gw = _new_rows(x, rows, k), _new_rows(w, n, k)
     gb = torch.empty(n, dtype=dt, device=dev) if bias else None
     ws = workspace
     if ws is None:
