@@ -125,7 +125,7 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, 
   }
 }
 // All of a wave's GROUPS matrix tiles of HIGH rows, PER of them at a time through
-// its own LDS; put(i, chunk(c)) writes the c-th four adjacent columns of tile i.
+// its own LDS; put(i, rows) writes the sums of tile i there.
 template <typename O, int GROUPS, int HIGH, int PER, typename Put>
 __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split, Put put) {
 #pragma unroll 1
@@ -1033,17 +1033,22 @@ int64_t tiles_of(int64_t M, int64_t N, int b) { return ((M + b - 1) / b) * ((N +
 constexpr int64_t FEW_ROWS = 32;
 
 // Whether a product is worth packing for.  Packing reads and writes the operands
-// once, in proportion to (M + N) K, and what it gains over the general kernel goes
-// with M N K; in float32 the kernel behind it needs enough of its 256 x 128 tiles.
-bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype) {
+// once, in proportion to (M + N) K, and costs a launch; what it gains over the general
+// kernel goes with M N K.  Kernel times, packed against general:
+//   bf16 forward, odd k     1024^3 23 us, 19;  2048 x 2048 x 512 21, 34;  1536^3 32, 33
+//   bf16 gx + gw, odd rows  700^3 37, 31;  1024^3 34, 53;  8192 x 128 x 512 32, 35
+//   float32 forward         700^3 62, 26;  1024^3 37, 46;  2048 x 2048 x 512 52, 67;
+//                           8192 x 128 x 512 53, 28
+// In float32 the kernel behind it needs enough of its 256 x 128 tiles and splits.
+bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype, bool forward) {
   if (M <= FEW_ROWS || N <= FEW_ROWS) return false;
   if (M > 1 << 20 || N > 1 << 20 || K > 1 << 20) return false;  // lanes' offsets within a tile fit 31 bits
   if (dtype == EEC_F32) {
     const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
     if (tiles * (K >= 1024 ? K / 256 : 1) < 100) return false;
   }
-  const double least = dtype == EEC_F32 ? 96 : 128;
-  return (double)M * N >= least * (M + N) && (double)M * N * K >= 4e8;
+  const double least = dtype != EEC_F32 && forward ? 2e9 : 4e8;
+  return (double)M * N >= 96.0 * (M + N) && (double)M * N * K >= least;
 }
 
 // How a product is run: a rule on sizes and on whether the operands take the tiled
@@ -1096,7 +1101,7 @@ size_t split_workspace(int64_t M, int64_t N, int64_t K, int32_t dtype, bool pack
 
 // Whether an operand of `size`-byte elements goes into LDS by 16-byte direct
 // loads: aligned rows, a whole number of 16-byte chunks along memory, and lanes'
-// offsets within a tile (256 lines or 64 k) that fit 31 bits.
+// offsets within a tile (256 lines or 32 k) that fit 31 bits.
 bool tiled_operand(const void* p, int64_t ld, int64_t along, int size) {
   return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && along * size % 16 == 0 && ld * size < (1 << 22);
 }
@@ -1155,7 +1160,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
   FwdPlan p{};
   const bool exact = dtype == EEC_E4M3 && out_dtype == EEC_F32;  // widened by the general kernel
-  p.packed = !exact && worth_packing(rows, outer, inner, dtype) &&
+  p.packed = !exact && worth_packing(rows, outer, inner, dtype, true) &&
              (dtype == EEC_F32 || inner * packed_size(dtype) % 16 != 0);
   size_t at = 0;
   p.off_x = at;
@@ -1183,9 +1188,9 @@ struct BwdPlan {
 BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
   BwdPlan p{};
   if (dtype == EEC_F32) {
-    p.gz = p.others = worth_packing(rows, inner, outer, dtype) && worth_packing(outer, inner, rows, dtype);
+    p.gz = p.others = worth_packing(rows, inner, outer, dtype, false) && worth_packing(outer, inner, rows, dtype, false);
   } else {
-    p.others = inner % 8 != 0 && worth_packing(rows, inner, outer, dtype) && worth_packing(outer, inner, rows, dtype);
+    p.others = inner % 8 != 0 && worth_packing(rows, inner, outer, dtype, false) && worth_packing(outer, inner, rows, dtype, false);
     // gz passes through k_act_grad anyway, or is small beside what gx and gw take
     p.gz = outer % 8 != 0 && (p.others || inner % 8 == 0) && rows > FEW_ROWS && outer < 1 << 20 &&
            (act != EEC_ACT_NONE || (double)rows * outer * inner >= 4e8);
