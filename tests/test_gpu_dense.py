@@ -204,9 +204,9 @@ def test_linear_and_backward_packed(rows, inner, outer, dt):
     test_linear_and_backward(rows, inner, outer, dt)
 
 
-def test_linear_packed_special_values():
+@pytest.mark.parametrize("rows,inner,outer", [(640, 1100, 601), (1301, 1301, 1301)])
+def test_linear_packed_special_values(rows, inner, outer):
     """An infinity or NaN in a packed float32 product reaches its own row alone, also beside values whose parts are zero."""
-    rows, inner, outer = 640, 1100, 601
     x = torch.full((rows, inner), 2.0, device=DEV)
     w = torch.full((outer, inner), 0.5, device=DEV)
     w[3] = -0.5
@@ -224,6 +224,57 @@ def test_linear_packed_special_values():
 @pytest.mark.parametrize("rows,inner,outer", [(640, 1100, 601), (517, 1543, 521), (300, 4097, 1000), (1301, 1305, 1301)])
 def test_linear_e4m3_packed(rows, inner, outer):
     test_linear_e4m3(rows, inner, outer, torch.bfloat16)
+
+
+# several workgroups a CU, 256 x 256 tiles; aligned and odd
+LARGE_SHAPES = [(2048, 2064, 2080), (2051, 2049, 2050), (2944, 2912, 2960), (2901, 2905, 2899)]
+
+
+def large_within(got, ref, bound, what):
+    """`within` on the device, of finite values."""
+    over = (got.double() - ref).abs() - bound
+    at = int(torch.argmax(over))
+    assert bool(torch.isfinite(got.float()).all()), what
+    assert float(over.flatten()[at]) <= 0, f"{what}[{at}]: {float(got.flatten()[at])} against {float(ref.flatten()[at])}"
+
+
+@pytest.mark.parametrize("dt", TYPES + [torch.float8_e4m3fn], ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", LARGE_SHAPES)
+def test_linear_large(rows, inner, outer, dt):
+    """As the smaller ones, the 64-bit products taken by the library on the device."""
+    say(f"[dense] large {rows}x{inner}x{outer} {dt}")
+    g = torch.Generator().manual_seed(rows + 3 * inner + 5 * outer)
+    eight = dt == torch.float8_e4m3fn
+    ot = torch.bfloat16 if eight else dt
+    x = rand(g, rows, inner, dtype=dt, scale=30.0 if eight else 1.0)
+    w = rand(g, outer, inner, dtype=dt, scale=30.0 if eight else inner ** -0.5)
+    xs = rand(g, rows).abs() * 0.01 + 0.001 if eight else None
+    ws = (rand(g, outer).abs() * 0.01 + 0.001) * inner ** -0.5 if eight else None
+    bias, res = rand(g, outer, dtype=ot), rand(g, rows, outer, dtype=ot)
+    out = B.linear(x, w, bias, "silu", res, x_scale=xs, w_scale=ws, out_dtype=ot, save_preact=True)
+    X, W = x.float().double(), w.float().double()
+    if eight:
+        X, W = X * xs.double()[:, None], W * ws.double()[:, None]
+    z = X @ W.t() + bias.double()
+    y = torch.nn.functional.silu(z) + res.double()
+    ez = (2 * inner + 32) * EPS * (X.abs() @ W.abs().t() + bias.double().abs())
+    large_within(out["preact"], z, ez + U[ot] * z.abs() + TINY[ot], "preact")
+    large_within(out["y"], y, 1.13 * ez + 16 * EPS * (z.abs() + y.abs()) + U[ot] * y.abs() + TINY[ot], "y")
+    if eight:
+        return
+    gy = rand(g, rows, outer, dtype=dt)
+    b = B.linear_backward(gy, x, w, out["preact"], "silu", bias=True)
+    z, G = out["preact"].double(), gy.double()
+    p = torch.sigmoid(z)
+    gz = G * p * (1 + z * (1 - p))
+    formula = 16 * EPS * G.abs() * (1 + z.abs())
+    e = U[dt] * gz.abs() + formula + TINY[dt]
+    a = gz.abs() + e
+    for what, ref, bound in (
+            ("gx", gz @ W, e @ W.abs() + (2 * outer + 32) * EPS * (a @ W.abs())),
+            ("gw", gz.t() @ X, e.t() @ X.abs() + (2 * rows + 32) * EPS * (a.t() @ X.abs())),
+            ("gbias", gz.sum(dim=0), formula.sum(dim=0) + (2 * rows + 32) * EPS * a.sum(dim=0))):
+        large_within(b[what], ref, bound + U[dt] * ref.abs() + TINY[dt], what)
 
 
 @pytest.mark.parametrize("ot", TYPES, ids=ids)
