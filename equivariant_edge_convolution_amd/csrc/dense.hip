@@ -37,25 +37,28 @@ struct Columns {
     if (e.w_scale) load_run(e.w_scale + n, left, scale);
   }
 };
+// What a row's L columns bring from memory to their epilogue.  It is loaded ahead,
+// for several rows at a time: the compiler keeps loads behind stores, and the wait
+// for a load is a wait for the stores before it.
 template <typename O, int L>
-struct Residual {
-  O v[L];  // as it comes from memory
+struct Incoming {
+  O residual[L];
+  float scale;
   __device__ __forceinline__ void load(const Epilogue& e, int64_t m, const Columns<O, L>& c) {
-    if (e.residual && m < e.M) load_raw<true>((const O*)e.residual + m * e.ldr + c.n, c.left, v);
+    if (m >= e.M) return;
+    if (e.residual) load_raw<true>((const O*)e.residual + m * e.ldr + c.n, c.left, residual);
+    if (e.x_scale) scale = e.x_scale[m];
   }
 };
 
-// L adjacent columns of one row, from their sums over k.  The residual comes
-// loaded, for several rows at a time: the compiler keeps loads behind stores, and
-// one after another each would wait for memory.
+// L adjacent columns of one row, from their sums over k.
 template <typename O, int L>
-__device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const Columns<O, L>& c, const Residual<O, L>& r,
+__device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const Columns<O, L>& c, const Incoming<O, L>& in,
                                            float (&v)[L]) {
   if (m >= e.M) return;
   if (e.x_scale) {
-    const float xs = e.x_scale[m];
 #pragma unroll
-    for (int i = 0; i < L; ++i) v[i] *= xs * c.scale[i];
+    for (int i = 0; i < L; ++i) v[i] *= in.scale * c.scale[i];
   }
   if (e.bias) {
 #pragma unroll
@@ -67,82 +70,112 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
   act_values<O>(v, e.act);
   if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) v[i] += (float)r.v[i];
+    for (int i = 0; i < L; ++i) v[i] += (float)in.residual[i];
   }
   store_run((O*)e.y + m * e.N + c.n, c.left, v, once);
 }
 
-// Finishes (or, split, stores) the ROWS x 64 sums of a wave, which it has put in
-// LDS row by row of 256 bytes, the 16-byte chunk c of row r at c ^ (r & 15).  From
-// there each access takes 16 bytes a lane of whole rows, and the code is short
-// whatever a lane's registers hold: written out for every register it no longer
-// fits the instruction cache (8192 x 8192 x 32 bf16: 64 us, this 46 us).
-// Up to eight rows' residuals a lane are on their way together.
-template <typename O, int ROWS>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, const char* lds, int64_t m0, int64_t n0, int split) {
-  constexpr int L = 16 / (int)sizeof(O), PER = L;              // columns of a lane, rows of one access
-  constexpr int TOGETHER = ROWS / PER < 8 ? ROWS / PER : 8;
-  static_assert(ROWS % (TOGETHER * PER) == 0, "whole accesses");
-  const int lane = threadIdx.x & 63, columns = (int)min((int64_t)64, e.N - n0);
-  float* part = e.part ? e.part + split * e.M * e.N : nullptr;
-  const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
-  if (col + L <= columns) {
-    const Columns<O, L> c(e, n0 + col, L);
-#pragma unroll 1
-    for (int r = r0; r < ROWS; r += TOGETHER * PER) {
-      Residual<O, L> res[TOGETHER];
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) res[i].load(e, m0 + r + i * PER, c);
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        const int row = r + i * PER;
-        float v[L];
-#pragma unroll
-        for (int u = 0; u < L; u += 4)
-          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
-        if (part == nullptr)
-          finish_run<O, L>(e, m0 + row, c, res[i], v);
-        else if (m0 + row < e.M)
-          store_run(part + (m0 + row) * e.N + n0 + col, L, v);
-      }
-    }
-  }
-  // the last columns of C that make no whole run: a row a lane, a column at a time
-  if (columns % L > 0 && lane < ROWS) {
-    const int64_t m = m0 + lane;
-#pragma unroll 1
-    for (int at = columns / L * L; at < columns; ++at) {
-      const Columns<O, 1> c(e, n0 + at, 1);
-      Residual<O, 1> res;
-      res.load(e, m, c);
-      float v[1];
-      __builtin_memcpy(v, lds + (lane * 256 + ((at / 4) ^ (lane & 15)) * 16 + at % 4 * 4), 4);
-      if (part == nullptr)
-        finish_run<O, 1>(e, m, c, res, v);
-      else if (m < e.M)
-        part[m * e.N + n0 + at] = v[0];
-    }
-  }
-}
-// All of a wave's GROUPS matrix tiles of HIGH rows, PER of them at a time through
-// its own LDS; put(i, rows) writes the sums of tile i there.
-template <typename O, int GROUPS, int HIGH, int PER, typename Put>
-__device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split, Put put) {
-#pragma unroll 1
-  for (int g = 0; g < GROUPS; g += PER) {
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i)
-      if (i / PER * PER == g) put(i, lds + i % PER * HIGH * 256);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    finish_rows<O, PER * HIGH>(e, lds, m0 + g * HIGH, n0, split);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
-}
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 // Chunk c (four adjacent columns) of a row of a wave's sums.
 __device__ __forceinline__ void put_sums(char* rows, int row, int c, const f32x4& v) {
   __builtin_memcpy(__builtin_assume_aligned(rows + (row * 256 + (c ^ (row & 15)) * 16), 16), &v, 16);
 }
+// The tiles as the matrix instructions leave them: 16 rows x 4 x 16 columns, 32 x 2 x 32.
+__device__ __forceinline__ void put_tile(const f32x4 (&acc)[4], char* rows) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), acc[j]);
+}
+__device__ __forceinline__ void put_tile(const f32x16 (&acc)[2], char* rows) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const f32x4 v = {acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]};
+      put_sums(rows, threadIdx.x & 31, j * 8 + a * 2 + (threadIdx.x >> 5 & 1), v);
+    }
+}
 
+// Finishes (or, split, stores) all of a wave's GROUPS matrix tiles of HIGH rows x 64
+// columns, PER of them at a time through its own LDS: put_tile writes a tile's
+// sums there, row by row of 256 bytes, the 16-byte chunk c of row r at c ^ (r & 15),
+// and the tiles move up, so that the registers of those that are done are free.
+// From there each access takes 16 bytes a lane of whole rows, and the code is short
+// whatever a lane's registers hold: written out for every register it no longer
+// fits the instruction cache (8192 x 8192 x 32 bf16: 64 us, this 46 us).
+// What up to four rows a lane need from memory is on its way before the stores of the
+// four ahead of them (8192 x 2048 x 8192 bf16 with residual, bias and SiLU 299 us with
+// the loads behind those stores, 287 so; 2048 x 1024 x 2048 float32 60 and 48; with
+// nothing to load and no activation it costs 1 to 4 %).
+template <typename O, int HIGH, int PER, typename Acc, int GROUPS, int NB>
+__device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split,
+                                            Acc (&acc)[GROUPS][NB]) {
+  constexpr int ROWS = PER * HIGH, ALL = GROUPS * HIGH;
+  constexpr int L = 16 / (int)sizeof(O), APART = L;  // columns of a lane, rows of one access
+  constexpr int TOGETHER = ROWS / APART < 4 ? ROWS / APART : 4, BATCH = TOGETHER * APART;
+  static_assert(ROWS % BATCH == 0, "whole accesses");
+  const int lane = threadIdx.x & 63, columns = (int)min((int64_t)64, e.N - n0);
+  float* part = e.part ? e.part + split * e.M * e.N : nullptr;
+  const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
+  const bool whole = col + L <= columns;
+  const Columns<O, L> c(e, n0 + col, whole ? L : 0);
+  Incoming<O, L> next[TOGETHER];
+  const auto load = [&](int row) {
+    if (!whole || part != nullptr || row - r0 >= ALL) return;
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) next[i].load(e, m0 + row + i * APART, c);
+  };
+  load(r0);
+#pragma unroll 1
+  for (int g = 0; g < GROUPS; g += PER) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) put_tile(acc[i], lds + i * HIGH * 256);
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = i + PER < GROUPS ? acc[i + PER < GROUPS ? i + PER : 0][j] : Acc{};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int64_t top = m0 + g * HIGH;
+    if (whole) {
+#pragma unroll 1
+      for (int r = r0; r < ROWS; r += BATCH) {
+        Incoming<O, L> in[TOGETHER];
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) in[i] = next[i];
+        load(g * HIGH + r + BATCH);
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) {
+          const int row = r + i * APART;
+          float v[L];
+#pragma unroll
+          for (int u = 0; u < L; u += 4)
+            __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
+          if (part == nullptr)
+            finish_run<O, L>(e, top + row, c, in[i], v);
+          else if (top + row < e.M)
+            store_run(part + (top + row) * e.N + n0 + col, L, v);
+        }
+      }
+    }
+    // the last columns of C that make no whole run: a row a lane, a column at a time
+    if (columns % L > 0 && lane < ROWS) {
+      const int64_t m = top + lane;
+#pragma unroll 1
+      for (int at = columns / L * L; at < columns; ++at) {
+        const Columns<O, 1> one(e, n0 + at, 1);
+        Incoming<O, 1> in;
+        in.load(e, m, one);
+        float v[1];
+        __builtin_memcpy(v, lds + (lane * 256 + ((at / 4) ^ (lane & 15)) * 16 + at % 4 * 4), 4);
+        if (part == nullptr)
+          finish_run<O, 1>(e, m, one, in, v);
+        else if (m < e.M)
+          part[m * e.N + n0 + at] = v[0];
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
 // Adds the splits in order and finishes: 4 columns a thread.
 template <typename O>
 __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
@@ -161,9 +194,9 @@ __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
         for (int c = 0; c < 4; ++c) v[c] += t[s][c];
     }
     const Columns<O, 4> c(e, n, e.N - n);
-    Residual<O, 4> r;
-    r.load(e, m, c);
-    finish_run<O, 4>(e, m, c, r, v);
+    Incoming<O, 4> in;
+    in.load(e, m, c);
+    finish_run<O, 4>(e, m, c, in, v);
   }
 }
 
@@ -365,8 +398,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   constexpr int P = M_::PLANES;
   using SA = Stage<T, A_KC, BM>;
   using SB = Stage<T, B_KC, BN>;
-  // sums: 4 KB of each wave for a matrix tile, two tiles at a time (one at a time the
-  // compiler picks the tile by a runtime index and keeps all of acc in scratch memory)
+  // sums: 4 KB of each wave for a matrix tile, two tiles at a time
   constexpr int PER = MI > 1 ? 2 : 1, TILES = P * (SA::PLANE + SB::PLANE), SUMS = 4 * PER * 4096;
   __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
   char* lds_b = lds + P * SA::PLANE;
@@ -415,10 +447,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
     if (k + GBK < ke) step(1, k + GBK);
   }
   __syncthreads();
-  finish_wave<O, MI, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
-  });
+  finish_wave<O, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, acc);
 }
 
 // ------------------------------------------------------------------ tiled product (16- and 8-bit, aligned)
@@ -427,7 +456,6 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // One operand's LDS tile of 64 bytes of k, filled by direct loads of 16 bytes a
 // lane (no registers, so later tiles' loads run under the present one's products).
@@ -557,10 +585,6 @@ struct Share {
     const Frag fb[1] = {b}, fa[1] = {a};
     acc[i][j] = Mat<T>::mul(fb, fa, acc[i][j]);
   }
-  __device__ __forceinline__ void put(int i, char* rows) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), acc[i][j]);
-  }
 };
 template <int MI>
 struct Share<e4m3, MI> {
@@ -570,15 +594,6 @@ struct Share<e4m3, MI> {
   f32x16 acc[GROUPS][NB] = {};
   __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {  // block scales of 2^0
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-  }
-  __device__ __forceinline__ void put(int i, char* rows) const {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const f32x4 v = {acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]};
-        put_sums(rows, threadIdx.x & 31, j * 8 + a * 2 + (threadIdx.x >> 5 & 1), v);
-      }
   }
 };
 template <typename S>
@@ -713,8 +728,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   static_assert(TA::BYTES >= SUMS * 256 && TB::BYTES >= SUMS * 256 && WAVES <= 8, "room for the sums");
   const int pair = wave >> 1;
   char *even = pair == 0 ? a0 : pair == 1 ? a1 : pair == 2 ? a2 : a3, *odd = pair == 0 ? b0 : pair == 1 ? b1 : pair == 2 ? b2 : b3;
-  finish_wave<O, S::GROUPS, S::ROWS, SUMS / S::ROWS>(
-      e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) { c.put(i, rows); });
+  finish_wave<O, S::ROWS, SUMS / S::ROWS>(e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, c.acc);
 #endif
 }
 
@@ -779,10 +793,7 @@ __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
   tile_barrier<0>();
   // 64 rows of sums in 16 KB for each wave: three in an A buffer, one in a B buffer
   char* mine = wave < 3 ? a0 + wave * 16384 : wave < 6 ? a1 + (wave - 3) * 16384 : wave == 6 ? b0 : b1;
-  finish_wave<float, 4, 16, 4>(e, mine, m0 + wm, n0 + wn, place.split, [&](int i, char* rows) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) put_sums(rows, lane & 15, j * 4 + (lane >> 4), acc[i][j]);
-  });
+  finish_wave<float, 16, 4>(e, mine, m0 + wm, n0 + wn, place.split, acc);
 #endif
 }
 
@@ -807,6 +818,11 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = (const T*)g.a + min((int64_t)(t * 16 + (lane & 15)), g.M - 1) * g.lda;
   f32x4 acc[MT] = {};
+  // the epilogue's inputs set out first, and are there when the sums are
+  const int64_t m = wave * 16 + (lane & 15);
+  const Columns<O, 4> columns(e, n0 + q * 4, wave < MT ? e.N - n0 - q * 4 : 0);
+  Incoming<O, 4> in;
+  if (wave < MT) in.load(e, m, columns);
   // A run of CHUNK k: lane group q holds STEPS * 8 adjacent ones, of which step s
   // multiplies the s-th 8 (the same k of both operands meet, which is all a sum asks).
   struct Run {
@@ -879,13 +895,7 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
 #pragma unroll
     for (int i = 1; i < WAVES; ++i) v += join[i][wave][lane];
     float r[4] = {v[0], v[1], v[2], v[3]};
-    const int64_t m = wave * 16 + (lane & 15);
-    if (n0 + q * 4 < e.N) {
-      const Columns<O, 4> c(e, n0 + q * 4, e.N - n0 - q * 4);
-      Residual<O, 4> res;
-      res.load(e, m, c);
-      finish_run<O, 4>(e, m, c, res, r);
-    }
+    if (n0 + q * 4 < e.N) finish_run<O, 4>(e, m, columns, in, r);
   }
 }
 
