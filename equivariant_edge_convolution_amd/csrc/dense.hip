@@ -1045,10 +1045,12 @@ constexpr int64_t FEW_ROWS = 32;
 // Whether a product is worth packing for.  Packing reads and writes the operands
 // once, in proportion to (M + N) K, and costs a launch; what it gains over the general
 // kernel goes with M N K.  Kernel times, packed against general:
-//   bf16 forward, odd k     1024^3 23 us, 19;  2048 x 2048 x 512 21, 34;  1536^3 32, 33
-//   bf16 gx + gw, odd rows  700^3 37, 31;  1024^3 34, 53;  8192 x 128 x 512 32, 35
-//   float32 forward         700^3 62, 26;  1024^3 37, 46;  2048 x 2048 x 512 52, 67;
-//                           8192 x 128 x 512 53, 28
+//   bf16 forward, odd k     1024^3 26 us, 20;  1531 x 2771 x 1029 42, 41;  2048 x 4096 x
+//   (GELU, bias, residual)  1025 44, 42;  4096 x 4096 x 513 45, 52;  2048^3 43, 55
+//   e4m3 forward, likewise  1024^3 21 us, 18;  1536^3 26, 26;  2048^3 32, 44
+//   bf16 gx + gw, odd rows  700^3 36, 31;  1024^3 35, 53;  8192 x 128 x 512 32, 35
+//   float32 forward         700^3 62, 25;  1024^3 37, 45;  2048 x 2048 x 512 51, 68;
+//                           8192 x 128 x 512 53, 27
 // In float32 the kernel behind it needs enough of its 256 x 128 tiles and splits.
 bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype, bool forward) {
   if (M <= FEW_ROWS || N <= FEW_ROWS) return false;
@@ -1057,7 +1059,7 @@ bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype, bool forward)
     const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
     if (tiles * (K >= 1024 ? K / 256 : 1) < 100) return false;
   }
-  const double least = dtype != EEC_F32 && forward ? 2e9 : 4e8;
+  const double least = !forward || dtype == EEC_F32 ? 4e8 : dtype == EEC_E4M3 ? 3e9 : 5e9;
   return (double)M * N >= 96.0 * (M + N) && (double)M * N * K >= least;
 }
 
@@ -1095,7 +1097,7 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool tiled, bo
   const bool general = p.kind == GENERAL || p.kind == SMALL;
   const int64_t step = 128;  // k of a split is a multiple of every kernel's tiles
   const int64_t least = general ? 128 : p.kind == PARTED ? 256 : 512;  // k of a split
-  int64_t s = K < 4 * least ? 1 : std::min<int64_t>((general ? 512 : 256) / p.tiles, K / least);
+  int64_t s = K < 4 * least ? 1 : std::min<int64_t>((p.kind == SMALL ? 512 : 256) / p.tiles, K / least);
   s = std::max<int64_t>(1, s);
   p.k_split = std::max<int64_t>(step, up((K + s - 1) / s, step));
   p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);

@@ -194,7 +194,8 @@ def test_linear_and_backward(rows, inner, outer, dt):
                (2 * rows + 32) * EPS * az.sum(axis=0) + U[dt] * np.abs(ref["gbias"]) + TINY[dt], f"{act} gbias")
 
 
-PACKED_SHAPES = [(640, 1100, 601), (700, 901, 777), (1031, 640, 643), (517, 1543, 521), (1301, 1301, 1301), (900, 512, 71)]
+PACKED_SHAPES = [(640, 1100, 601), (700, 901, 777), (1031, 640, 643), (517, 1543, 521), (1301, 1301, 1301), (900, 512, 71),
+                 (1751, 1701, 1711)]
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
@@ -221,7 +222,8 @@ def test_linear_packed_special_values(rows, inner, outer):
     np.testing.assert_allclose(rest, np.broadcast_to(ref, rest.shape), rtol=2.0 ** -22)
 
 
-@pytest.mark.parametrize("rows,inner,outer", [(640, 1100, 601), (517, 1543, 521), (300, 4097, 1000), (1301, 1305, 1301)])
+@pytest.mark.parametrize("rows,inner,outer", [(640, 1100, 601), (517, 1543, 521), (300, 4097, 1000), (1301, 1305, 1301),
+                                              (1501, 1505, 1503)])
 def test_linear_e4m3_packed(rows, inner, outer):
     test_linear_e4m3(rows, inner, outer, torch.bfloat16)
 
