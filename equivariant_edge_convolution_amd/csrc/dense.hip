@@ -51,15 +51,38 @@ struct Incoming {
   }
 };
 
+// v x_scale w_scale.  Scales of ordinary size (2^-50 to 2^51) are multiplied with each
+// other first; others could leave float32's range there, or with the sum, where the
+// result does not (1e-30 and 1e-15, 1e35 and 1e-35; an infinity would make a sum of 0
+// a NaN), so their mantissas and powers of two are taken apart.  Telling the two apart
+// takes 2 us of 138 (8192 x 4096 x 4096 e4m3).
+__device__ __forceinline__ bool ordinary(float scale) { return (__float_as_uint(scale) >> 23) - 77u <= 100u; }
+template <int L>
+__device__ __forceinline__ void scale_run(float (&v)[L], float row, const float (&columns)[L]) {
+  bool plain = ordinary(row);
+#pragma unroll
+  for (int i = 0; i < L; ++i) plain = plain && ordinary(columns[i]);
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] *= row * columns[i];
+  } else {
+    const float m = __builtin_amdgcn_frexp_mantf(row);
+    const int p = __builtin_amdgcn_frexp_expf(row);
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      float c = columns[i];
+      asm volatile("" : "+v"(c));  // taken apart here, not ahead of the loop over rows (16 registers)
+      v[i] = ldexpf(v[i] * (m * __builtin_amdgcn_frexp_mantf(c)), p + __builtin_amdgcn_frexp_expf(c));
+    }
+  }
+}
+
 // L adjacent columns of one row, from their sums over k.
 template <typename O, int L>
 __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const Columns<O, L>& c, const Incoming<O, L>& in,
                                            float (&v)[L]) {
   if (m >= e.M) return;
-  if (e.x_scale) {
-#pragma unroll
-    for (int i = 0; i < L; ++i) v[i] *= in.scale * c.scale[i];
-  }
+  if (e.x_scale) scale_run(v, in.scale, c.scale);
   if (e.bias) {
 #pragma unroll
     for (int i = 0; i < L; ++i) v[i] += c.bias[i];

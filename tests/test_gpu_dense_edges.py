@@ -1,0 +1,31 @@
+"""The dense operators where values, sizes and arguments are at their limits, against the definitions in 64 bits.
+
+Bounds as in test_gpu_dense.py: U of one rounding to the output's type, EPS = 2^-24 of each float32 operation."""
+import pytest
+import torch
+
+from equivariant_edge_convolution_amd import binding as B
+
+from gpu_util import DEV
+from test_gpu_dense import EPS, TINY, TYPES, U, f64, ids, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("ot", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", [(3, 64, 24), (70, 130, 50), (200, 256, 256)])
+def test_e4m3_scales_of_any_size(rows, inner, outer, ot):
+    """Row scales whose product, or whose product with the sum, leaves float32's range where z does not.
+
+    Constant codes, so that every sum over k is exact: what is left are the scales' two products and the output's rounding."""
+    for xs, ws, code in ((1e-30, 1e-15, 448.0), (1e-15, 1e-30, 448.0), (1e20, 1e20, 0.0), (1e35, 1e-35, 448.0),
+                         (1e-36, 1e36, 416.0), (3e-39, 7.0, 448.0), (0.01, 0.003, 448.0)):
+        x = torch.full((rows, inner), code, device=DEV).to(torch.float8_e4m3fn)
+        w = torch.full((outer, inner), 1.5, device=DEV).to(torch.float8_e4m3fn)
+        sx, sw = torch.full((rows,), xs, device=DEV), torch.full((outer,), ws, device=DEV)
+        y = B.linear(x, w, x_scale=sx, w_scale=sw, out_dtype=ot)["y"]
+        z = f64(sx)[:, None] * f64(sw)[None, :] * (inner * code * 1.5)
+        if ot == torch.float16 and z.max() > 65504.0:
+            assert bool(torch.isinf(y).all())
+        else:
+            within(y, z, (U[ot] + 4 * EPS) * z + TINY[ot], f"{xs} {ws} {code}")
