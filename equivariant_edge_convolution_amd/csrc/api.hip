@@ -612,10 +612,11 @@ eec_status eec_add_rms_norm_backward(void* stream, int64_t rows, int64_t width, 
 
 static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
   if (bad_size(rows) || bad_width(outer) || bad_width(inner)) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
-  // output tiles of one product, counted as the kernels launch them
-  const int64_t r = rows / 128 + 1, o = outer / 128 + 1, i = inner / 128 + 1;
-  if (r * o >= (1 << 22) || r * i >= (1 << 22) || o * i >= (1 << 22))
-    return fail(EEC_ERR_SHAPE, "a product of more than 2^36 outputs");
+  return EEC_OK;
+}
+// The outputs of one product that is asked for.
+static eec_status check_outputs(int64_t m, int64_t n) {
+  if (m > 0 && n > (int64_t(1) << 36) / m) return fail(EEC_ERR_SHAPE, "a product of more than 2^36 outputs");
   return EEC_OK;
 }
 
@@ -634,6 +635,7 @@ eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, 
     return fail(EEC_ERR_SHAPE, "out_dtype must be dtype (f32, f16 or bf16 with e4m3 operands)");
   TRY(check_act(act));
   TRY(check_linear(rows, outer, inner));
+  TRY(check_outputs(rows, outer));
   TRY(check_matrix(x, rows, inner, ldx, dtype, "x"));
   TRY(check_matrix(w, outer, inner, ldw, dtype, "w"));
   if (eight) {
@@ -672,6 +674,8 @@ eec_status eec_linear_backward(void* stream, int64_t rows, int64_t outer, int64_
   if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
   TRY(check_act(act));
   TRY(check_linear(rows, outer, inner));
+  if (gx) TRY(check_outputs(rows, inner));
+  if (gw) TRY(check_outputs(outer, inner));
   TRY(check_matrix(gy, rows, outer, ldgy, dtype, "gy"));
   if (gw) TRY(check_matrix(x, rows, inner, ldx, dtype, "x"));
   if (gx) TRY(check_matrix(w, outer, inner, ldw, dtype, "w"));

@@ -1141,10 +1141,30 @@ bool tiled_operand(const void* p, int64_t ld, int64_t along, int size) {
   return ((uintptr_t)p & 15) == 0 && ld * size % 16 == 0 && along * size % 16 == 0 && ld * size < (1 << 22);
 }
 
+// Rows of C of one launch: with at most 2^36 outputs its tiles then stay below 2^24, and
+// its threads (256 for a 128 x 128 tile, 512 for a 256 x 256 one) are counted in 32 bits.
+constexpr int64_t LAUNCH_ROWS = int64_t(1) << 30;
+
 // One product; packed_*: the operand is as k_pack leaves it.
 template <typename T, typename O, bool A_KC, bool B_KC>
 void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bool packed_a, bool packed_b) {
   if (g.M == 0 || g.N == 0) return;
+  if constexpr (A_KC) {  // the rows of gw are columns, at most 2^27
+    if (g.M > LAUNCH_ROWS) {  // k is not split there, and at most a 16-bit gz is packed: row after row, as it is
+      const int64_t first = g.M / 2;
+      Product rest = g;
+      Epilogue to = e;
+      g.M = first;
+      rest.M -= first;
+      rest.a = (const T*)g.a + first * g.lda;
+      to.y = (O*)e.y + first * g.N;
+      if (e.preact) to.preact = (O*)e.preact + first * g.N;
+      if (e.residual) to.residual = (const O*)e.residual + first * e.ldr;
+      if (e.x_scale) to.x_scale = e.x_scale + first;
+      product<T, O, A_KC, B_KC>(st, g, e, ws, dtype, packed_a, packed_b);
+      return product<T, O, A_KC, B_KC>(st, rest, to, ws, dtype, packed_a, packed_b);
+    }
+  }
   const bool packed = packed_a && packed_b;
   const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value &&
                        (packed_a || tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T))) &&

@@ -29,3 +29,24 @@ def test_e4m3_scales_of_any_size(rows, inner, outer, ot):
             assert bool(torch.isinf(y).all())
         else:
             within(y, z, (U[ot] + 4 * EPS) * z + TINY[ot], f"{xs} {ws} {code}")
+
+
+def test_rows_up_to_the_limit():
+    """2^31 - 1 rows of one column: one product of as many outputs, and sums over as many rows."""
+    rows = 2 ** 31 - 1
+    x = torch.empty((rows, 1), dtype=torch.bfloat16, device=DEV)
+    x.view(-1)[: rows // 2] = 3.0
+    x.view(-1)[rows // 2:] = -5.0
+    x[-1] = 7.0
+    w, bias = torch.full((1, 1), 2.0, dtype=x.dtype, device=DEV), torch.full((1,), 0.5, dtype=x.dtype, device=DEV)
+    y = B.linear(x, w, bias, residual=x)["y"]
+    for part in (slice(0, rows // 2), slice(rows // 2, rows - 1), slice(rows - 1, rows)):
+        v = float(x[part][0])
+        assert bool((y[part] == 3.0 * v + 0.5).all()), part
+    del y
+    b = B.linear_backward(x, x, w)
+    for part in (slice(0, rows // 2), slice(rows // 2, rows - 1), slice(rows - 1, rows)):
+        assert bool((b["gx"][part] == 2.0 * float(x[part][0])).all()), part
+    # sums of at most 2^22 equal terms are exact in float32; joined in order, then rounded
+    gw, gb = 9.0 * (rows // 2) + 25.0 * (rows // 2) + 49.0, -2.0 * (rows // 2) + 7.0
+    assert abs(float(b["gw"]) - gw) <= 2.0 ** -7 * gw and abs(float(b["gbias"]) - gb) <= 2.0 ** -7 * abs(gb)
