@@ -1064,6 +1064,8 @@ int64_t tiles_of(int64_t M, int64_t N, int b) { return ((M + b - 1) / b) * ((N +
 // instructions (4096 x 4096 bf16: 14 us at 32 rows, where tiles take 17 us; 21 us
 // at 64, where they take 18 us).
 constexpr int64_t FEW_ROWS = 32;
+// And its columns: 16 a workgroup of 512, threads that a launch counts in 32 bits (the widest layer is one workgroup past that).
+constexpr int64_t FEW_COLUMNS = 16 * ((int64_t(1) << 23) - 1);
 
 // Whether a product is worth packing for.  Packing reads and writes the operands
 // once, in proportion to (M + N) K, and costs a launch; what it gains over the general
@@ -1093,7 +1095,7 @@ bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype, bool forward)
 // through some 200.
 Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool tiled, bool packed, bool forward) {
   Plan p{};
-  if (forward && M <= FEW_ROWS) {
+  if (forward && M <= FEW_ROWS && N <= FEW_COLUMNS) {
     p.kind = FEW;
     p.splits = 1;
     return p;

@@ -50,3 +50,14 @@ def test_rows_up_to_the_limit():
     # sums of at most 2^22 equal terms are exact in float32; joined in order, then rounded
     gw, gb = 9.0 * (rows // 2) + 25.0 * (rows // 2) + 49.0, -2.0 * (rows // 2) + 7.0
     assert abs(float(b["gw"]) - gw) <= 2.0 ** -7 * gw and abs(float(b["gbias"]) - gb) <= 2.0 ** -7 * abs(gb)
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("outer", [2 ** 27 - 16, 2 ** 27])
+def test_outputs_up_to_the_limit(outer, rows):
+    """The widest layers of one and of a few rows."""
+    w = torch.arange(outer, device=DEV, dtype=torch.float32).remainder_(251).to(torch.bfloat16)[:, None]
+    x = torch.tensor([1.0, -2.0, 4.0, 0.5] * 5, device=DEV, dtype=w.dtype)[:rows, None]
+    y = B.linear(x, w)["y"]
+    for i in range(rows):
+        assert torch.equal(y[i], w[:, 0] * float(x[i, 0])), i
