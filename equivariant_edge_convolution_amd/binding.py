@@ -217,6 +217,14 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+def _given(workspace: torch.Tensor, device) -> tuple[int, int]:
+    """(address, bytes) of a caller's workspace, of any type, in this device's memory (a kernel would take a host
+    address for its own)."""
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}, not on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def neighbors_workspace_bytes(n_atoms: int, box, cutoff: float) -> int:
     return int(lib().eec_neighbors_workspace_bytes(int(n_atoms), _box(box), float(cutoff)))
 
@@ -324,10 +332,12 @@ def edge_message(graph: Graph, pos: torch.Tensor, box, species: torch.Tensor, mo
     dev = pos.device
     n = graph.n_atoms
     A = out if out is not None else torch.empty((n, 16, model.channels), dtype=torch.float32, device=dev)
-    ws = workspace if workspace is not None else _workspace(workspace_bytes(n, graph.n_edges, model), dev)
+    if workspace is None:
+        workspace = _workspace(workspace_bytes(n, graph.n_edges, model), dev)
+    ws, size = _given(workspace, dev)
     g, m = graph.struct(), model.struct()
     _check(lib().eec_edge_message(_stream(dev), ctypes.byref(g), _ptr(pos), _box(box), _ptr(species),
-                                  ctypes.byref(m), _ptr(A), _ptr(ws), ws.numel()), "edge_message")
+                                  ctypes.byref(m), _ptr(A), ws, size), "edge_message")
     return A
 
 
@@ -513,15 +523,17 @@ def add_rms_norm_backward(gy: torch.Tensor, sum: torch.Tensor, weight: torch.Ten
     w = _vector(weight, "weight", n, dt, dev)
     rs = _vector(rstd, "rstd", rows, torch.float32, dev)
     gx = _new_rows(sum, rows, n)
-    gw = ws = None
+    gw, ws, size = None, None, 0
+    if workspace is not None:
+        ws, size = _given(workspace, dev)
     if weight is not None:
         gw = torch.empty(n, dtype=dt, device=dev)
-        ws = workspace
-        if ws is None:
-            ws = _workspace(lib().eec_add_rms_norm_backward_workspace_bytes(rows, n), dev)
+        if workspace is None:
+            workspace = _workspace(lib().eec_add_rms_norm_backward_workspace_bytes(rows, n), dev)
+            ws, size = workspace.data_ptr(), workspace.numel()
     _check(lib().eec_add_rms_norm_backward(_raw_stream(dev), rows, n, DTYPES[dt], gy.data_ptr(), ldgy, sum.data_ptr(),
-                                           lds, w, rs, _address(gsum), ldgs, gx.data_ptr(), _address(gw), _address(ws),
-                                           ws.numel() if ws is not None else 0), "add_rms_norm_backward")
+                                           lds, w, rs, _address(gsum), ldgs, gx.data_ptr(), _address(gw), ws, size),
+           "add_rms_norm_backward")
     return dict(gx=gx, gweight=gw)
 
 
@@ -547,14 +559,16 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     out = dict(y=y)
     if save_preact:
         out["preact"] = torch.empty((rows, n), dtype=ot, device=dev)
-    ws = workspace
     dt, ot = DTYPES[dt], DTYPES[ot]
-    if ws is None:
-        need = _linear_workspace(rows, n, k, dt, ot)
-        ws = _workspace(need, dev) if need else None
+    ws, size = None, 0
+    if workspace is not None:
+        ws, size = _given(workspace, dev)
+    elif need := _linear_workspace(rows, n, k, dt, ot):
+        workspace = _workspace(need, dev)
+        ws, size = workspace.data_ptr(), need
     _check(lib().eec_linear(_raw_stream(dev), rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(),
                             ldw, wsc, b, _address(residual), ldr, ACTS[act], y.data_ptr(), _address(out.get("preact")),
-                            _address(ws), ws.numel() if ws is not None else 0), "linear")
+                            ws, size), "linear")
     return out
 
 
@@ -576,12 +590,12 @@ def linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: 
             raise ValueError("preact must be contiguous")
     gx, gw = _new_rows(x, rows, k), _new_rows(w, n, k)
     gb = torch.empty(n, dtype=dt, device=dev) if bias else None
-    ws = workspace
-    if ws is None:
-        ws = _workspace(lib().eec_linear_backward_workspace_bytes(rows, n, k, DTYPES[dt], ACTS[act]), dev)
+    if workspace is None:
+        workspace = _workspace(lib().eec_linear_backward_workspace_bytes(rows, n, k, DTYPES[dt], ACTS[act]), dev)
+    ws, size = _given(workspace, dev)
     _check(lib().eec_linear_backward(_raw_stream(dev), rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
                                      x.data_ptr(), ldx, w.data_ptr(), ldw, _address(preact), gx.data_ptr(),
-                                     gw.data_ptr(), _address(gb), ws.data_ptr(), ws.numel()), "linear_backward")
+                                     gw.data_ptr(), _address(gb), ws, size), "linear_backward")
     return dict(gx=gx, gw=gw, gbias=gb)
 
 

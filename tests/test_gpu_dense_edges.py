@@ -61,3 +61,22 @@ def test_outputs_up_to_the_limit(outer, rows):
     y = B.linear(x, w)["y"]
     for i in range(rows):
         assert torch.equal(y[i], w[:, 0] * float(x[i, 0])), i
+
+
+def test_workspace_of_the_wrong_kind_is_refused():
+    x, w = torch.randn(300, 1320, device=DEV), torch.randn(280, 1320, device=DEV)
+    gy, rstd = torch.randn(300, 280, device=DEV), torch.ones(300, device=DEV)
+    gain = torch.ones(1320, device=DEV)
+    calls = (lambda ws: B.linear(x, w, workspace=ws)["y"],
+             lambda ws: B.linear_backward(gy, x, w, workspace=ws)["gw"],
+             lambda ws: B.add_rms_norm_backward(x, x, gain, rstd, workspace=ws)["gweight"])
+    for call in calls:
+        size = 16 << 20
+        for bad in (torch.empty(size, dtype=torch.uint8), torch.empty(size, dtype=torch.uint8).pin_memory(),
+                    torch.empty((2, size), dtype=torch.uint8, device=DEV)[:, ::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(bad)
+        with pytest.raises(B.EECError, match="WORKSPACE"):
+            call(torch.empty(256, dtype=torch.uint8, device=DEV))
+        # its bytes count, whatever it is made of
+        assert torch.equal(call(torch.empty(size // 4, dtype=torch.float32, device=DEV)), call(None))
