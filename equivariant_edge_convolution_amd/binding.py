@@ -586,7 +586,8 @@ def linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: 
     if act != "none":
         if preact is None:
             raise ValueError("an activation's backward needs preact")
-        if _matrix(preact, "preact", rows, n, dt, dev) != n:
+        _matrix(preact, "preact", rows, n, dt, dev)
+        if not preact.is_contiguous():
             raise ValueError("preact must be contiguous")
     gx, gw = _new_rows(x, rows, k), _new_rows(w, n, k)
     gb = torch.empty(n, dtype=dt, device=dev) if bias else None

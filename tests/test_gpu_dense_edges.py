@@ -80,3 +80,22 @@ def test_workspace_of_the_wrong_kind_is_refused():
             call(torch.empty(256, dtype=torch.uint8, device=DEV))
         # its bytes count, whatever it is made of
         assert torch.equal(call(torch.empty(size // 4, dtype=torch.float32, device=DEV)), call(None))
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_backward_without_outputs(act):
+    """A layer of no outputs: nothing reaches x, and the other gradients are empty."""
+    x, w = torch.ones((4, 8), device=DEV), torch.ones((0, 8), device=DEV)
+    out = B.linear(x, w, act=act, save_preact=True)
+    b = B.linear_backward(torch.ones((4, 0), device=DEV), x, w, out["preact"], act)
+    assert bool((b["gx"] == 0).all()) and b["gw"].shape == (0, 8) and b["gbias"].shape == (0,)
+
+
+def test_backward_refuses_a_strided_preact():
+    x, w = torch.ones((4, 8), device=DEV), torch.ones((6, 8), device=DEV)
+    wide = torch.ones((4, 12), device=DEV)
+    for bad in (wide[:, :6], wide[:, ::2], torch.ones((6, 4), device=DEV).t()):
+        with pytest.raises(ValueError):
+            B.linear_backward(torch.ones((4, 6), device=DEV), x, w, bad, "silu")
+    # one row, or one column, of any stride is contiguous
+    B.linear_backward(torch.ones((1, 6), device=DEV), x[:1], w, wide[:1, :6], "silu")
