@@ -561,7 +561,9 @@ eec_status eec_add_rms_norm(void* stream, int64_t rows, int64_t width, int32_t d
                             float* scale, float* rstd) {
   if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
   if (bad_size(rows) || width < 1 || bad_width(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
-  if (!(isfinite(eps) && eps >= 0.0)) return fail(EEC_ERR_SHAPE, "eps must be finite and >= 0");
+  // eps joins the mean in float32: past its range it would be another eps, 0 or infinity
+  if (!(isfinite((float)eps) && eps >= 0.0 && (eps == 0.0 || (float)eps > 0.f)))
+    return fail(EEC_ERR_SHAPE, "eps must be 0 or a positive number within float32's range");
   const int32_t ytype = scale != nullptr ? (int32_t)EEC_E4M3 : dtype;
   TRY(check_matrix(x, rows, width, ldx, dtype, "x"));
   TRY(check_optional(residual, rows, width, ldr, dtype, "residual"));

@@ -421,7 +421,7 @@ typedef enum {
  *             e4m3; a row that holds a NaN or an infinity has a NaN scale and
  *             NaN codes
  *   rstd      [rows] float32 or NULL (what the backward reads)
- *   eps       finite, >= 0 */
+ *   eps       0, or positive and within float32's range (2^-149 and more) */
 EEC_API eec_status eec_add_rms_norm(void *stream, int64_t rows, int64_t width, int32_t dtype, const void *x,
                             int64_t ldx, const void *residual, int64_t ldr, const void *weight, double eps,
                             void *sum, void *y, float *scale, float *rstd);

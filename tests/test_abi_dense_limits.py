@@ -1,10 +1,8 @@
 """Sizes and arguments at the limits the header names (CPU only).  Nothing is launched: a call that passes the check
 under test is stopped by the next one, an output that overlaps an input."""
-import ctypes
-
 import pytest
 
-from test_abi_dense import P, linear, linear_bwd
+from test_abi_dense import P, linear, linear_bwd, norm
 
 
 @pytest.mark.parametrize("call,status", [
@@ -28,3 +26,13 @@ from test_abi_dense import P, linear, linear_bwd
 ])
 def test_products_up_to_the_limit(call, status):
     assert call() == status
+
+
+@pytest.mark.parametrize("eps,status", [
+    (0.0, "EEC_ERR_ALIAS"), (1e-45, "EEC_ERR_ALIAS"), (1e-12, "EEC_ERR_ALIAS"), (3.4e38, "EEC_ERR_ALIAS"),
+    # float32 would have 0 or infinity in their place, and a row of zeros NaN in place of zeros
+    (1e-46, "EEC_ERR_SHAPE"), (1e-300, "EEC_ERR_SHAPE"), (3.5e38, "EEC_ERR_SHAPE"), (1e300, "EEC_ERR_SHAPE"),
+    (float("inf"), "EEC_ERR_SHAPE"), (float("-inf"), "EEC_ERR_SHAPE"), (-1e-300, "EEC_ERR_SHAPE"),
+])
+def test_eps_within_float32(eps, status):
+    assert norm(eps=eps, y=P(1)) == status
