@@ -1,8 +1,10 @@
 """The dense operators where values, sizes and arguments are at their limits, against the definitions in 64 bits.
 
 Bounds as in test_gpu_dense.py: U of one rounding to the output's type, EPS = 2^-24 of each float32 operation."""
+import numpy as np
 import pytest
 import torch
+from scipy import special
 
 from equivariant_edge_convolution_amd import binding as B
 
@@ -99,3 +101,59 @@ def test_backward_refuses_a_strided_preact():
             B.linear_backward(torch.ones((4, 6), device=DEV), x, w, bad, "silu")
     # one row, or one column, of any stride is contiguous
     B.linear_backward(torch.ones((1, 6), device=DEV), x[:1], w, wide[:1, :6], "silu")
+
+
+def act_values(dt, act, n):
+    lo = -87.0 if act == "silu" else -13.0  # exp(-|z|), exp(-z^2 / 2) stay normal float32
+    return torch.linspace(lo, 9.0, n, dtype=torch.float64).to(dt).to(DEV)[:, None]
+
+
+def act_bound(dt, act, z):
+    """In EPS of the value: the functions 16; with 16-bit outputs the exponential's argument is rounded as well, by 2.5 EPS of
+    z^2 / 2 (GELU: the square, the constant, their product) or 1.5 EPS of |z| (SiLU)."""
+    if dt == torch.float32:
+        return 16.0 + 0 * z
+    return 16.0 + (1.5 * np.abs(z) if act == "silu" else 1.25 * z * z)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("rows", [32, 4001])
+def test_activation_tails(rows, act, dt):
+    """A layer of one input and weight 1 is its activation: right to the output's rounding where it is small, too."""
+    x, one = act_values(dt, act, rows), torch.ones((1, 1), dtype=dt, device=DEV)
+    out = B.linear(x, one, act=act, save_preact=True)
+    assert torch.equal(out["preact"], x)
+    z = f64(x)
+    if act == "silu":
+        y = z / (1.0 + np.exp(-z))
+    else:
+        y = 0.5 * z * special.erfc(-z / np.sqrt(2.0))
+    within(out["y"], y, (U[dt] + act_bound(dt, act, z) * EPS) * np.abs(y) + TINY[dt], "y")
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("act", ["gelu"])
+def test_activation_slope_tails(act, dt):
+    """Read from gbias: a product would hold float32 slopes to 2^-131 only."""
+    z = act_values(dt, act, 4001)
+    one = torch.ones((1, 1), dtype=dt, device=DEV)
+    slope = B.linear_backward(torch.ones_like(z.t()), one, torch.ones_like(z), z.t().contiguous(), act)["gbias"][:, None]
+    v = f64(z)
+    if act == "silu":
+        p, q = 1.0 / (1.0 + np.exp(-v)), 1.0 / (1.0 + np.exp(v))
+        a, b = p, v * p * q
+    else:
+        a, b = 0.5 * special.erfc(-v / np.sqrt(2.0)), v * np.exp(-0.5 * v * v) / np.sqrt(2.0 * np.pi)
+    within(slope, a + b, U[dt] * np.abs(a + b) + act_bound(dt, act, v) * EPS * (np.abs(a) + np.abs(b)) + TINY[dt], "slope")
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_activations_of_special_values(dt):
+    """As the definitions have them: 0 times infinity is NaN."""
+    x = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 30.0, -30.0] * 8, dtype=dt, device=DEV)[:, None]
+    one = torch.ones((1, 1), dtype=dt, device=DEV)
+    for act, at_minus in (("relu", 0.0), ("silu", float("nan")), ("gelu", float("nan"))):
+        y = f64(B.linear(x, one, act=act)["y"])[:7, 0]
+        assert y[0] == 0.0 and y[1] == 0.0 and y[2] == np.inf and np.isnan(y[4]) and y[5] == 30.0, act
+        assert (np.isnan(y[3]) if np.isnan(at_minus) else y[3] == at_minus) and abs(y[6]) < 1e-11, act
