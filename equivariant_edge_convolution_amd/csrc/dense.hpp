@@ -101,11 +101,30 @@ __device__ __forceinline__ void store_run_e4m3(uint8_t* __restrict__ p, int64_t 
   }
 }
 
-// 1 / (1 + exp(-z)) on the exponential and reciprocal instructions: the rounding of
-// z log2(e) makes exp(-z) up to 1.5 |z| 2^-24 wrong, which is within 2 x 2^-24 of
-// the largest value of z sigmoid(z) wherever it matters (|z| exp(-|z|) <= 0.37).
-__device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+// exp(x) from k = x log2(e) as rounded and `lost`, what that rounding left out.
+__device__ __forceinline__ float exp_and(float k, float lost) {
+  const float e = __builtin_amdgcn_exp2f(k);
+  return __builtin_fmaf(e, lost * 0.69314718055994531f, e);
+}
+// sigmoid(z) = 1 / (1 + exp(-z)) and sigmoid(-z), so that z sigmoid(z) and its slope are
+// within 16 x 2^-24 of their size before a float32 output is rounded, down to
+// exp(-|z|) = 2^-126: both from exp(-|z|), so that neither cancels, and its argument keeps
+// what its rounding loses (130 x 2^-24 at z = -87).  Beside a 16-bit output all of that is
+// below the output's rounding, and the shorter form has it down to z = -88 (32768 x 512 x 512
+// bf16 forward with SiLU: 31.1 us in the long form, 29.5 in the short one).
+template <typename O>
+__device__ __forceinline__ void sigmoids(float z, float& plus, float& minus) {
+  constexpr float C = -1.44269504088896341f, C_LOW = (float)(-1.44269504088896341 - (double)C);
+  if constexpr (sizeof(O) == 4) {
+    const float a = fabsf(z), k = a * C;
+    const float e = a > 200.f ? 0.f : exp_and(k, __builtin_fmaf(a, C, -k) + a * C_LOW);
+    const float r = __builtin_amdgcn_rcpf(1.f + e), small = e * r;
+    plus = z < 0.f ? small : r;
+    minus = z < 0.f ? r : small;
+  } else {
+    plus = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * C));
+    minus = 1.f - plus;
+  }
 }
 
 // GELU is z Phi(z), with Phi(-|z|) = erfc(|z| / sqrt 2) / 2.  For z < 0 that is taken as it
@@ -132,11 +151,6 @@ __device__ __forceinline__ float half_erfcx(float z) {
   p = __builtin_fmaf(p, t, 2.256280333e-01f);
   return p * t * 0.5f;
 }
-// exp(x) from k = x log2(e) as rounded and `lost`, what that rounding left out.
-__device__ __forceinline__ float exp_and(float k, float lost) {
-  const float e = __builtin_amdgcn_exp2f(k);
-  return __builtin_fmaf(e, lost * 0.69314718055994531f, e);
-}
 template <typename O>
 __device__ __forceinline__ float gauss(float z) {
   constexpr float C = -0.72134752044448170f, C_LOW = (float)(-0.72134752044448170 - (double)C);
@@ -154,7 +168,11 @@ template <typename O, int N>
 __device__ __forceinline__ void act_values(float (&z)[N], int act) {
   if (act == EEC_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] *= sigmoid(z[i]);
+    for (int i = 0; i < N; ++i) {
+      float p, q;
+      sigmoids<O>(z[i], p, q);
+      z[i] *= p;
+    }
   } else if (act == EEC_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -172,8 +190,9 @@ __device__ __forceinline__ void act_slopes(float (&g)[N], const float (&z)[N], i
   if (act == EEC_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float p = sigmoid(z[i]);
-      g[i] *= p * (1.f + z[i] * (1.f - p));
+      float p, q;
+      sigmoids<O>(z[i], p, q);
+      g[i] *= p * (1.f + z[i] * q);
     }
   } else if (act == EEC_ACT_GELU) {
 #pragma unroll

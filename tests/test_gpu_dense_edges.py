@@ -117,7 +117,7 @@ def act_bound(dt, act, z):
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("rows", [32, 4001])
 def test_activation_tails(rows, act, dt):
     """A layer of one input and weight 1 is its activation: right to the output's rounding where it is small, too."""
@@ -133,7 +133,7 @@ def test_activation_tails(rows, act, dt):
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_activation_slope_tails(act, dt):
     """Read from gbias: a product would hold float32 slopes to 2^-131 only."""
     z = act_values(dt, act, 4001)
