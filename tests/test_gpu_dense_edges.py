@@ -157,3 +157,35 @@ def test_activations_of_special_values(dt):
         y = f64(B.linear(x, one, act=act)["y"])[:7, 0]
         assert y[0] == 0.0 and y[1] == 0.0 and y[2] == np.inf and np.isnan(y[4]) and y[5] == 30.0, act
         assert (np.isnan(y[3]) if np.isnan(at_minus) else y[3] == at_minus) and abs(y[6]) < 1e-11, act
+
+
+def e4m3_codes(kind, rows, k, g):
+    """[rows][k] of e4m3: every code (no NaN), normal values, or groups of eight whose largest product hides the others."""
+    if kind == "codes":
+        u = torch.randint(0, 254, (rows, k), generator=g, dtype=torch.int64)
+        u = torch.where(u >= 127, u + 1, u)  # 0x7f and 0xff are NaN
+        return u.to(torch.uint8).view(torch.float8_e4m3fn).to(DEV)
+    if kind == "normal":
+        return (30.0 * torch.randn(rows, k, generator=g)).clamp(-448, 448).to(torch.float8_e4m3fn).to(DEV)
+    # products 2^16 and, seven times, 1.875 1.875 2^2: just under two steps of 2^3, cut to one each
+    v = torch.full((rows, k), 3.75)
+    v[:, ::8] = 256.0
+    return v.to(torch.float8_e4m3fn).to(DEV)
+
+
+@pytest.mark.parametrize("ot", [torch.float16, torch.bfloat16], ids=ids)
+@pytest.mark.parametrize("kind", ["codes", "normal", "hidden"])
+@pytest.mark.parametrize("rows,inner,outer", [(16, 64, 64), (16, 4096, 40), (64, 64, 64), (200, 4096, 256), (300, 8192, 264),
+                                              (70, 4095, 50)])
+def test_e4m3_sums_with_16_bit_outputs(rows, inner, outer, kind, ot):
+    """Within 2^-10 of sum |x||w| whatever the length: 7 2^-13 from the cut products, and from float32's sums of k / 8
+    groups 2^-24 each, 2^-14 at k = 8192."""
+    g = torch.Generator().manual_seed(inner + rows)
+    x, w = e4m3_codes(kind, rows, inner, g), e4m3_codes(kind, outer, inner, g)
+    sx, sw = torch.full((rows,), 2.0 ** -8, device=DEV), torch.full((outer,), 2.0 ** -8, device=DEV)
+    X, W = x.float().double() * 2.0 ** -8, w.float().double() * 2.0 ** -8
+    z, S = f64(X @ W.t()), f64(X.abs() @ W.abs().t())
+    y = B.linear(x, w, x_scale=sx, w_scale=sw, out_dtype=ot)["y"]
+    within(y, z, 2.0 ** -10 * S + U[ot] * np.abs(z) + TINY[ot], "16-bit output")
+    wide = B.linear(x, w, x_scale=sx, w_scale=sw, out_dtype=torch.float32)["y"]
+    within(wide, z, (inner / 8 + 32) * EPS * S, "float32 output")
