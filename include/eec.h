@@ -451,9 +451,11 @@ EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t w
  *   preact  [rows][outer] z in out_dtype, or NULL (what the backward reads)
  *   workspace >= eec_linear_workspace_bytes(rows, outer, inner, dtype, out_dtype);
  *   may be NULL where that is 0
- * float32 operands keep float32's accuracy on the bf16 matrix cores: each is
- * the sum of three bf16 parts (exact above 2^-100, to within 2^-131 below), and
- * the six part products down to 2^-16 of the largest are taken.  e4m3 products
+ * float32 operands are multiplied on the bf16 matrix cores, about as exactly
+ * as float32: each is the sum of three bf16 parts (exact above 2^-100, to within
+ * 2^-131 below), and the six part products down to 2^-16 of the largest are
+ * taken.  What is left out cuts each product towards zero by 0.6 2^-24 of it on
+ * average, 2^-21 at most. e4m3 products
  * with a 16-bit output are summed by the 8-bit matrix instructions, which cut
  * each of eight products adjacent in k towards zero at 2^-13 of the largest
  * one's power of two: z may be off by 7 2^-13 (8.5e-4) of sum |x||w| at worst
