@@ -189,3 +189,17 @@ def test_e4m3_sums_with_16_bit_outputs(rows, inner, outer, kind, ot):
     within(y, z, 2.0 ** -10 * S + U[ot] * np.abs(z) + TINY[ot], "16-bit output")
     wide = B.linear(x, w, x_scale=sx, w_scale=sw, out_dtype=torch.float32)["y"]
     within(wide, z, (inner / 8 + 32) * EPS * S, "float32 output")
+
+
+@pytest.mark.parametrize("rows,width,groups", [(1000, 64, 250), (1001, 500, 251), (9, 64, 3), (5000, 64, 512), (100, 4096, 100)])
+def test_norm_backward_has_no_group_without_rows(rows, width, groups):
+    """The weight gradient's partial rows are those of workgroups that have rows (four at a time where a wave takes one)."""
+    g = torch.Generator().manual_seed(rows)
+    s, gy = (torch.randn(rows, width, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    w, rstd = torch.ones(width, dtype=torch.bfloat16, device=DEV), torch.ones(rows, device=DEV)
+    floats = B.lib().eec_add_rms_norm_backward_workspace_bytes(rows, width) // 4
+    ws = torch.full((floats,), -1234.5, device=DEV)
+    gw = B.add_rms_norm_backward(gy, s, w, rstd, workspace=ws)["gweight"]
+    assert bool((ws[groups * width:] == -1234.5).all()) and bool((ws[: groups * width] != -1234.5).all())
+    a, size = f64(gy) * f64(s), np.abs(f64(gy) * f64(s)).sum(axis=0)
+    within(gw, a.sum(axis=0), U[torch.bfloat16] * np.abs(a.sum(axis=0)) + (rows + 8) * EPS * size + TINY[torch.bfloat16], "gweight")
