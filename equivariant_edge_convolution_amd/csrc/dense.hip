@@ -1254,8 +1254,12 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
     p.gz = p.others = worth_packing(rows, inner, outer, dtype, false) && worth_packing(outer, inner, rows, dtype, false);
   } else {
     p.others = inner % 8 != 0 && worth_packing(rows, inner, outer, dtype, false) && worth_packing(outer, inner, rows, dtype, false);
-    // gz passes through k_act_grad anyway, or is small beside what gx and gw take
-    p.gz = outer % 8 != 0 && (p.others || inner % 8 == 0) && rows > FEW_ROWS && outer < 1 << 20 &&
+    // gz passes through k_act_grad anyway, or is small beside what gx and gw take.  Not so
+    // where its rows of 128 columns would be mostly padding and more than four times x:
+    // 10^6 x 8 -> 1 with SiLU 572 us and 256 MB packed, 490 and 2 as it is (-> 33: 680, 609;
+    // -> 63: 788, 796); 32768 rows of it 45 and 54 us, in 8 MB, stay packed.
+    const bool padding = rows > 1 << 19 && up(outer, 128) > std::max(2 * outer, 4 * inner);
+    p.gz = outer % 8 != 0 && (p.others || inner % 8 == 0) && rows > FEW_ROWS && outer < 1 << 20 && !padding &&
            (act != EEC_ACT_NONE || (double)rows * outer * inner >= 4e8);
   }
   size_t at = 0;

@@ -83,3 +83,11 @@ def test_special_values_packed(dt, rows, inner, outer):
     assert np.isposinf(gb[6]) and np.isnan(gb[-1]) and np.all(np.isfinite(np.delete(gb, (6, outer - 1))))
     np.testing.assert_allclose(np.delete(gx, (4, 7), axis=0), 0.125 * (outer - 2), rtol=2.0 ** -22 + T.U[dt])
     np.testing.assert_allclose(np.delete(gw, (6, outer - 1), axis=0), 0.5 * rows, rtol=2.0 ** -22 + T.U[dt])
+
+
+@pytest.mark.parametrize("rows,inner,outer", [(600001, 8, 1), (600001, 24, 33), (600001, 64, 5)])
+def test_backward_of_many_narrow_rows(rows, inner, outer):
+    """The workspace stays in proportion to the operands: gz is not padded to rows that dwarf them."""
+    assert backward_bytes(rows, outer, inner, torch.bfloat16, "silu") <= 4 * packed(torch.bfloat16, (rows, inner), (rows, outer))
+    assert backward_bytes(2 ** 31 - 1, 1, 8, torch.bfloat16, "silu") <= 2 ** 33
+    T.test_linear_large(rows, inner, outer, torch.bfloat16)
