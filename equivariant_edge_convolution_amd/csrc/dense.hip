@@ -1004,6 +1004,11 @@ struct ActGrad {
   void* gbias;     // with one strip the sums themselves instead, or NULL
 };
 
+// 16-bit types: gz is rounded to the type, as the matrix instructions take it (its column
+// sums are not); two parts of it would double both products.  With the rounded preact that
+// leaves gx and gw 2.4e-3 off in norm against 64 bits (8192 x 2048 x 8192 bf16), where
+// products of gz in float32 are 1.7e-3 off by their own rounding.
+//
 // gz = gy act'(preact), as it is or packed, and its column sums: a wave takes 64 x 8
 // (float32: 4) columns, a workgroup's waves deal the rows of a strip in turn.
 template <typename T>
@@ -1078,6 +1083,8 @@ constexpr int64_t FEW_COLUMNS = 16 * ((int64_t(1) << 23) - 1);
 // kernel goes with M N K.  Kernel times, packed against general:
 //   bf16 forward, odd k     1024^3 26 us, 20;  1531 x 2771 x 1029 42, 41;  2048 x 4096 x
 //   (GELU, bias, residual)  1025 44, 42;  4096 x 4096 x 513 45, 52;  2048^3 43, 55
+//   (so 16-bit forwards start between 4.4e9 and 8.6e9 products, where one of three sizes
+//   still loses 2 us and two gain 7 and 12)
 //   e4m3 forward, likewise  1024^3 21 us, 18;  1536^3 26, 26;  2048^3 32, 44
 //   bf16 gx + gw, odd rows  700^3 36, 31;  1024^3 35, 53;  8192 x 128 x 512 32, 35
 //   float32 forward         700^3 62, 25;  1024^3 37, 45;  2048 x 2048 x 512 51, 68;

@@ -7,6 +7,9 @@ channels of A, trained with the dense operators and evaluated in 8 bits.
     s   = x + d1,   y2  = norm(s)          (one call)
     o   = silu(y2 W3 + b3) W4 + b4 + s,    E_i = o . w
 
+The head gives energies.  Its backward ends at the gradient of x: the library takes no
+gradient of A on to the positions, so there are no forces through the head.
+
 The target is the model's own quadratic readout, standardised over the cell, so
 the data need nothing but a seeded cell.  Every product, norm and gradient is one
 of the library's calls; torch allocates, and takes the optimiser's elementwise step.
@@ -55,7 +58,7 @@ class Head:
         return e, (x, n1, h1, n2, h2, o)
 
     def backward(self, ge: torch.Tensor, kept) -> tuple[dict, torch.Tensor]:
-        """Gradients of the weights, and of x (what a force through the message would start from)."""
+        """Gradients of the weights, and of x."""
         p = self.p
         x, n1, h1, n2, h2, o = kept
         be = B.linear_backward(ge, o["y"], p["w"], bias=False)

@@ -387,15 +387,21 @@ EEC_API size_t eec_workspace_bytes(int32_t n_atoms, int64_t n_edges, const eec_m
  * addition with a root-mean-square norm, and a dense layer with bias,
  * activation and residual, each with its backward, and both with 8-bit (e4m3)
  * rows for evaluation.
+ * Such a network gives energies and the gradients of its weights and of its
+ * input; no entry point takes a gradient of A on to the positions, so forces
+ * come from the fixed readout of eec_energy_forces alone.
  *
  * Conventions on top of those above
  *   - A matrix input has a row stride in elements (ld* >= its width, so that a
  *     range of columns of wider features is taken as it is, e.g. the l = 0
  *     channels of A [n_atoms][16][C] with ld = 16 C); its columns are adjacent.
  *     Outputs, vectors and preact are contiguous.  Pointers need the alignment of
- *     their elements only.
+ *     their elements only; large 16- and 8-bit products are fastest from operands
+ *     whose pointers and row strides are multiples of 16 bytes (a view of 8192 rows of
+ *     2048 bf16 whose rows are not: 440 us against 264, copied to such rows first 250).
  *   - Sums, norms and products are accumulated in float32; every output is
- *     rounded once, to nearest even, to its type.
+ *     rounded once, to nearest even, to its type.  float32's range holds for the
+ *     sums, too: a row of |s| beyond 2^64 has an infinite mean square and rstd 0.
  *   - NaN and infinities propagate by the formulas.  Sizes may be odd, one, or
  *     zero (a sum over nothing is 0).  Rows and strides are at most 2^31 - 1,
  *     columns (width, outer, inner) 2^27, and a product has at most 2^36 outputs. */
@@ -429,7 +435,10 @@ EEC_API eec_status eec_add_rms_norm(void *stream, int64_t rows, int64_t width, i
 /* eec_add_rms_norm_backward -- with a = gy weight and xhat = s rstd:
  *   gx      = rstd (a - xhat mean_j(a xhat)) + gsum   the gradient of x and of residual
  *   gweight = sum_rows gy xhat                        (fixed order)
- *   sum     s as the forward wrote it (or x itself where there was no residual)
+ *   sum     s as the forward wrote it (or x itself where there was no residual).
+ *           In 16 bits that is the rounded s, beside the unrounded one's rstd:
+ *           gx and gweight carry its rounding as well as their own, about 1.4
+ *           times the error of a backward that has s in float32
  *   gsum    the gradient that reaches s by other ways, or NULL
  *   gx [rows][width], gweight [width]: dtype, either may be NULL
  *   workspace >= eec_add_rms_norm_backward_workspace_bytes(rows, width), read
@@ -472,6 +481,8 @@ EEC_API size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t i
 /* eec_linear_backward -- with gz = gy act'(preact), rounded once to dtype for
  * the products (EEC_ACT_NONE: gz = gy):
  *   gx [rows][inner] = gz w,  gw [outer][inner] = gz^T x,  gbias [outer] = sum_rows gz
+ * In 16 bits that rounding, and that of preact, come on top of the outputs' own:
+ * about 1.4 times the error of products that have gz and z in float32.
  * (dtype each, any may be NULL; the gradient of residual is gy itself).
  *   dtype   EEC_F32, EEC_F16 or EEC_BF16
  *   preact  [rows][outer] as the forward wrote it; may be NULL with EEC_ACT_NONE
