@@ -37,11 +37,15 @@ SYMBOLS = (
     "eec_energy_forces_timed", "eec_workspace_bytes",
     "eec_radial_table_floats", "eec_radial_table_levels", "eec_radial_table_build", "eec_energy_forces_tabulated", "eec_last_error",
     "eec_add_rms_norm", "eec_add_rms_norm_backward", "eec_add_rms_norm_backward_workspace_bytes",
+    "eec_quantize_rows",
     "eec_linear", "eec_linear_workspace_bytes", "eec_linear_backward", "eec_linear_backward_workspace_bytes",
+    "eec_gated_linear", "eec_gated_linear_workspace_bytes", "eec_gated_linear_backward",
+    "eec_gated_linear_backward_workspace_bytes",
 )
 PHASES = ("prepare", "forward", "readout", "backward", "scatter")
 VARIANTS = {"direct": 0, "folded": 1, "tabulated": 2}
-DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3, torch.int8: 4}
+EIGHT_BITS = (torch.float8_e4m3fn, torch.int8)
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 
 
@@ -128,6 +132,8 @@ def lib() -> ctypes.CDLL:
     L.eec_add_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
     L.eec_add_rms_norm_backward.restype = ctypes.c_int
     L.eec_add_rms_norm_backward.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp, sz]
+    L.eec_quantize_rows.restype = ctypes.c_int
+    L.eec_quantize_rows.argtypes = [vp, i64, i64, i32, i32, vp, i64, vp, vp]
     L.eec_linear_workspace_bytes.restype = sz
     L.eec_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
     L.eec_linear.restype = ctypes.c_int
@@ -136,6 +142,14 @@ def lib() -> ctypes.CDLL:
     L.eec_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
     L.eec_linear_backward.restype = ctypes.c_int
     L.eec_linear_backward.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, sz]
+    L.eec_gated_linear_workspace_bytes.restype = sz
+    L.eec_gated_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    L.eec_gated_linear.restype = ctypes.c_int
+    L.eec_gated_linear.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, vp, i64, vp, vp, i32, vp, vp, vp, sz]
+    L.eec_gated_linear_backward_workspace_bytes.restype = sz
+    L.eec_gated_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.eec_gated_linear_backward.restype = ctypes.c_int
+    L.eec_gated_linear_backward.argtypes = [vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, sz]
     _lib = L
     return L
 
@@ -470,7 +484,7 @@ def _vector(t: torch.Tensor | None, name: str, n: int, dtype, device):
 def _dense_input(t: torch.Tensor, name: str):
     """(rows, width, dtype, device) of an operator's first matrix."""
     if t.dim() != 2 or t.dtype not in DTYPES or not t.is_cuda:
-        raise ValueError(f"{name} must be a device matrix of float32, float16, bfloat16 or (linear) float8_e4m3fn")
+        raise ValueError(f"{name} must be a device matrix of float32, float16, bfloat16 or (layers) float8_e4m3fn or int8")
     return *t.shape, t.dtype, t.device
 
 
@@ -537,16 +551,30 @@ def add_rms_norm_backward(gy: torch.Tensor, sum: torch.Tensor, weight: torch.Ten
     return dict(gx=gx, gweight=gw)
 
 
+def quantize_rows(x: torch.Tensor, dtype: torch.dtype = torch.int8) -> dict:
+    """eec_quantize_rows: ``y``, the rows of ``x`` (any row stride) in int8 or
+    float8_e4m3fn, and ``scale``, what a code of each row is worth."""
+    rows, n, dt, dev = _dense_input(x, "x")
+    if dtype not in EIGHT_BITS:
+        raise ValueError(f"rows are quantised to int8 or float8_e4m3fn, not {dtype}")
+    ldx = _matrix(x, "x", rows, n, dt, dev)
+    y = torch.empty((rows, n), dtype=dtype, device=dev)
+    scale = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(lib().eec_quantize_rows(_raw_stream(dev), rows, n, DTYPES[dt], DTYPES[dtype], x.data_ptr(), ldx, y.data_ptr(),
+                                   scale.data_ptr()), "quantize_rows")
+    return dict(y=y, scale=scale)
+
+
 def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
            residual: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
            w_scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, save_preact: bool = False,
            workspace: torch.Tensor | None = None) -> dict:
     """eec_linear: ``y`` = act(x w^T + bias) + residual and, with
-    ``save_preact``, ``preact`` (what act is applied to).  float8_e4m3fn
+    ``save_preact``, ``preact`` (what act is applied to).  float8_e4m3fn and int8
     operands take their row scales and ``out_dtype`` (bfloat16 by default)."""
     rows, k, dt, dev = _dense_input(x, "x")
     n = w.shape[0]
-    ot = out_dtype if out_dtype is not None else (torch.bfloat16 if dt == torch.float8_e4m3fn else dt)
+    ot = out_dtype if out_dtype is not None else (torch.bfloat16 if dt in EIGHT_BITS else dt)
     if ot not in DTYPES or act not in ACTS:
         raise ValueError(f"unknown out_dtype {ot} or activation {act!r}")
     ldx = _matrix(x, "x", rows, k, dt, dev)
@@ -597,6 +625,82 @@ def linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: 
     _check(lib().eec_linear_backward(_raw_stream(dev), rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
                                      x.data_ptr(), ldx, w.data_ptr(), ldw, _address(preact), gx.data_ptr(),
                                      gw.data_ptr(), _address(gb), ws, size), "linear_backward")
+    return dict(gx=gx, gw=gw, gbias=gb)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_workspace(rows: int, outer: int, inner: int, dtype: int, out_dtype: int) -> int:
+    return lib().eec_gated_linear_workspace_bytes(rows, outer, inner, dtype, out_dtype)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_backward_workspace(rows: int, outer: int, inner: int, dtype: int) -> int:
+    return lib().eec_gated_linear_backward_workspace_bytes(rows, outer, inner, dtype)
+
+
+def _halves(w: torch.Tensor) -> int:
+    """Outputs of a gated layer with the weight ``w`` [2 outer][inner]."""
+    if w.dim() != 2 or w.shape[0] % 2:
+        raise ValueError(f"w must be [2 outer][inner], the gate's rows first, not {list(w.shape)}")
+    return w.shape[0] // 2
+
+
+def gated_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, act: str = "silu",
+                 x_scale: torch.Tensor | None = None, w_scale: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, save_preact: bool = False,
+                 workspace: torch.Tensor | None = None) -> dict:
+    """eec_gated_linear: ``y`` = act(gate) value with (gate, value) = x w^T + bias,
+    w [2 outer][inner] (the gate's rows first), and, with ``save_preact``,
+    ``preact`` [rows][2 outer].  float8_e4m3fn and int8 operands take their row
+    scales and ``out_dtype`` (bfloat16 by default)."""
+    rows, k, dt, dev = _dense_input(x, "x")
+    n = _halves(w)
+    ot = out_dtype if out_dtype is not None else (torch.bfloat16 if dt in EIGHT_BITS else dt)
+    if ot not in DTYPES or act not in ACTS:
+        raise ValueError(f"unknown out_dtype {ot} or activation {act!r}")
+    ldx = _matrix(x, "x", rows, k, dt, dev)
+    ldw = _matrix(w, "w", 2 * n, k, dt, dev)
+    xs = _vector(x_scale, "x_scale", rows, torch.float32, dev)
+    wsc = _vector(w_scale, "w_scale", 2 * n, torch.float32, dev)
+    b = _vector(bias, "bias", 2 * n, ot, dev)
+    y = x.new_empty((rows, n)) if ot == dt else torch.empty((rows, n), dtype=ot, device=dev)
+    out = dict(y=y)
+    if save_preact:
+        out["preact"] = torch.empty((rows, 2 * n), dtype=ot, device=dev)
+    dt, ot = DTYPES[dt], DTYPES[ot]
+    ws, size = None, 0
+    if workspace is not None:
+        ws, size = _given(workspace, dev)
+    elif need := _gated_workspace(rows, n, k, dt, ot):
+        workspace = _workspace(need, dev)
+        ws, size = workspace.data_ptr(), need
+    _check(lib().eec_gated_linear(_raw_stream(dev), rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, wsc, b,
+                                  ACTS[act], y.data_ptr(), _address(out.get("preact")), ws, size), "gated_linear")
+    return out
+
+
+def gated_linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: torch.Tensor, act: str = "silu",
+                          bias: bool = True, workspace: torch.Tensor | None = None) -> dict:
+    """eec_gated_linear_backward: ``gx``, ``gw`` [2 outer][inner] and, with
+    ``bias``, ``gbias`` [2 outer], from the forward's ``preact``."""
+    rows, k, dt, dev = _dense_input(x, "x")
+    n = _halves(w)
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    ldx = _matrix(x, "x", rows, k, dt, dev)
+    ldw = _matrix(w, "w", 2 * n, k, dt, dev)
+    ldgy = _matrix(gy, "gy", rows, n, dt, dev)
+    _matrix(preact, "preact", rows, 2 * n, dt, dev)
+    if not preact.is_contiguous():
+        raise ValueError("preact must be contiguous")
+    gx, gw = _new_rows(x, rows, k), _new_rows(w, 2 * n, k)
+    gb = torch.empty(2 * n, dtype=dt, device=dev) if bias else None
+    if workspace is None:
+        workspace = _workspace(_gated_backward_workspace(rows, n, k, DTYPES[dt]), dev)
+    ws, size = _given(workspace, dev)
+    _check(lib().eec_gated_linear_backward(_raw_stream(dev), rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
+                                           x.data_ptr(), ldx, w.data_ptr(), ldw, preact.data_ptr(), gx.data_ptr(),
+                                           gw.data_ptr(), _address(gb), ws, size), "gated_linear_backward")
     return dict(gx=gx, gw=gw, gbias=gb)
 
 

@@ -527,8 +527,9 @@ namespace {
 constexpr int64_t MAX_SIZE = INT32_MAX;
 constexpr int64_t MAX_WIDTH = int64_t(1) << 27;  // columns: a launch counts its threads in 32 bits
 
-size_t dtype_bytes(int32_t t) { return t == EEC_F32 ? 4 : t == EEC_E4M3 ? 1 : 2; }
+size_t dtype_bytes(int32_t t) { return t == EEC_F32 ? 4 : t == EEC_E4M3 || t == EEC_I8 ? 1 : 2; }
 bool float_dtype(int32_t t) { return t == EEC_F32 || t == EEC_F16 || t == EEC_BF16; }
+bool eight_bits(int32_t t) { return t == EEC_E4M3 || t == EEC_I8; }
 
 // A [rows][width] matrix with a row stride; nothing is read of an empty one.
 eec_status check_matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int32_t dtype, const char* name) {
@@ -581,6 +582,21 @@ eec_status eec_add_rms_norm(void* stream, int64_t rows, int64_t width, int32_t d
   return launched("add_rms_norm");
 }
 
+eec_status eec_quantize_rows(void* stream, int64_t rows, int64_t width, int32_t dtype, int32_t codes, const void* x,
+                             int64_t ldx, void* y, float* scale) {
+  if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
+  if (!eight_bits(codes)) return fail(EEC_ERR_SHAPE, "codes must be i8 or e4m3");
+  if (bad_size(rows) || width < 1 || bad_width(width)) return fail(EEC_ERR_SHAPE, "bad rows or width");
+  TRY(check_matrix(x, rows, width, ldx, dtype, "x"));
+  TRY(check_matrix(y, rows, width, width, codes, "y"));
+  TRY(check_matrix(scale, rows, 1, 1, EEC_F32, "scale"));
+  TRY(check_alias({matrix(y, rows, width, width, codes, "y"), matrix(scale, rows, 1, 1, EEC_F32, "scale")},
+                  {matrix(x, rows, width, ldx, dtype, "x")}));
+  if (rows == 0) return ok();
+  launch_quantize((hipStream_t)stream, dtype, codes, rows, width, x, ldx, y, scale);
+  return launched("quantize_rows");
+}
+
 size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t width) {
   if (bad_size(rows) || width < 1 || bad_width(width)) return 0;
   return norm_bwd_workspace(rows, width);
@@ -616,6 +632,16 @@ static eec_status check_linear(int64_t rows, int64_t outer, int64_t inner) {
   if (bad_size(rows) || bad_width(outer) || bad_width(inner)) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
   return EEC_OK;
 }
+// The types of a layer's operands and outputs.
+static eec_status check_operands(int32_t dtype, int32_t out_dtype, int64_t inner) {
+  const bool eight = eight_bits(dtype);
+  if (!eight && !float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16, bf16, e4m3 or i8");
+  if (eight ? !float_dtype(out_dtype) : out_dtype != dtype)
+    return fail(EEC_ERR_SHAPE, "out_dtype must be dtype (f32, f16 or bf16 with 8-bit operands)");
+  if (dtype == EEC_I8 && inner > MAX_INNER_I8)
+    return fail(EEC_ERR_SHAPE, "inner beyond what 32 bits hold of sums of 8-bit integers' products");
+  return EEC_OK;
+}
 // The outputs of one product that is asked for.
 static eec_status check_outputs(int64_t m, int64_t n) {
   if (m > 0 && n > (int64_t(1) << 36) / m) return fail(EEC_ERR_SHAPE, "a product of more than 2^36 outputs");
@@ -623,7 +649,7 @@ static eec_status check_outputs(int64_t m, int64_t n) {
 }
 
 size_t eec_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
-  if (bad_size(rows) || bad_width(outer) || bad_width(inner) || (!float_dtype(dtype) && dtype != EEC_E4M3)) return 0;
+  if (bad_size(rows) || bad_width(outer) || bad_width(inner) || (!float_dtype(dtype) && !eight_bits(dtype))) return 0;
   return linear_workspace(rows, outer, inner, dtype, out_dtype);
 }
 
@@ -631,10 +657,8 @@ eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, 
                       const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
                       const float* w_scale, const void* bias, const void* residual, int64_t ldr, int32_t act,
                       void* y, void* preact, void* workspace, size_t workspace_bytes) {
-  const bool eight = dtype == EEC_E4M3;
-  if (!eight && !float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16, bf16 or e4m3");
-  if (eight ? !float_dtype(out_dtype) : out_dtype != dtype)
-    return fail(EEC_ERR_SHAPE, "out_dtype must be dtype (f32, f16 or bf16 with e4m3 operands)");
+  TRY(check_operands(dtype, out_dtype, inner));
+  const bool eight = eight_bits(dtype);
   TRY(check_act(act));
   TRY(check_linear(rows, outer, inner));
   TRY(check_outputs(rows, outer));
@@ -644,7 +668,7 @@ eec_status eec_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, 
     TRY(check_matrix(x_scale, rows, 1, 1, EEC_F32, "x_scale"));
     TRY(check_matrix(w_scale, outer, 1, 1, EEC_F32, "w_scale"));
   } else if (x_scale != nullptr || w_scale != nullptr) {
-    return fail(EEC_ERR_SHAPE, "scales belong to e4m3 operands");
+    return fail(EEC_ERR_SHAPE, "scales belong to 8-bit operands");
   }
   TRY(check_optional(bias, 1, outer, outer, out_dtype, "bias"));
   TRY(check_optional(residual, rows, outer, ldr, out_dtype, "residual"));
@@ -696,6 +720,86 @@ eec_status eec_linear_backward(void* stream, int64_t rows, int64_t outer, int64_
                         outer > 0 ? gbias : nullptr};
   launch_linear_bwd((hipStream_t)stream, a, (char*)workspace);
   return launched("linear_backward");
+}
+
+// Both halves of a gated layer's w are one matrix, and their outputs count together.
+static eec_status check_gated(int64_t rows, int64_t outer, int64_t inner) {
+  if (outer > MAX_WIDTH / 2) return fail(EEC_ERR_SHAPE, "bad rows, outer or inner");
+  return check_linear(rows, outer, inner);
+}
+
+size_t eec_gated_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
+  if (bad_size(rows) || outer < 0 || outer > MAX_WIDTH / 2 || bad_width(inner) || (!float_dtype(dtype) && !eight_bits(dtype)))
+    return 0;
+  return gated_workspace(rows, outer, inner, dtype, out_dtype);
+}
+
+eec_status eec_gated_linear(void* stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype,
+                            const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                            const float* w_scale, const void* bias, int32_t act, void* y, void* preact, void* workspace,
+                            size_t workspace_bytes) {
+  TRY(check_operands(dtype, out_dtype, inner));
+  TRY(check_act(act));
+  TRY(check_gated(rows, outer, inner));
+  const int64_t both = 2 * outer;
+  TRY(check_outputs(rows, both));
+  TRY(check_matrix(x, rows, inner, ldx, dtype, "x"));
+  TRY(check_matrix(w, both, inner, ldw, dtype, "w"));
+  if (eight_bits(dtype)) {
+    TRY(check_matrix(x_scale, rows, 1, 1, EEC_F32, "x_scale"));
+    TRY(check_matrix(w_scale, both, 1, 1, EEC_F32, "w_scale"));
+  } else if (x_scale != nullptr || w_scale != nullptr) {
+    return fail(EEC_ERR_SHAPE, "scales belong to 8-bit operands");
+  }
+  TRY(check_optional(bias, 1, both, both, out_dtype, "bias"));
+  TRY(check_matrix(y, rows, outer, outer, out_dtype, "y"));
+  TRY(check_optional(preact, rows, both, both, out_dtype, "preact"));
+  TRY(check_ws(workspace, workspace_bytes, gated_workspace(rows, outer, inner, dtype, out_dtype)));
+  TRY(check_alias({matrix(y, rows, outer, outer, out_dtype, "y"), matrix(preact, rows, both, both, out_dtype, "preact"),
+                   span(workspace, workspace_bytes, "workspace")},
+                  {matrix(x, rows, inner, ldx, dtype, "x"), matrix(w, both, inner, ldw, dtype, "w"),
+                   matrix(x_scale, rows, 1, 1, EEC_F32, "x_scale"), matrix(w_scale, both, 1, 1, EEC_F32, "w_scale"),
+                   matrix(bias, 1, both, both, out_dtype, "bias")}));
+  if (rows == 0 || outer == 0) return ok();
+  const LinearArgs a{rows, outer, inner, x, w, bias, nullptr, ldx, ldw, 0, x_scale, w_scale, dtype, out_dtype, act,
+                     y, preact};
+  launch_gated((hipStream_t)stream, a, (char*)workspace);
+  return launched("gated_linear");
+}
+
+size_t eec_gated_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype) {
+  if (bad_size(rows) || outer < 0 || outer > MAX_WIDTH / 2 || bad_width(inner) || !float_dtype(dtype)) return 0;
+  return gated_bwd_workspace(rows, outer, inner, dtype);
+}
+
+eec_status eec_gated_linear_backward(void* stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                                     int32_t act, const void* gy, int64_t ldgy, const void* x, int64_t ldx,
+                                     const void* w, int64_t ldw, const void* preact, void* gx, void* gw, void* gbias,
+                                     void* workspace, size_t workspace_bytes) {
+  if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
+  TRY(check_act(act));
+  TRY(check_gated(rows, outer, inner));
+  const int64_t both = 2 * outer;
+  if (gx) TRY(check_outputs(rows, inner));
+  if (gw) TRY(check_outputs(both, inner));
+  TRY(check_matrix(gy, rows, outer, ldgy, dtype, "gy"));
+  if (gw) TRY(check_matrix(x, rows, inner, ldx, dtype, "x"));
+  if (gx) TRY(check_matrix(w, both, inner, ldw, dtype, "w"));
+  TRY(check_matrix(preact, rows, both, both, dtype, "preact"));
+  TRY(check_optional(gx, rows, inner, inner, dtype, "gx"));
+  TRY(check_optional(gw, both, inner, inner, dtype, "gw"));
+  TRY(check_optional(gbias, 1, both, both, dtype, "gbias"));
+  TRY(check_ws(workspace, workspace_bytes, gated_bwd_workspace(rows, outer, inner, dtype)));
+  TRY(check_alias({matrix(gx, rows, inner, inner, dtype, "gx"), matrix(gw, both, inner, inner, dtype, "gw"),
+                   matrix(gbias, 1, both, both, dtype, "gbias"), span(workspace, workspace_bytes, "workspace")},
+                  {matrix(gy, rows, outer, ldgy, dtype, "gy"), matrix(x, rows, inner, ldx, dtype, "x"),
+                   matrix(w, both, inner, ldw, dtype, "w"), matrix(preact, rows, both, both, dtype, "preact")}));
+  if (outer == 0 && inner == 0) return ok();
+  const LinearBwdArgs a{rows, outer, inner, gy, x, w, preact, ldgy, ldx, ldw, dtype, act,
+                        rows > 0 && inner > 0 ? gx : nullptr, outer > 0 && inner > 0 ? gw : nullptr,
+                        outer > 0 ? gbias : nullptr};
+  launch_gated_bwd((hipStream_t)stream, a, (char*)workspace);
+  return launched("gated_linear_backward");
 }
 
 }  // extern "C"

@@ -79,39 +79,8 @@ __global__ void __launch_bounds__(256) k_act_grad(ActGrad a) {
 }
 
 
-// The forward's workspace: x and w packed, split sums.
-struct FwdPlan {
-  bool packed;
-  size_t off_x, off_w, off_split, bytes;
-};
-FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
-  FwdPlan p{};
-  const bool exact = dtype == EEC_E4M3 && out_dtype == EEC_F32;  // widened by the general kernel
-  p.packed = !exact && worth_packing(rows, outer, inner, dtype, true) &&
-             (dtype == EEC_F32 || inner * packed_size(dtype) % 16 != 0);
-  size_t at = 0;
-  p.off_x = at;
-  if (p.packed) at += packed_bytes(dtype, rows, inner);
-  p.off_w = at;
-  if (p.packed) at += packed_bytes(dtype, outer, inner);
-  p.off_split = at;
-  p.bytes = at + split_workspace(rows, outer, inner, dtype, p.packed, true);
-  return p;
-}
+}  // namespace
 
-// Rows of a strip at least: four for each wave, so that a few rows are one strip and
-// their column sums need no second launch.
-constexpr int STRIP_ROWS = 16;
-int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
-  const int64_t per = 64 * (dtype == EEC_F32 ? 4 : 8), wide = (cols + per - 1) / per;
-  return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 1024 / std::max<int64_t>(1, wide)));
-}
-
-// The backward's: gz (packed or not), column sums, x and w packed, split sums.
-struct BwdPlan {
-  bool gz, others;  // packed
-  size_t off_gz, off_part, off_xp, off_wp, off_split, bytes;
-};
 BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
   BwdPlan p{};
   if (dtype == EEC_F32) {
@@ -146,36 +115,11 @@ BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int3
   return p;
 }
 
-}  // namespace
-
 size_t linear_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype) {
-  return fwd_plan(rows, outer, inner, dtype, out_dtype).bytes;
+  return fwd_plan(rows, outer, inner, dtype, out_dtype, false).bytes;
 }
 
-void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) {
-  const FwdPlan p = fwd_plan(a.rows, a.outer, a.inner, a.dtype, a.out_dtype);
-  const Epilogue e{a.bias, a.residual, a.ldr, a.x_scale, a.w_scale, a.act, a.y, a.preact, 0, 0, nullptr};
-  by_type(a.out_dtype, [&](auto zero) {
-    using O = decltype(zero);
-    using E = std::conditional_t<std::is_same<O, float>::value, e4m3_wide, e4m3>;
-    Product g{a.x, a.w, a.ldx, a.ldw, a.rows, a.outer, a.inner, 0, 0, 0};
-    if (p.packed) {
-      const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, ws + p.off_x);
-      const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, ws + p.off_w);
-      const Packings both{{x, w}};
-      if (a.dtype == EEC_E4M3)
-        pack<e4m3>(st, both);
-      else
-        pack<O>(st, both);
-      g = Product{x.to, w.to, x.to_ld, w.to_ld, a.rows, a.outer, a.inner, 0, x.plane, w.plane};
-    }
-    float* split = (float*)(ws + p.off_split);
-    if (a.dtype == EEC_E4M3)
-      product<E, O, true, true>(st, g, e, split, a.dtype, p.packed, p.packed);
-    else
-      product<O, O, true, true>(st, g, e, split, a.dtype, p.packed, p.packed);
-  });
-}
+void launch_linear(hipStream_t st, const LinearArgs& a, char* ws) { launch_forward<false>(st, a, ws); }
 
 size_t linear_bwd_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act) {
   return bwd_plan(rows, outer, inner, dtype, act).bytes;
@@ -200,9 +144,17 @@ void launch_linear_bwd(hipStream_t st, const LinearBwdArgs& a, char* ws) {
     }
     const void* gz = packed ? z.to : shaped ? ws + p.off_gz : (const char*)a.gy;
     const int64_t ldgz = packed ? z.to_ld : shaped ? a.outer : a.ldgy;
-    Product gx{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0, z.plane, 0};
-    Product gw{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0, z.plane, 0};
-    if (p.others && products) {
+    if (products) launch_backward_products(st, a, p, gz, ldgz, packed, z.plane, ws);
+  });
+}
+
+void launch_backward_products(hipStream_t st, const LinearBwdArgs& a, const BwdPlan& p, const void* gz, int64_t ldgz,
+                              bool packed, int64_t plane, char* ws) {
+  by_type(a.dtype, [&](auto zero) {
+    using T = decltype(zero);
+    Product gx{gz, a.w, ldgz, a.ldw, a.rows, a.inner, a.outer, 0, plane, 0};
+    Product gw{gz, a.x, ldgz, a.ldx, a.outer, a.inner, a.rows, 0, plane, 0};
+    if (p.others) {
       const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, a.gw ? ws + p.off_xp : nullptr);
       const Packing w = packing(a.dtype, a.w, a.ldw, a.outer, a.inner, a.gx ? ws + p.off_wp : nullptr);
       pack<T>(st, Packings{{x, w}});

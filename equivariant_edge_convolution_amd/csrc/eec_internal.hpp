@@ -175,8 +175,14 @@ size_t norm_bwd_workspace(int64_t rows, int64_t width);
 void launch_norm_bwd(hipStream_t s, int32_t dtype, int64_t rows, int64_t width, const void* gy, int64_t ldgy,
                      const void* sum, int64_t lds, const void* weight, const float* rstd, const void* gsum,
                      int64_t ldgs, void* gx, void* gweight, char* ws);
+// Rows of x as codes (EEC_I8 or EEC_E4M3) with a scale each.
+void launch_quantize(hipStream_t s, int32_t dtype, int32_t codes, int64_t rows, int64_t width, const void* x,
+                     int64_t ldx, void* y, float* scale);
 // out[j] = sum_p part[p][j], rounded to dtype.
 void launch_column_sum(hipStream_t s, int32_t dtype, const float* part, int parts, int64_t n, void* out);
+
+// Terms of a sum of products of 8-bit integers at most: 2^14 each, below 2^31 together.
+constexpr int64_t MAX_INNER_I8 = (1 << 17) - 1;
 
 // One dense layer, or one of its backward products.
 struct LinearArgs {
@@ -196,8 +202,23 @@ struct LinearBwdArgs {
   int32_t dtype, act;
   void *gx, *gw, *gbias;
 };
+// The backward's workspace: gz (packed or not), column sums, x and w packed, split sums.
+struct BwdPlan {
+  bool gz, others;  // packed
+  size_t off_gz, off_part, off_xp, off_wp, off_split, bytes;
+};
+BwdPlan bwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act);
+// gx and gw from gz (rows of ldgz elements; packed: planes `plane` bytes apart).
+void launch_backward_products(hipStream_t s, const LinearBwdArgs& a, const BwdPlan& p, const void* gz, int64_t ldgz,
+                              bool packed, int64_t plane, char* ws);
 size_t linear_bwd_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t act);
 void launch_linear_bwd(hipStream_t s, const LinearBwdArgs& a, char* ws);
+
+// The gated layer: w, bias and preact have 2 outer rows (columns), the gate's first.
+size_t gated_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype);
+void launch_gated(hipStream_t s, const LinearArgs& a, char* ws);
+size_t gated_bwd_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
+void launch_gated_bwd(hipStream_t s, const LinearBwdArgs& a, char* ws);
 
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

@@ -1,12 +1,15 @@
-// Residual addition + root-mean-square norm over the last axis, and its backward.
+// Residual addition + root-mean-square norm over the last axis, and its backward; rows
+// in 8 bits.
 //
 //   s = x + residual (float32, unrounded),  rstd = 1 / sqrt(mean(s^2) + eps),
 //   y = s rstd w;   8-bit rows: scale = max(max|y|, 2^-100) / 448,
 //   q = e4m3(y / scale).
 //   backward, with a = gy w and xhat = s rstd:
 //   gx = rstd (a - xhat mean(a xhat)) + gsum,   gw = sum_rows gy xhat.
+//   rows in 8 bits without a norm: scale = max(max|x|, 2^-100) / most (127 for integers,
+//   448 for e4m3), q = round(x / scale).
 //
-// Both passes are bound by memory: a row is read once into registers, its sums
+// All of them are bound by memory: a row is read once into registers, its sums
 // are taken there, and what is written is written from there.  A row belongs to
 // one wave where it fits 4 accesses of 16 bytes per lane (no barrier at all),
 // to a workgroup of 4 or 16 waves where it is wider, and is read twice by one
@@ -350,6 +353,130 @@ __global__ void __launch_bounds__(1024) k_column_sum(const float* __restrict__ p
   }
 }
 
+// ------------------------------------------------------------------ rows in 8 bits
+
+template <typename Q>
+struct Code;
+template <>
+struct Code<e4m3> {
+  static constexpr float MOST = E4M3_MAX;
+  template <int N>
+  static __device__ __forceinline__ void store(uint8_t* p, int64_t valid, const float (&v)[N]) {
+    store_run_e4m3(p, valid, v);
+  }
+};
+template <>
+struct Code<int8_t> {
+  static constexpr float MOST = 127.f;
+  // The integers next to v (to even), four to a register; 0 for a NaN.
+  template <int N>
+  static __device__ __forceinline__ void store(uint8_t* p, int64_t valid, const float (&v)[N]) {
+    uint32_t q[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      q[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float r = v[4 * i + j];
+        q[i] |= ((uint32_t)(int)rintf(r == r ? r : 0.f) & 255u) << (8 * j);
+      }
+    }
+    if (valid >= N) {
+      __builtin_memcpy(p, q, N);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < valid) p[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+    }
+  }
+};
+
+// x / scale, correctly rounded, with inv = 1 / scale correctly rounded: one correction of
+// x inv by its exact remainder (Markstein 1990) takes three instructions where a division
+// takes ten.  The remainder is exact for scales above 2^-80; other rows are divided.
+template <int N>
+__device__ __forceinline__ void divide_run(float (&v)[N], float scale, float inv) {
+  if (scale > 8.2718061e-25f) {  // 2^-80
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float q = v[i] * inv;
+      v[i] = __builtin_fmaf(__builtin_fmaf(-q, scale, v[i]), inv, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] /= scale;
+  }
+}
+template <typename Q>
+__device__ __forceinline__ float scale_of(float amax) {
+  if (!(amax <= 3.4028235e38f)) return __builtin_nanf("");  // a NaN or an infinity in the row
+  return (amax < AMAX_FLOOR ? AMAX_FLOOR : amax) / Code<Q>::MOST;
+}
+
+struct QuantizeRows {
+  const void* x;
+  int64_t ldx, rows;
+  int width;
+  uint8_t* y;
+  float* scale;
+};
+// As k_norm: a row in the registers of TPR threads, read once.
+template <typename T, typename Q, int TPR, int CH>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_quantize(QuantizeRows a) {
+  constexpr int V = VEC<T>;
+  constexpr int GROUPS = TPR < 256 ? 256 / TPR : 1;
+  __shared__ float red[TPR / 64];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int n = a.width;
+  for (int64_t row = (int64_t)blockIdx.x * GROUPS + grp; row < a.rows; row += (int64_t)gridDim.x * GROUPS) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    float s[CH][V];
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = (c * TPR + t) * V;
+      load_run<true>(x + at, n - at, s[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < V; ++i) amax = nan_max(amax, fabsf(s[c][i]));
+    const float scale = scale_of<Q>(row_reduce<TPR, true>(amax, red)), inv = 1.f / scale;
+    if (t == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = (c * TPR + t) * V;
+      divide_run(s[c], scale, inv);
+      Code<Q>::store(a.y + row * n + at, n - at, s[c]);
+    }
+  }
+}
+// Rows too wide for registers: read twice by one workgroup.
+template <typename T, typename Q>
+__global__ void __launch_bounds__(1024) k_quantize_wide(QuantizeRows a) {
+  constexpr int V = VEC<T>;
+  __shared__ float red[16];
+  const int n = a.width;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    float amax = 0.f;
+    for (int64_t at = threadIdx.x * V; at < n; at += 1024 * V) {
+      float s[V];
+      load_run(x + at, n - at, s);
+#pragma unroll
+      for (int i = 0; i < V; ++i) amax = nan_max(amax, fabsf(s[i]));
+    }
+    const float scale = scale_of<Q>(row_reduce<1024, true>(amax, red)), inv = 1.f / scale;
+    if (threadIdx.x == 0) a.scale[row] = scale;
+    for (int64_t at = threadIdx.x * V; at < n; at += 1024 * V) {
+      float s[V];
+      load_run(x + at, n - at, s);
+      divide_run(s, scale, inv);
+      Code<Q>::store(a.y + row * n + at, n - at, s);
+    }
+  }
+}
+
 // Threads per row and accesses per thread for rows of `width` elements of T, as
 // (TPR, CH); CH = 0: the row does not fit.
 template <typename T, typename F>
@@ -403,6 +530,29 @@ void launch_norm(hipStream_t st, int32_t dtype, int64_t rows, int64_t width, con
         constexpr int B = TPR < 256 ? 256 : TPR, PER = B / TPR;
         const int64_t groups = std::min<int64_t>((rows + PER - 1) / PER, MAX_GROUPS);
         k_norm<T, TPR, CH><<<dim3((unsigned)groups), B, 0, st>>>(in, out);
+      }
+    });
+  });
+}
+
+void launch_quantize(hipStream_t st, int32_t dtype, int32_t codes, int64_t rows, int64_t width, const void* x,
+                     int64_t ldx, void* y, float* scale) {
+  const QuantizeRows a{x, ldx, rows, (int)width, (uint8_t*)y, scale};
+  by_type(dtype, [&](auto zero) {
+    using T = decltype(zero);
+    by_width<T>(width, [&](auto tpr, auto ch) {
+      constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value, B = TPR < 256 ? 256 : TPR, PER = B / TPR;
+      const dim3 grid((unsigned)std::min<int64_t>((rows + PER - 1) / PER, MAX_GROUPS));
+      if constexpr (CH == 0) {
+        if (codes == EEC_I8)
+          k_quantize_wide<T, int8_t><<<grid, B, 0, st>>>(a);
+        else
+          k_quantize_wide<T, e4m3><<<grid, B, 0, st>>>(a);
+      } else {
+        if (codes == EEC_I8)
+          k_quantize<T, int8_t, TPR, CH><<<grid, B, 0, st>>>(a);
+        else
+          k_quantize<T, e4m3, TPR, CH><<<grid, B, 0, st>>>(a);
       }
     });
   });

@@ -3,6 +3,12 @@
 //
 // All products are C[m][n] = sum_k A(m, k) B(n, k), either operand with k along memory
 // or across it.
+//
+// Gated products (G) have two outputs' worth of B: rows 0 to outer - 1 of it are the gate,
+// the others the value, and y = act(gate) value.  Their columns are interleaved, 32 of the
+// gate and the same 32 of the value in turn, so that the 64 columns of a wave hold both
+// halves of 32 outputs and meet in its epilogue; only the rows that B's tiles are loaded
+// from, and that epilogue, differ from a plain product.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -22,7 +28,8 @@ struct Epilogue {
   const float *x_scale, *w_scale;
   int32_t act;
   void *y, *preact;
-  int64_t M, N;
+  int64_t M, N;  // of the product
+  int64_t outer; // gated: columns of y
   float* part;  // split sums [split][M][N] instead of all of the above, or NULL
 };
 
@@ -97,23 +104,60 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
   store_run((O*)e.y + m * e.N + c.n, c.left, v, once);
 }
 
+// Gated: L adjacent columns of gate and value of one row.
+template <typename O, int L>
+__device__ __forceinline__ void finish_gated(const Epilogue& e, int64_t m, const Columns<O, L>& gate,
+                                             const Columns<O, L>& value, float scale, float (&g)[L], float (&v)[L]) {
+  if (m >= e.M) return;
+  if (e.x_scale) {
+    scale_run(g, scale, gate.scale);
+    scale_run(v, scale, value.scale);
+  }
+  if (e.bias) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) g[i] += gate.bias[i], v[i] += value.bias[i];
+  }
+  const bool once = e.outer * (int64_t)sizeof(O) % 128 == 0;
+  if (e.preact) {
+    O* z = (O*)e.preact + m * 2 * e.outer;
+    store_run(z + gate.n, gate.left, g, once);
+    store_run(z + value.n, value.left, v, once);
+  }
+  act_values<O>(g, e.act);
+#pragma unroll
+  for (int i = 0; i < L; ++i) v[i] *= g[i];
+  store_run((O*)e.y + m * e.outer + gate.n, gate.left, v, once);
+}
+// Column of the product that holds the gate of output h; the value is 32 further.
+__device__ __forceinline__ int64_t gate_column(int64_t h) { return (h >> 5) * 64 + (h & 31); }
+// Row of B that a line (a column of the product) comes from; lines past the end, which are not stored, repeat the last.
+__device__ __forceinline__ int64_t gated_row(int64_t line, int64_t outer) {
+  return min((line >> 6) * 32 + (line & 31), outer - 1) + (line & 32 ? outer : 0);
+}
+
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // Chunk c (four adjacent columns) of a row of a wave's sums.
 __device__ __forceinline__ void put_sums(char* rows, int row, int c, const f32x4& v) {
   __builtin_memcpy(__builtin_assume_aligned(rows + (row * 256 + (c ^ (row & 15)) * 16), 16), &v, 16);
 }
 // The tiles as the matrix instructions leave them: 16 rows x 4 x 16 columns, 32 x 2 x 32.
-__device__ __forceinline__ void put_tile(const f32x4 (&acc)[4], char* rows) {
+// Sums of integers are exact, and rounded once here.
+__device__ __forceinline__ f32x4 as_floats(const f32x4& v) { return v; }
+__device__ __forceinline__ f32x4 as_floats(const i32x4& v) { return __builtin_convertvector(v, f32x4); }
+template <typename Acc>
+__device__ __forceinline__ void put_tile(const Acc (&acc)[4], char* rows) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), acc[j]);
+  for (int j = 0; j < 4; ++j) put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), as_floats(acc[j]));
 }
-__device__ __forceinline__ void put_tile(const f32x16 (&acc)[2], char* rows) {
+template <typename Acc>
+__device__ __forceinline__ void put_tile(const Acc (&acc)[2], char* rows) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const f32x4 v = {acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]};
+      const f32x4 v = {(float)acc[j][4 * a], (float)acc[j][4 * a + 1], (float)acc[j][4 * a + 2], (float)acc[j][4 * a + 3]};
       put_sums(rows, threadIdx.x & 31, j * 8 + a * 2 + (threadIdx.x >> 5 & 1), v);
     }
 }
@@ -198,27 +242,132 @@ __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
-// Adds the splits in order and finishes: 4 columns a thread.
-template <typename O>
-__global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
-  const int64_t per_row = (e.N + 3) / 4, total = e.M * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / per_row, n = i % per_row * 4;
-    float v[4] = {};
-    for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads on their way
-      float t[8][4];
+// The same for a gated product: a lane takes L outputs, whose gate and value lie 128 bytes
+// apart in its row of the LDS.
+template <typename O, int HIGH, int PER, typename Acc, int GROUPS, int NB>
+__device__ __forceinline__ void finish_wave_gated(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split,
+                                                  Acc (&acc)[GROUPS][NB]) {
+  constexpr int ROWS = PER * HIGH, ALL = GROUPS * HIGH;
+  constexpr int L = 16 / (int)sizeof(O), APART = 2 * L;  // outputs of a lane, rows of one access
+  constexpr int TOGETHER = ROWS / APART < 4 ? ROWS / APART : 4, BATCH = TOGETHER * APART;
+  static_assert(ROWS % BATCH == 0, "whole accesses");
+  const int64_t h0 = n0 / 2;
+  const int lane = threadIdx.x & 63, columns = (int)min((int64_t)32, e.outer - h0);
+  float* part = e.part ? e.part + split * e.M * e.N : nullptr;
+  const int r0 = lane / (32 / L), col = lane % (32 / L) * L;
+  const bool whole = col + L <= columns;
+  const Columns<O, L> gate(e, h0 + col, whole ? L : 0), value(e, e.outer + h0 + col, whole ? L : 0);
+  float next[TOGETHER];
+  const auto load = [&](int row) {
+    if (!e.x_scale || row - r0 >= ALL) return;
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        load_run(e.part + ((int64_t)(s0 + s) * e.M + m) * e.N + n, s0 + s < splits ? e.N - n : 0, t[s]);
+    for (int i = 0; i < TOGETHER; ++i)
+      if (m0 + row + i * APART < e.M) next[i] = e.x_scale[m0 + row + i * APART];
+  };
+  load(r0);
+#pragma unroll 1
+  for (int g = 0; g < GROUPS; g += PER) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
+    for (int i = 0; i < PER; ++i) put_tile(acc[i], lds + i * HIGH * 256);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] += t[s][c];
+    for (int i = 0; i < GROUPS; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = i + PER < GROUPS ? acc[i + PER < GROUPS ? i + PER : 0][j] : Acc{};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int64_t top = m0 + g * HIGH;
+    const auto sums = [&](int row, int at, float* to, int bytes) {
+      __builtin_memcpy(to, lds + (row * 256 + ((at / 4) ^ (row & 15)) * 16 + at % 4 * 4), bytes);
+    };
+    if (whole) {
+#pragma unroll 1
+      for (int r = r0; r < ROWS; r += BATCH) {
+        float scale[TOGETHER];
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) scale[i] = next[i];
+        load(g * HIGH + r + BATCH);
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) {
+          const int row = r + i * APART;
+          float a[L], v[L];
+#pragma unroll
+          for (int u = 0; u < L; u += 4) {
+            const int c = (col + u) / 4;
+            __builtin_memcpy(&a[u], __builtin_assume_aligned(lds + (row * 256 + (c ^ (row & 15)) * 16), 16), 16);
+            __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + ((c + 8) ^ (row & 15)) * 16), 16), 16);
+          }
+          if (part == nullptr) {
+            finish_gated<O, L>(e, top + row, gate, value, scale[i], a, v);
+          } else if (top + row < e.M) {
+            float* to = part + (top + row) * e.N + n0 + col;
+            store_run(to, L, a);
+            store_run(to + 32, L, v);
+          }
+        }
+      }
     }
-    const Columns<O, 4> c(e, n, e.N - n);
-    Incoming<O, 4> in;
-    in.load(e, m, c);
-    finish_run<O, 4>(e, m, c, in, v);
+    // the last outputs that make no whole run: a row a lane, an output at a time
+    if (columns % L > 0 && lane < ROWS) {
+      const int64_t m = top + lane;
+#pragma unroll 1
+      for (int at = columns / L * L; at < columns; ++at) {
+        float a[1], v[1];
+        sums(lane, at, a, 4);
+        sums(lane, at + 32, v, 4);
+        if (part == nullptr) {
+          const Columns<O, 1> one(e, h0 + at, 1), two(e, e.outer + h0 + at, 1);
+          finish_gated<O, 1>(e, m, one, two, e.x_scale && m < e.M ? e.x_scale[m] : 0.f, a, v);
+        } else if (m < e.M) {
+          float* to = part + m * e.N + n0 + at;
+          to[0] = a[0];
+          to[32] = v[0];
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+template <bool G, typename O, int HIGH, int PER, typename Acc, int GROUPS, int NB>
+__device__ __forceinline__ void finish(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split,
+                                       Acc (&acc)[GROUPS][NB]) {
+  if constexpr (G)
+    finish_wave_gated<O, HIGH, PER>(e, lds, m0, n0, split, acc);
+  else
+    finish_wave<O, HIGH, PER>(e, lds, m0, n0, split, acc);
+}
+
+// Four adjacent columns of row m, the splits added in order.
+__device__ __forceinline__ void join_run(const Epilogue& e, int splits, int64_t m, int64_t n, int64_t left, float (&v)[4]) {
+  for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads on their way
+    float t[8][4];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      load_run(e.part + ((int64_t)(s0 + s) * e.M + m) * e.N + n, s0 + s < splits ? left : 0, t[s]);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += t[s][c];
+  }
+}
+// Adds the splits in order and finishes: 4 columns (outputs) a thread.
+template <typename O, bool G = false>
+__global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
+  const int64_t width = G ? e.outer : e.N, per_row = (width + 3) / 4, total = e.M * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / per_row, n = i % per_row * 4, left = width - n;
+    if constexpr (G) {
+      float a[4] = {}, v[4] = {};
+      join_run(e, splits, m, gate_column(n), left, a);
+      join_run(e, splits, m, gate_column(n) + 32, left, v);
+      const Columns<O, 4> gate(e, n, left), value(e, e.outer + n, left);
+      finish_gated<O, 4>(e, m, gate, value, e.x_scale ? e.x_scale[m] : 0.f, a, v);
+    } else {
+      float v[4] = {};
+      join_run(e, splits, m, n, left, v);
+      const Columns<O, 4> c(e, n, left);
+      Incoming<O, 4> in;
+      in.load(e, m, c);
+      finish_run<O, 4>(e, m, c, in, v);
+    }
   }
 }
 
@@ -251,6 +400,7 @@ struct Mat;  // operand planes in LDS (element type, count), and the product of 
 template <>
 struct Mat<f16> {
   using E = f16;
+  using Acc = f32x4;
   static constexpr int PLANES = 1;
   using Frag = f16x8;
   static __device__ __forceinline__ f32x4 mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 c) {
@@ -260,6 +410,7 @@ struct Mat<f16> {
 template <>
 struct Mat<bf16> {
   using E = bf16;
+  using Acc = f32x4;
   static constexpr int PLANES = 1;
   using Frag = bf16x8;
   static __device__ __forceinline__ f32x4 mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 c) {
@@ -278,10 +429,22 @@ struct Mat<bf16> {
 template <>
 struct Mat<e4m3> {
   using E = e4m3;
+  using Acc = f32x4;
   static constexpr int PLANES = 1;
   using Frag = long;
   static __device__ __forceinline__ f32x4 mul(const Frag (&b)[1], const Frag (&a)[1], f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b[0], a[0], c, 0, 0, 0);
+  }
+};
+// 8-bit integers: sums of up to MAX_INNER_I8 products of (-128)^2 are exact in 32 bits.
+template <>
+struct Mat<int8_t> {
+  using E = int8_t;
+  using Acc = i32x4;
+  static constexpr int PLANES = 1;
+  using Frag = long;
+  static __device__ __forceinline__ i32x4 mul(const Frag (&b)[1], const Frag (&a)[1], i32x4 c) {
+    return __builtin_amdgcn_mfma_i32_16x16x32_i8(b[0], a[0], c, 0, 0, 0);
   }
 };
 struct e4m3_wide : e4m3 {};
@@ -290,6 +453,7 @@ struct Mat<e4m3_wide> : Mat<bf16> {};
 template <>
 struct Mat<float> {
   using E = bf16;
+  using Acc = f32x4;
   static constexpr int PLANES = 3;
   using Frag = bf16x8;
   // The part products in rising size.  The three left out have the sign of the whole: each
@@ -374,7 +538,7 @@ __device__ __forceinline__ Place place_of(int64_t M, int64_t N) {
 // A tile of LINES lines x 32 k of one operand, an 8-element chunk per thread (two
 // with 128 lines).  KC: k runs along memory (a chunk is one run), otherwise the
 // lines do (a chunk is 8 runs of R lines).
-template <typename T, bool KC, int LINES>
+template <typename T, bool KC, int LINES, bool G = false>
 struct Stage {
   static constexpr int R = LINES / 64;
   static constexpr int ROW = GBK * sizeof(typename Mat<T>::E) + 8 * sizeof(typename Mat<T>::E);
@@ -387,7 +551,8 @@ struct Stage {
       const int64_t k = k0 + (threadIdx.x & 3) * 8, left = k_end - k;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const int64_t line = min(line0 + (threadIdx.x >> 2) + 64 * i, lines - 1);  // lines past the end: not stored
+        const int64_t l = line0 + (threadIdx.x >> 2) + 64 * i;
+        const int64_t line = G ? gated_row(l, lines) : min(l, lines - 1);  // lines past the end: not stored
         load_raw(p + line * ld + k, left, r[i].v);
       }
     } else {
@@ -418,14 +583,14 @@ struct Stage {
 // k-major ones are turned) into LDS rows of 32 k; the next two steps' loads are in
 // flight while the present one is multiplied.  B is the first factor of the matrix
 // instruction, so a lane holds four adjacent columns of one row of C.
-template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI>
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, bool G = false>
 __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   static_assert(WM * WN == 4, "four waves");
   constexpr int BM = WM * MI * 16, BN = WN * 64;
   using M_ = Mat<T>;
   constexpr int P = M_::PLANES;
   using SA = Stage<T, A_KC, BM>;
-  using SB = Stage<T, B_KC, BN>;
+  using SB = Stage<T, B_KC, BN, G>;
   // sums: 4 KB of each wave for a matrix tile, two tiles at a time
   constexpr int PER = MI > 1 ? 2 : 1, TILES = P * (SA::PLANE + SB::PLANE), SUMS = 4 * PER * 4096;
   __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
@@ -435,7 +600,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   const int64_t m0 = place.m, n0 = place.n;
   const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
-  f32x4 acc[MI][4] = {};
+  typename M_::Acc acc[MI][4] = {};
   SA sa[2];
   SB sb[2];
   auto load = [&](int s, int64_t k) {
@@ -475,7 +640,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
     if (k + GBK < ke) step(1, k + GBK);
   }
   __syncthreads();
-  finish_wave<O, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, acc);
+  finish<G, O, 16, PER>(e, lds + wave * PER * 4096, m0 + wm, n0 + wn, place.split, acc);
 }
 
 // ------------------------------------------------------------------ tiled product (16- and 8-bit, aligned)
@@ -498,7 +663,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 //       banks.  Only the low bits of a chunk's place depend on the lane, so a few
 //       address registers serve all fragments.
 // Neither has a bank conflict by the counter.
-template <typename T, bool KC, int LINES, int WAVES>
+template <typename T, bool KC, int LINES, int WAVES, bool G = false>
 struct Tile {
   static constexpr int BK = 64 / (int)sizeof(T);          // k of a tile
   static constexpr int LOADS = LINES / 16 / WAVES;        // direct loads of one wave
@@ -529,14 +694,19 @@ struct Tile {
     return PER_LOAD == 2 ? (u & 9) | (u & 2) << 1 | (u >> 1 & 2) : (u & 4) | (u & 1) << 1 | (u >> 1 & 1);
   }
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t line0, int64_t lines, int64_t k0) {
+    static_assert(!G || (KC && LOADS * 16 <= 32), "a wave loads lines of one half");
     const int lane = threadIdx.x & 63;
-    base = (const char*)p + (KC ? (line0 * ld + k0) : (k0 * ld + line0)) * (int64_t)sizeof(T);
+    // gated: the wave's lines are all of the gate, or all of the value
+    const int64_t first = G ? line0 / 2 + (place(0) * 16 & 32 ? lines : 0) : line0;
+    base = (const char*)p + (KC ? (first * ld + k0) : (k0 * ld + line0)) * (int64_t)sizeof(T);
     step = (KC ? (int64_t)BK : (int64_t)BK * ld) * (int64_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       if constexpr (KC) {
         const int r = place(i) * 16 + (lane >> 2), c = (lane & 3) ^ (r >> 2 & 3);
-        const int64_t line = min((int64_t)r, lines - 1 - line0);  // lines past the end: not stored
+        // lines past the end: not stored
+        const int64_t line = G ? min((int64_t)((r >> 6) * 32 + (r & 31)), lines - 1 - line0 / 2)
+                               : min((int64_t)r, lines - 1 - line0);
         off[i] = (uint32_t)(line * ld * (int64_t)sizeof(T)) + c * 16;
       } else {
         const int k = at_k(i), c = (lane % CHUNKS) ^ (k % PER_LOAD * 2);
@@ -606,7 +776,7 @@ struct Tile {
 template <typename T, int MI>
 struct Share {
   static constexpr int ROWS = 16, GROUPS = MI;  // rows of a matrix tile, tiles along m
-  static constexpr int NB = 4, AHEAD = 2;
+  static constexpr int NB = 4, AHEAD = 2, PRODUCTS = NB;  // PRODUCTS: instructions of one group
   using Frag = typename Mat<T>::Frag;
   f32x4 acc[GROUPS][NB] = {};
   __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {
@@ -617,11 +787,24 @@ struct Share {
 template <int MI>
 struct Share<e4m3, MI> {
   static constexpr int ROWS = 32, GROUPS = MI / 2;
-  static constexpr int NB = 2, AHEAD = 1;
+  static constexpr int NB = 2, AHEAD = 1, PRODUCTS = NB;
   using Frag = i32x8;
   f32x16 acc[GROUPS][NB] = {};
   __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {  // block scales of 2^0
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+  }
+};
+template <int MI>
+struct Share<int8_t, MI> {
+  static constexpr int ROWS = 32, GROUPS = MI / 2;
+  static constexpr int NB = 2, AHEAD = 1, PRODUCTS = 2 * NB;
+  using Frag = i32x8;
+  i32x16 acc[GROUPS][NB] = {};
+  __device__ __forceinline__ void mul(int i, int j, const Frag& b, const Frag& a) {
+    const i32x4 b0 = __builtin_shufflevector(b, b, 0, 1, 2, 3), b1 = __builtin_shufflevector(b, b, 4, 5, 6, 7);
+    const i32x4 a0 = __builtin_shufflevector(a, a, 0, 1, 2, 3), a1 = __builtin_shufflevector(a, a, 4, 5, 6, 7);
+    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b0, a0, acc[i][j], 0, 0, 0);
+    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b1, a1, acc[i][j], 0, 0, 0);
   }
 };
 template <typename S>
@@ -663,7 +846,7 @@ __device__ __forceinline__ void multiply(S& c, const Ahead<S>& f, const char* la
       __builtin_amdgcn_sched_group_barrier(0x100, TA::READS, 0);
     else
       __builtin_amdgcn_sched_group_barrier(0x100, TA::READS + TB::READS, 0);
-    __builtin_amdgcn_sched_group_barrier(0x008, S::NB, 0);  // products
+    __builtin_amdgcn_sched_group_barrier(0x008, S::PRODUCTS, 0);  // products
   }
 }
 
@@ -685,12 +868,12 @@ __device__ __forceinline__ void tile_barrier() {
 // six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, 43 with
 // eight).
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
-template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS>
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS, bool G = false>
 __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
   using TA = Tile<T, A_KC, BM, WAVES>;
-  using TB = Tile<T, B_KC, BN, WAVES>;
+  using TB = Tile<T, B_KC, BN, WAVES, G>;
   constexpr int BK = TA::BK, LOADS = TA::LOADS + TB::LOADS;
   // The buffers are variables of their own: the compiler then sees that loads into
   // one do not touch the others, and does not wait for them before it reads.
@@ -756,7 +939,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   static_assert(TA::BYTES >= SUMS * 256 && TB::BYTES >= SUMS * 256 && WAVES <= 8, "room for the sums");
   const int pair = wave >> 1;
   char *even = pair == 0 ? a0 : pair == 1 ? a1 : pair == 2 ? a2 : a3, *odd = pair == 0 ? b0 : pair == 1 ? b1 : pair == 2 ? b2 : b3;
-  finish_wave<O, S::ROWS, SUMS / S::ROWS>(e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, c.acc);
+  finish<G, O, S::ROWS, SUMS / S::ROWS>(e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, c.acc);
 #endif
 }
 
@@ -766,11 +949,11 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
 // (k_pack: k in whole groups of four tiles).  A step is 32 k of all six planes,
 // 72 KB of LDS, and does all six part products, so a plane is loaded once; two
 // buffers: a step's 96 products a wave take 3100 cycles, the next one's loads 1900.
-template <bool A_KC, bool B_KC>
+template <bool A_KC, bool B_KC, bool G = false>
 __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
 #ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
   using TA = Tile<bf16, A_KC, 256, 8>;
-  using TB = Tile<bf16, B_KC, 128, 8>;
+  using TB = Tile<bf16, B_KC, 128, 8, G>;
   __shared__ __attribute__((aligned(1024))) char a0[3 * TA::BYTES], a1[3 * TA::BYTES], b0[3 * TB::BYTES], b1[3 * TB::BYTES];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const Place place = place_of<256, 128>(e.M, e.N);
@@ -821,7 +1004,7 @@ __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
   tile_barrier<0>();
   // 64 rows of sums in 16 KB for each wave: three in an A buffer, one in a B buffer
   char* mine = wave < 3 ? a0 + wave * 16384 : wave < 6 ? a1 + (wave - 3) * 16384 : wave == 6 ? b0 : b1;
-  finish_wave<float, 16, 4>(e, mine, m0 + wm, n0 + wn, place.split, acc);
+  finish<G, float, 16, 4>(e, mine, m0 + wm, n0 + wn, place.split, acc);
 #endif
 }
 
@@ -831,24 +1014,27 @@ __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
 // memory straight into the first factor of the matrix instruction, once, x (a few
 // rows, in the L2) into the second.  The 8 waves deal runs of 128 bytes of k in
 // turn and are joined in LDS, in wave order, so one launch does it all.
-template <typename T, typename O, int MT>
+// Gated: 8 rows of the gate and the same 8 of the value, which meet after the join.
+template <typename T, typename O, int MT, bool G = false>
 __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   using M_ = Mat<T>;
   constexpr int WAVES = 8, P = M_::PLANES;
   constexpr int CHUNK = sizeof(T) == 4 ? 32 : sizeof(T) == 2 ? 64 : 128;  // k of one run
   constexpr int STEPS = CHUNK / 32;                                      // matrix steps of one run
   constexpr int TOGETHER = MT == 1 ? 4 : 2;                              // runs in flight
-  __shared__ f32x4 join[WAVES][MT][64];
+  __shared__ typename M_::Acc join[WAVES][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const T* w = (const T*)g.b + min(n0 + (lane & 15), g.N - 1) * g.ldb;
+  const int64_t n0 = (int64_t)blockIdx.x * (G ? 8 : 16);
+  const int64_t line = G ? min(n0 + (lane & 7), g.N - 1) + (lane & 8 ? g.N : 0) : min(n0 + (lane & 15), g.N - 1);
+  const T* w = (const T*)g.b + line * g.ldb;
   const T* x[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = (const T*)g.a + min((int64_t)(t * 16 + (lane & 15)), g.M - 1) * g.lda;
-  f32x4 acc[MT] = {};
+  typename M_::Acc acc[MT] = {};
   // the epilogue's inputs set out first, and are there when the sums are
   const int64_t m = wave * 16 + (lane & 15);
-  const Columns<O, 4> columns(e, n0 + q * 4, wave < MT ? e.N - n0 - q * 4 : 0);
+  const int64_t n = n0 + (G ? q & 1 : q) * 4, left = wave < MT ? (G ? e.outer : e.N) - n : 0;
+  const Columns<O, 4> columns(e, n, left), value(e, G ? e.outer + n : n, G ? left : 0);
   Incoming<O, 4> in;
   if (wave < MT) in.load(e, m, columns);
   // A run of CHUNK k: lane group q holds STEPS * 8 adjacent ones, of which step s
@@ -919,11 +1105,18 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   }
   __syncthreads();
   if (wave < MT) {
-    f32x4 v = join[0][wave][lane];
+    typename M_::Acc v = join[0][wave][lane];
 #pragma unroll
     for (int i = 1; i < WAVES; ++i) v += join[i][wave][lane];
-    float r[4] = {v[0], v[1], v[2], v[3]};
-    if (n0 + q * 4 < e.N) finish_run<O, 4>(e, m, columns, in, r);
+    float r[4] = {(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+    if constexpr (G) {
+      float b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __shfl_xor(r[i], 32);
+      if (q < 2 && n < e.outer) finish_gated<O, 4>(e, m, columns, value, in.scale, r, b);
+    } else {
+      if (n0 + q * 4 < e.N) finish_run<O, 4>(e, m, columns, in, r);
+    }
   }
 }
 
@@ -972,7 +1165,8 @@ __global__ void __launch_bounds__(256) k_pack(Packings all) {
 
 constexpr int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // Element size of `dtype`'s packed form, its stride, rows and bytes.
-inline int packed_size(int32_t dtype) { return dtype == EEC_E4M3 ? 1 : 2; }
+inline bool eight_bits(int32_t dtype) { return dtype == EEC_E4M3 || dtype == EEC_I8; }
+inline int packed_size(int32_t dtype) { return eight_bits(dtype) ? 1 : 2; }
 inline Packing packing(int32_t dtype, const void* from, int64_t ld, int64_t rows, int64_t cols, char* to) {
   Packing p{from, ld, rows, cols, to, 0, 0, 0};
   p.to_ld = up(cols, 128);
@@ -1028,7 +1222,7 @@ inline bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype, bool f
     const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
     if (tiles * (K >= 1024 ? K / 256 : 1) < 100) return false;
   }
-  const double least = !forward || dtype == EEC_F32 ? 4e8 : dtype == EEC_E4M3 ? 3e9 : 5e9;
+  const double least = !forward || dtype == EEC_F32 ? 4e8 : eight_bits(dtype) ? 3e9 : 5e9;
   return (double)M * N >= 96.0 * (M + N) && (double)M * N * K >= least;
 }
 
@@ -1051,7 +1245,7 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool ti
   // the small ones, two workgroups with four buffers share a CU instead: bf16 with
   // bias, GELU and residual, 1536 x 2816 x 1024 24 us (large tiles 35), 2048 x 4096 x
   // 1024 31 (38), x 4096 87 (99, split); beyond, split large tiles are even.
-  const double steps = (double)K * (dtype == EEC_E4M3 ? 1 : 2) / 64;
+  const double steps = (double)K * (eight_bits(dtype) ? 1 : 2) / 64;
   const double us128 = (double)((t128 + 255) / 256) * (10 + 0.25 * steps);
   const double us256 = (double)((t256 + 255) / 256) * (20 + 0.49 * steps);
   const bool shared = t128 > 256 && t128 <= 512 && steps <= 128;
@@ -1091,8 +1285,11 @@ inline bool tiled_operand(const void* p, int64_t ld, int64_t along, int size) {
 // its threads (256 for a 128 x 128 tile, 512 for a 256 x 256 one) are counted in 32 bits.
 constexpr int64_t LAUNCH_ROWS = int64_t(1) << 30;
 
-// One product; packed_*: the operand is as k_pack leaves it.
-template <typename T, typename O, bool A_KC, bool B_KC>
+// Columns of a gated product.
+constexpr int64_t gated_columns(int64_t outer) { return up(outer, 32) * 2; }
+
+// One product; packed_*: the operand is as k_pack leaves it.  Gated: g.N is outer.
+template <typename T, typename O, bool A_KC, bool B_KC, bool G = false>
 void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bool packed_a, bool packed_b) {
   if (g.M == 0 || g.N == 0) return;
   if constexpr (A_KC) {  // the rows of gw are columns, at most 2^27
@@ -1104,21 +1301,22 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
       rest.M -= first;
       rest.a = (const T*)g.a + first * g.lda;
       to.y = (O*)e.y + first * g.N;
-      if (e.preact) to.preact = (O*)e.preact + first * g.N;
+      if (e.preact) to.preact = (O*)e.preact + first * g.N * (G ? 2 : 1);
       if (e.residual) to.residual = (const O*)e.residual + first * e.ldr;
       if (e.x_scale) to.x_scale = e.x_scale + first;
-      product<T, O, A_KC, B_KC>(st, g, e, ws, dtype, packed_a, packed_b);
-      return product<T, O, A_KC, B_KC>(st, rest, to, ws, dtype, packed_a, packed_b);
+      product<T, O, A_KC, B_KC, G>(st, g, e, ws, dtype, packed_a, packed_b);
+      return product<T, O, A_KC, B_KC, G>(st, rest, to, ws, dtype, packed_a, packed_b);
     }
   }
   const bool packed = packed_a && packed_b;
   const bool aligned = dtype != EEC_F32 && !std::is_same<T, e4m3_wide>::value &&
                        (packed_a || tiled_operand(g.a, g.lda, A_KC ? g.K : g.M, sizeof(T))) &&
                        (packed_b || tiled_operand(g.b, g.ldb, B_KC ? g.K : g.N, sizeof(T)));
-  const Plan p = plan_product(g.M, g.N, g.K, dtype, aligned, packed, A_KC && B_KC);
-  g.k_split = p.k_split;
   e.M = g.M;
-  e.N = g.N;
+  e.N = G ? gated_columns(g.N) : g.N;
+  e.outer = g.N;
+  const Plan p = plan_product(e.M, e.N, g.K, dtype, aligned, packed, A_KC && B_KC);
+  g.k_split = p.k_split;
   e.part = p.splits > 1 ? ws : nullptr;
   const dim3 grid((unsigned)(p.tiles * p.splits));
   Product t = g;
@@ -1127,22 +1325,22 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   if (packed_b && !B_KC) t.N = t.ldb;
   if constexpr (std::is_same<T, float>::value) {
     t.K = up(g.K, 128);
-    if (p.kind == PARTED) k_parted<A_KC, B_KC><<<grid, 512, 0, st>>>(t, e);
+    if (p.kind == PARTED) k_parted<A_KC, B_KC, G><<<grid, 512, 0, st>>>(t, e);
   } else if constexpr (!std::is_same<T, e4m3_wide>::value) {
-    if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8, 4><<<grid, 512, 0, st>>>(t, e);
-    if (p.kind == TILE128X2) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 4><<<grid, 256, 0, st>>>(t, e);
-    if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 8><<<grid, 256, 0, st>>>(t, e);
+    if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8, 4, G><<<grid, 512, 0, st>>>(t, e);
+    if (p.kind == TILE128X2) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 4, G><<<grid, 256, 0, st>>>(t, e);
+    if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 8, G><<<grid, 256, 0, st>>>(t, e);
   }
   if constexpr (A_KC && B_KC) {
-    const dim3 columns((unsigned)((g.N + 15) / 16));
-    if (p.kind == FEW && g.M <= 16) k_few<T, O, 1><<<columns, 512, 0, st>>>(g, e);
-    if (p.kind == FEW && g.M > 16) k_few<T, O, 2><<<columns, 512, 0, st>>>(g, e);
+    const dim3 columns((unsigned)(G ? (g.N + 7) / 8 : (g.N + 15) / 16));
+    if (p.kind == FEW && g.M <= 16) k_few<T, O, 1, G><<<columns, 512, 0, st>>>(g, e);
+    if (p.kind == FEW && g.M > 16) k_few<T, O, 2, G><<<columns, 512, 0, st>>>(g, e);
   }
-  if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC, 2, 2, 4><<<grid, 256, 0, st>>>(g, e);
-  if (p.kind == SMALL) k_product<T, O, A_KC, B_KC, 4, 1, 1><<<grid, 256, 0, st>>>(g, e);
+  if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC, 2, 2, 4, G><<<grid, 256, 0, st>>>(g, e);
+  if (p.kind == SMALL) k_product<T, O, A_KC, B_KC, 4, 1, 1, G><<<grid, 256, 0, st>>>(g, e);
   if (p.splits > 1) {
     const int64_t runs = g.M * ((g.N + 3) / 4);
-    k_join_splits<O><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)p.splits);
+    k_join_splits<O, G><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)p.splits);
   }
 }
 
@@ -1151,6 +1349,67 @@ void by_type(int32_t dtype, F&& f) {
   if (dtype == EEC_F32) return f(float());
   if (dtype == EEC_F16) return f(f16());
   f(bf16());
+}
+
+// ------------------------------------------------------------------ a layer's forward pass
+
+// Its workspace: x and w packed, split sums.  Gated: w has 2 outer rows.
+struct FwdPlan {
+  bool packed;
+  size_t off_x, off_w, off_split, bytes;
+};
+inline FwdPlan fwd_plan(int64_t rows, int64_t outer, int64_t inner, int32_t dtype, int32_t out_dtype, bool gated) {
+  FwdPlan p{};
+  const int64_t lines = gated ? 2 * outer : outer, columns = gated ? gated_columns(outer) : outer;
+  const bool exact = dtype == EEC_E4M3 && out_dtype == EEC_F32;  // widened by the general kernel
+  p.packed = !exact && worth_packing(rows, lines, inner, dtype, true) &&
+             (dtype == EEC_F32 || inner * packed_size(dtype) % 16 != 0);
+  size_t at = 0;
+  p.off_x = at;
+  if (p.packed) at += packed_bytes(dtype, rows, inner);
+  p.off_w = at;
+  if (p.packed) at += packed_bytes(dtype, lines, inner);
+  p.off_split = at;
+  p.bytes = at + split_workspace(rows, columns, inner, dtype, p.packed, true);
+  return p;
+}
+
+template <bool G>
+void launch_forward(hipStream_t st, const LinearArgs& a, char* ws) {
+  const FwdPlan p = fwd_plan(a.rows, a.outer, a.inner, a.dtype, a.out_dtype, G);
+  const Epilogue e{a.bias, a.residual, a.ldr, a.x_scale, a.w_scale, a.act, a.y, a.preact, 0, 0, 0, nullptr};
+  by_type(a.out_dtype, [&](auto zero) {
+    using O = decltype(zero);
+    using E = std::conditional_t<std::is_same<O, float>::value, e4m3_wide, e4m3>;
+    Product g{a.x, a.w, a.ldx, a.ldw, a.rows, a.outer, a.inner, 0, 0, 0};
+    if (p.packed) {
+      const Packing x = packing(a.dtype, a.x, a.ldx, a.rows, a.inner, ws + p.off_x);
+      const Packing w = packing(a.dtype, a.w, a.ldw, G ? 2 * a.outer : a.outer, a.inner, ws + p.off_w);
+      const Packings both{{x, w}};
+      if (eight_bits(a.dtype))
+        pack<e4m3>(st, both);  // bytes, of either kind
+      else
+        pack<O>(st, both);
+      g = Product{x.to, w.to, x.to_ld, w.to_ld, a.rows, a.outer, a.inner, 0, x.plane, w.plane};
+    }
+    float* split = (float*)(ws + p.off_split);
+    if (a.dtype == EEC_E4M3)
+      product<E, O, true, true, G>(st, g, e, split, a.dtype, p.packed, p.packed);
+    else if (a.dtype == EEC_I8)
+      product<int8_t, O, true, true, G>(st, g, e, split, a.dtype, p.packed, p.packed);
+    else
+      product<O, O, true, true, G>(st, g, e, split, a.dtype, p.packed, p.packed);
+  });
+}
+
+// ------------------------------------------------------------------ gradient of the activation
+
+// Rows of a strip at least: four for each wave, so that a few rows are one strip and
+// their column sums need no second launch.
+constexpr int STRIP_ROWS = 16;
+inline int64_t act_grad_strips(int64_t rows, int64_t cols, int32_t dtype) {
+  const int64_t per = 64 * (dtype == EEC_F32 ? 4 : 8), wide = (cols + per - 1) / per;
+  return std::max<int64_t>(1, std::min<int64_t>((rows + STRIP_ROWS - 1) / STRIP_ROWS, 1024 / std::max<int64_t>(1, wide)));
 }
 
 }  // namespace

@@ -405,7 +405,8 @@ EEC_API size_t eec_workspace_bytes(int32_t n_atoms, int64_t n_edges, const eec_m
  *   - NaN and infinities propagate by the formulas.  Sizes may be odd, one, or
  *     zero (a sum over nothing is 0).  Rows and strides are at most 2^31 - 1,
  *     columns (width, outer, inner) 2^27, and a product has at most 2^36 outputs. */
-typedef enum { EEC_F32 = 0, EEC_F16 = 1, EEC_BF16 = 2, EEC_E4M3 = 3 /* OCP: max 448, no infinity */ } eec_dtype;
+typedef enum { EEC_F32 = 0, EEC_F16 = 1, EEC_BF16 = 2, EEC_E4M3 = 3 /* OCP: max 448, no infinity */,
+               EEC_I8 = 4 /* signed 8-bit integers: operands of a layer */ } eec_dtype;
 typedef enum {
   EEC_ACT_NONE = 0,
   EEC_ACT_RELU = 1,
@@ -449,13 +450,25 @@ EEC_API eec_status eec_add_rms_norm_backward(void *stream, int64_t rows, int64_t
                                      void *gx, void *gweight, void *workspace, size_t workspace_bytes);
 EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t width);
 
+/* eec_quantize_rows -- rows in 8 bits, as eec_linear takes them: tokens (rows of x) and
+ * channels (rows of w) alike.  Per row of `width` (>= 1) elements
+ *   scale = max(max_j |x_j|, 2^-100) / 127 (EEC_I8) or / 448 (EEC_E4M3),
+ *   y_j   = x_j / scale, rounded to the nearest code (to even);
+ * scale and quotient are float32, each correctly rounded.
+ *   dtype   EEC_F32, EEC_F16 or EEC_BF16: the type of x
+ *   codes   EEC_I8 (codes -127 to 127) or EEC_E4M3: the type of y
+ *   y       [rows][width], scale [rows] float32
+ * A row that holds a NaN or an infinity has a NaN scale, and codes 0 (EEC_I8) or NaN. */
+EEC_API eec_status eec_quantize_rows(void *stream, int64_t rows, int64_t width, int32_t dtype, int32_t codes,
+                             const void *x, int64_t ldx, void *y, float *scale);
+
 /* eec_linear --
  *   z = x w^T (x_scale_i w_scale_j with 8-bit operands) + bias,
  *   y = act(z) + residual
  *   x [rows][inner], w [outer][inner]: dtype;  bias [outer], residual
  *   [rows][outer]: out_dtype, or NULL
- *   out_dtype  dtype itself; with EEC_E4M3 operands any of the other three
- *   x_scale [rows], w_scale [outer] float32: EEC_E4M3 only, and required there
+ *   out_dtype  dtype itself; with EEC_E4M3 or EEC_I8 operands EEC_F32, EEC_F16 or EEC_BF16
+ *   x_scale [rows], w_scale [outer] float32: EEC_E4M3 and EEC_I8 only, and required there
  *   y       [rows][outer] out_dtype
  *   preact  [rows][outer] z in out_dtype, or NULL (what the backward reads)
  *   workspace >= eec_linear_workspace_bytes(rows, outer, inner, dtype, out_dtype);
@@ -470,7 +483,10 @@ EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t w
  * one's power of two: z may be off by 7 2^-13 (8.5e-4) of sum |x||w| at worst
  * (codes at random: 1.6e-4 at inner = 64, 2e-5 at 4096; normal values 2e-5 and
  * 1.3e-6), which can exceed a 16-bit output's own rounding where the sum
- * cancels.  With a float32 output they are summed in float32. */
+ * cancels.  With a float32 output they are summed in float32.  EEC_I8 products
+ * (codes -128 to 127, inner at most 131071) are summed exactly, in 32-bit integers;
+ * the sum is rounded once to float32 and scaled there (summed in parts over k,
+ * where a few large outputs make that faster, each part is rounded). */
 EEC_API eec_status eec_linear(void *stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
                       int32_t out_dtype, const void *x, int64_t ldx, const float *x_scale, const void *w,
                       int64_t ldw, const float *w_scale, const void *bias, const void *residual, int64_t ldr,
@@ -493,6 +509,39 @@ EEC_API eec_status eec_linear_backward(void *stream, int64_t rows, int64_t outer
                                void *gbias, void *workspace, size_t workspace_bytes);
 EEC_API size_t eec_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
                                            int32_t act);
+
+/* eec_gated_linear -- the gated layer of a feed-forward block:
+ *   z = x w^T (x_scale_i w_scale_j with 8-bit operands) + bias,  its columns
+ *       0 .. outer - 1 the gate, outer .. 2 outer - 1 the value,
+ *   y = act(gate) value
+ *   x [rows][inner], w [2 outer][inner] (the gate's rows first): dtype
+ *   bias    [2 outer] out_dtype, or NULL
+ *   x_scale [rows], w_scale [2 outer] float32: 8-bit operands only, and required there
+ *   y       [rows][outer] out_dtype
+ *   preact  [rows][2 outer] z in out_dtype, or NULL (what the backward reads)
+ *   workspace >= eec_gated_linear_workspace_bytes(rows, outer, inner, dtype, out_dtype)
+ * Types, activations, sums and limits as eec_linear's, for 2 outer columns; y is
+ * computed from z before its rounding. */
+EEC_API eec_status eec_gated_linear(void *stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                            int32_t out_dtype, const void *x, int64_t ldx, const float *x_scale,
+                            const void *w, int64_t ldw, const float *w_scale, const void *bias, int32_t act,
+                            void *y, void *preact, void *workspace, size_t workspace_bytes);
+EEC_API size_t eec_gated_linear_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
+                                        int32_t out_dtype);
+
+/* eec_gated_linear_backward -- with gz = (gy value act'(gate), gy act(gate)), [rows][2 outer],
+ * rounded once to dtype for the products:
+ *   gx [rows][inner] = gz w,  gw [2 outer][inner] = gz^T x,  gbias [2 outer] = sum_rows gz
+ * (dtype each, any may be NULL).
+ *   dtype   EEC_F32, EEC_F16 or EEC_BF16
+ *   preact  [rows][2 outer] as the forward wrote it: rounded to dtype, which in 16
+ *           bits comes on top of the roundings of gz and of the outputs
+ *   workspace >= eec_gated_linear_backward_workspace_bytes(rows, outer, inner, dtype) */
+EEC_API eec_status eec_gated_linear_backward(void *stream, int64_t rows, int64_t outer, int64_t inner,
+                                     int32_t dtype, int32_t act, const void *gy, int64_t ldgy, const void *x,
+                                     int64_t ldx, const void *w, int64_t ldw, const void *preact, void *gx,
+                                     void *gw, void *gbias, void *workspace, size_t workspace_bytes);
+EEC_API size_t eec_gated_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
 
 /* Thread-local text of the last error on this thread ("" if none). */
 EEC_API const char *eec_last_error(void);

@@ -2,17 +2,21 @@
 
     norm    s = x + residual,  rstd = (mean_j s_j^2 + eps)^(-1/2),  y = s rstd w
     linear  z = x w^T + bias,  y = act(z) + residual
+    gated   (gate, value) = z = x w^T + bias, half of the columns each,  y = act(gate) value
+    rows in 8 bits   scale = max(max_j |x_j|, 2^-100) / most,  q = round(x / scale)
 
 and, with gy the gradient of y,
 
     norm    a = gy w,  xhat = s rstd,  gx = rstd (a - xhat mean_j(a xhat)) + gsum,
             gw = sum_rows gy xhat
     linear  gz = gy act'(z),  gx = gz w,  gw = gz^T x,  gbias = sum_rows gz
+    gated   gz = (gy value act'(gate), gy act(gate)),  gx, gw and gbias as above
 """
 import numpy as np
 from scipy.special import erf
 
 E4M3_MAX = 448.0
+I8_MAX = 127.0
 AMAX_FLOOR = 2.0 ** -100
 
 
@@ -70,3 +74,29 @@ def linear(x, w, bias=None, act_name="none", residual=None):
 def linear_backward(gy, x, w, z, act_name="none"):
     gz = gy if act_name == "none" else gy * act_slope(z, act_name)
     return dict(gz=gz, gx=gz @ w, gw=gz.T @ x, gbias=gz.sum(axis=0))
+
+
+def gated(x, w, bias=None, act_name="silu"):
+    z = x @ w.T
+    if bias is not None:
+        z = z + bias
+    n = z.shape[1] // 2
+    return dict(preact=z, y=act(z[:, :n], act_name) * z[:, n:])
+
+
+def gated_gz(gy, z, act_name="silu"):
+    n = z.shape[1] // 2
+    gate, value = z[:, :n], z[:, n:]
+    return np.concatenate([gy * value * act_slope(gate, act_name), gy * act(gate, act_name)], axis=1)
+
+
+def gated_backward(gy, x, w, z, act_name="silu"):
+    gz = gated_gz(gy, z, act_name)
+    return dict(gz=gz, gx=gz @ w, gw=gz.T @ x, gbias=gz.sum(axis=0))
+
+
+def quantize_i8(x):
+    """Codes and float32 scales of float32 rows: quotients rounded to float32 as scales are, then to the nearest integer."""
+    x = x.astype(np.float32)
+    scale = np.maximum(np.abs(x).max(axis=1), np.float32(AMAX_FLOOR)) / np.float32(I8_MAX)
+    return np.rint(x / scale[:, None]).astype(np.int8), scale

@@ -1,0 +1,236 @@
+"""The gated layer (eec_gated_linear and its backward) against the float64 oracle, element by element.
+
+Bounds, from the roundings (U = half a step of the type, EPS = 2^-24 that of float32), as in test_gpu_dense:
+  z         (2 inner + 32) EPS S with S = sum_k |x||w| + |bias|, and U |z| where it is kept;
+  y         a = act(gate) carries 1.13 of gate's error and 16 EPS (|gate| + |a|); the product |a| ez + |value| ea + ea ez
+            and its own EPS, and U |y|;
+  backward  gz carries U |gz|, 18 EPS |gy value| (1 + |gate|) in the gate's half (the slope's 16 and two products) and
+            18 EPS |gy| (|gate| + |a|) in the value's, propagated through the products' sums.
+Values below the type's normal range are within half of its smallest step.
+"""
+import numpy as np
+import pytest
+import torch
+
+from equivariant_edge_convolution_amd import binding as B
+from oracle import dense as D
+
+from gpu_util import DEV, np_, say
+from test_gpu_dense import EPS, TINY, TYPES, U, f64, ids, rand, view, within
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [  # rows, inner, outer
+    (1, 1, 1), (1, 64, 64), (3, 0, 5), (0, 16, 8), (17, 33, 65), (128, 128, 128), (129, 257, 130), (300, 1029, 7),
+    (5, 2050, 300), (1000, 64, 256), (16, 512, 48), (33, 4096, 264), (64, 96, 1000), (257, 320, 513), (2, 8, 4096),
+    (512, 1024, 512), (1, 5000, 3), (31, 40, 31), (40, 40, 33)]
+USES = (("silu", True, 0, 0), ("none", False, 0, 0), ("gelu", True, 3, 1), ("relu", False, 8, 8))
+
+
+def within_range(got, ref, bound, what):
+    """within, where values past the type's largest (a product of two halves in float16) have to be infinities; those
+    that the bound leaves on either side may be either."""
+    most, got = torch.finfo(got.dtype).max, f64(got)
+    past = np.abs(ref) - bound > most * (1 + 2.0 ** -11)
+    assert np.array_equal(got[past], np.sign(ref[past]) * np.inf), what
+    inside = np.abs(ref) + bound <= most
+    within(np.where(inside, got, 0.0), np.where(inside, ref, 0.0), bound, what)
+
+
+def check_forward(x, w, bias, act, out, dt, ez):
+    X, W = f64(x), f64(w)
+    ref = D.gated(X, W, None if bias is None else f64(bias), act)
+    n = W.shape[0] // 2
+    z, y = ref["preact"], ref["y"]
+    gate, value, eg, ev = z[:, :n], z[:, n:], ez[:, :n], ez[:, n:]
+    a = np.abs(D.act(gate, act))
+    ea = 1.13 * eg + 16 * EPS * (np.abs(gate) + a)
+    if "preact" in out:
+        within_range(out["preact"], z, ez + U[out["y"].dtype] * np.abs(z) + TINY[out["y"].dtype], f"{act} preact")
+    within_range(out["y"], y, a * ev + np.abs(value) * ea + ea * ev + (EPS + U[out["y"].dtype]) * np.abs(y) + TINY[out["y"].dtype],
+           f"{act} y")
+
+
+def error_of_z(x, w, bias):
+    X, W = f64(x), f64(w)
+    return (2 * X.shape[1] + 32) * EPS * (np.abs(X) @ np.abs(W).T + (0 if bias is None else np.abs(f64(bias))))
+
+
+def check_backward(gy, x, w, preact, act, b, dt):
+    X, W, G, z = f64(x), f64(w), f64(gy), f64(preact)
+    rows, n = G.shape
+    ref = D.gated_backward(G, X, W, z, act)
+    gate, value = z[:, :n], z[:, n:]
+    ez = np.concatenate([18 * EPS * np.abs(G * value) * (1 + np.abs(gate)),
+                         18 * EPS * np.abs(G) * (np.abs(gate) + np.abs(D.act(gate, act)))], axis=1) + TINY[dt]
+    az = np.abs(ref["gz"]) + ez
+    bias = ez.sum(axis=0) + (2 * rows + 32) * EPS * az.sum(axis=0)
+    ez = ez + U[dt] * np.abs(ref["gz"])
+    within(b["gx"], ref["gx"], ez @ np.abs(W) + (4 * n + 32) * EPS * (az @ np.abs(W)) + U[dt] * np.abs(ref["gx"]) + TINY[dt],
+           f"{act} gx")
+    within(b["gw"], ref["gw"], ez.T @ np.abs(X) + (2 * rows + 32) * EPS * (az.T @ np.abs(X)) + U[dt] * np.abs(ref["gw"]) +
+           TINY[dt], f"{act} gw")
+    if b["gbias"] is not None:
+        within(b["gbias"], ref["gbias"], bias + U[dt] * np.abs(ref["gbias"]) + TINY[dt], f"{act} gbias")
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", SHAPES)
+def test_gated_and_backward(rows, inner, outer, dt):
+    say(f"[gated] {rows}x{inner}x{outer} {dt}")
+    g = torch.Generator().manual_seed(rows * 7919 + inner * 13 + outer)
+    for act, has_b, pad, shift in USES:
+        x = view(rand(g, rows, inner, dtype=dt), pad, shift)
+        w = view(rand(g, 2 * outer, inner, dtype=dt, scale=max(inner, 1) ** -0.5), pad, shift)
+        bias = rand(g, 2 * outer, dtype=dt) if has_b else None
+        out = B.gated_linear(x, w, bias, act, save_preact=True)
+        check_forward(x, w, bias, act, out, dt, error_of_z(x, w, bias))
+        # the same without keeping z
+        assert torch.equal(B.gated_linear(x, w, bias, act)["y"], out["y"])
+        gy = view(rand(g, rows, outer, dtype=dt), pad, shift)
+        check_backward(gy, x, w, out["preact"], act, B.gated_linear_backward(gy, x, w, out["preact"], act, bias=has_b), dt)
+
+
+# rows, inner, outer: whole tiles of every size, tiles that the last outputs fill in part, split sums, packed operands
+LARGE = [(2048, 512, 1024), (4096, 256, 1408), (1000, 2048, 96), (600, 4096, 160), (1531, 1029, 1387), (1301, 1301, 651),
+         (4100, 136, 132), (8211, 256, 68), (2000, 520, 501), (513, 640, 3000)]
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", LARGE)
+def test_gated_large(rows, inner, outer, dt):
+    """The same at sizes that take the tiled, packed and split paths; gradients of every operand."""
+    say(f"[gated] large {rows}x{inner}x{outer} {dt}")
+    g = torch.Generator().manual_seed(rows + inner + outer)
+    x = rand(g, rows, inner, dtype=dt)
+    w = rand(g, 2 * outer, inner, dtype=dt, scale=inner ** -0.5)
+    bias, gy = rand(g, 2 * outer, dtype=dt), rand(g, rows, outer, dtype=dt)
+    out = B.gated_linear(x, w, bias, "silu", save_preact=True)
+    check_forward(x, w, bias, "silu", out, dt, error_of_z(x, w, bias))
+    check_backward(gy, x, w, out["preact"], "silu", B.gated_linear_backward(gy, x, w, out["preact"], "silu"), dt)
+
+
+def test_float32_keeps_float32():
+    """float32 products are as exact as float32 arithmetic in norm, whichever path takes them (packed planes or not)."""
+    for rows, inner, outer in ((1301, 1301, 651), (2048, 512, 1024), (100, 700, 90)):
+        g = torch.Generator().manual_seed(rows)
+        x, w = rand(g, rows, inner), rand(g, 2 * outer, inner, scale=inner ** -0.5)
+        z = f64(B.gated_linear(x, w, None, "none", save_preact=True)["preact"])
+        ref = f64(x) @ f64(w).T
+        assert np.linalg.norm(z - ref) <= EPS * ((6 * inner / 64) ** 0.5 + 2) * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("rows", [3, 200, 700])
+def test_special_values(rows, dt):
+    """A NaN or an infinity reaches its own row (of x) or output (of w), by the formula."""
+    inner, outer = 64, 256
+    x = torch.full((rows, inner), 0.5, dtype=dt, device=DEV)
+    w = torch.full((2 * outer, inner), 0.125, dtype=dt, device=DEV)  # z = 4
+    x[1, 5] = float("nan")
+    w[7, 3] = float("nan")            # a gate
+    w[outer + 9, 0] = float("inf")    # a value
+    w[20] = -64.0                     # a gate of -2048: silu 0
+    y = f64(B.gated_linear(x, w, None, "silu")["y"])
+    rest = np.delete(np.arange(rows), 1)
+    assert np.all(np.isnan(y[1])) and np.all(np.isnan(y[:, 7])) and np.all(np.isposinf(y[rest, 9])) and np.all(y[rest, 20] == 0.0)
+    others = np.delete(np.arange(outer), (7, 9, 20))
+    np.testing.assert_allclose(y[np.ix_(rest, others)], 16.0 / (1.0 + np.exp(-4.0)), rtol=U[dt] + 32 * EPS)
+
+
+EIGHT = [(1, 64, 48), (5, 2050, 300), (17, 33, 65), (129, 257, 130), (300, 1029, 7), (512, 1024, 512), (2048, 512, 1024),
+         (1501, 1505, 751), (600, 4096, 160), (33, 4096, 264)]
+
+
+@pytest.mark.parametrize("out_dt", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", EIGHT)
+def test_gated_integers(rows, inner, outer, out_dt):
+    """8-bit integer operands: exact sums, each rounded to float32 (in parts over k at most 32 times), times two scales."""
+    g = torch.Generator().manual_seed(rows * 31 + inner)
+    codes = lambda *s: torch.randint(-128, 128, s, generator=g, dtype=torch.int8).to(DEV)
+    x, w = view(codes(rows, inner), 5, 2), codes(2 * outer, inner)
+    xs, ws = (0.01 + torch.rand(rows, generator=g)).to(DEV), (0.01 + torch.rand(2 * outer, generator=g)).to(DEV) / inner
+    bias = rand(g, 2 * outer, dtype=out_dt)
+    out = B.gated_linear(x, w, bias, "gelu", xs, ws, out_dt, save_preact=True)
+    S = np.outer(f64(xs), f64(ws)) * (np.abs(f64(x)) @ np.abs(f64(w)).T) + np.abs(f64(bias))
+    check_forward(f64_rows(x, xs), f64_rows(w, ws), bias, "gelu", out, out_dt, 64 * EPS * S)
+    y = B.gated_linear(x, w, None, "none", torch.ones_like(xs), torch.ones_like(ws), torch.float32, save_preact=True)
+    z = f64(x) @ f64(w).T
+    assert np.abs(z).max() < 2 ** 24  # every sum is a float32 number, and so is every part of one
+    assert np.array_equal(f64(y["preact"]), z)
+
+
+def f64_rows(codes, scale):
+    return codes.cpu().to(torch.float64) * scale.cpu().to(torch.float64)[:, None]
+
+
+@pytest.mark.parametrize("out_dt", TYPES, ids=ids)
+@pytest.mark.parametrize("rows,inner,outer", EIGHT)
+def test_gated_e4m3(rows, inner, outer, out_dt):
+    """e4m3 operands; 16-bit outputs from the 8-bit matrix instructions, whose sums are off by 2^-10 of sum |x||w| at worst."""
+    g = torch.Generator().manual_seed(rows * 17 + inner)
+    q = lambda *s: torch.randn(*s, generator=g).to(torch.float8_e4m3fn).to(DEV)
+    x, w = view(q(rows, inner), 5, 2), q(2 * outer, inner)
+    xs, ws = (0.5 + torch.rand(rows, generator=g)).to(DEV), (0.5 + torch.rand(2 * outer, generator=g)).to(DEV) / inner ** 0.5
+    out = B.gated_linear(x, w, None, "silu", xs, ws, out_dt, save_preact=True)
+    X, W = f64_rows(x.float(), xs), f64_rows(w.float(), ws)
+    S = X.abs().numpy() @ W.abs().numpy().T
+    cut = (2 * inner + 32) * EPS + (2.0 ** -10 if out_dt != torch.float32 else 0.0)
+    check_forward(X, W, None, "silu", out, out_dt, cut * S)
+
+
+def test_default_output_of_8_bits_is_bfloat16():
+    x, w = torch.ones((4, 16), dtype=torch.int8, device=DEV), torch.ones((6, 16), dtype=torch.int8, device=DEV)
+    one = lambda n: torch.ones(n, device=DEV)
+    y = B.gated_linear(x, w, None, "none", one(4), one(6))["y"]
+    assert y.dtype == torch.bfloat16 and torch.all(y == 256.0)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_gradients_against_differences(dt):
+    """The backward of the forward itself: a change of x, w and bias along the gradient changes the loss as it says.
+
+    Differences of float64 losses of the oracle, at the operands that the kernels read; the products' own bounds allow
+    (2 outer 2 + 32) EPS + 3 U of the sums of magnitudes, here below 40 U of the gradient's norm."""
+    g = torch.Generator().manual_seed(5)
+    rows, inner, outer = 40, 24, 18
+    x, w, bias, gy = (rand(g, *s, dtype=dt, scale=0.7) for s in ((rows, inner), (2 * outer, inner), (2 * outer,), (rows, outer)))
+    pre = B.gated_linear(x, w, bias, "gelu", save_preact=True)["preact"]
+    b = B.gated_linear_backward(gy, x, w, pre, "gelu")
+    X, W, b0, G = f64(x), f64(w), f64(bias), f64(gy)
+    loss = lambda X, W, b0: (D.gated(X, W, b0, "gelu")["y"] * G).sum()
+    h = 1e-6
+    for at, grad in ((0, b["gx"]), (1, b["gw"]), (2, b["gbias"])):
+        d = f64(grad)
+        step = [d if i == at else 0.0 for i in range(3)]
+        slope = (loss(X + h * step[0], W + h * step[1], b0 + h * step[2]) - loss(X - h * step[0], W - h * step[1], b0 - h * step[2])) / (2 * h)
+        assert abs(slope - (d * d).sum()) <= (40 * U[dt] + 1e-6) * (d * d).sum()
+
+
+def test_optional_gradients_and_repeats():
+    """Only what is asked for is written, and twice the same bits."""
+    g = torch.Generator().manual_seed(6)
+    x, w, gy = rand(g, 300, 64), rand(g, 2 * 96, 64), rand(g, 300, 96)
+    pre = B.gated_linear(x, w, None, "silu", save_preact=True)["preact"]
+    a, b = (B.gated_linear_backward(gy, x, w, pre, "silu") for _ in range(2))
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    ws = torch.empty(B.lib().eec_gated_linear_backward_workspace_bytes(300, 96, 64, 0), dtype=torch.uint8, device=DEV)
+    for want in ("gx", "gw", "gbias"):
+        out = {k: torch.full_like(v, 7.0) for k, v in a.items()}
+        at = lambda k: out[k].data_ptr() if k == want else None
+        st = B.lib().eec_gated_linear_backward(B._raw_stream(x.device), 300, 96, 64, 0, 2, gy.data_ptr(), 96, x.data_ptr(), 64,
+                                               w.data_ptr(), 64, pre.data_ptr(), at("gx"), at("gw"), at("gbias"), ws.data_ptr(), ws.numel())
+        assert B.STATUS[st] == "EEC_OK"
+        torch.cuda.synchronize()
+        assert torch.equal(out[want], a[want]) and all(torch.all(out[k] == 7.0) for k in out if k != want)
+
+
+def test_arguments_of_the_binding():
+    x, w = torch.zeros((4, 8), device=DEV), torch.zeros((6, 8), device=DEV)
+    for call in (lambda: B.gated_linear(x, w[:5]), lambda: B.gated_linear(x, w.cpu()), lambda: B.gated_linear(x, w[:, ::2]),
+                 lambda: B.gated_linear(x, w, act="tanh"), lambda: B.gated_linear(x, w, torch.zeros(3, device=DEV)),
+                 lambda: B.gated_linear(x, w.half()), lambda: B.gated_linear(x[0], w),
+                 lambda: B.gated_linear_backward(x[:, :3], x, w, torch.zeros((4, 8), device=DEV)[:, :6]),
+                 lambda: B.gated_linear_backward(x[:, :3], x, w, torch.zeros((4, 3), device=DEV))):
+        with pytest.raises(ValueError):
+            call()
