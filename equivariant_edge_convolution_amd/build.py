@@ -17,6 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libeec.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["neighbors.hip", "radial.hip", "fold.hip", "table.hip", "conv.hip", "norm.hip", "dense.hip", "gated.hip",
+           "orthogonalize.hip",
            "api.hip"]
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 FLAGS = [

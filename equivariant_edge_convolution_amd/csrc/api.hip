@@ -802,4 +802,71 @@ eec_status eec_gated_linear_backward(void* stream, int64_t rows, int64_t outer, 
   return launched("gated_linear_backward");
 }
 
+// Sizes of an update: the longer side's tiles are counted in 32 bits, the shorter one's square has to be held.
+static eec_status check_update(int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 0 || batch > 65535 || rows < 0 || cols < 0 || std::max(rows, cols) > (1 << 20) ||
+      std::min(rows, cols) > (1 << 15))
+    return fail(EEC_ERR_SHAPE, "bad batch, rows or cols");
+  return EEC_OK;
+}
+// The iteration holds X and b A + c A^2 in 16 bits, which end at 16 there: singular values s of X start within
+// [0, 1] and go to s (a + b s^2 + c s^4), so their largest is followed from step to step.
+static eec_status check_coefficients(int32_t steps, const double* c) {
+  if (steps < 1 || steps > 64) return fail(EEC_ERR_SHAPE, "steps must be 1 to 64");
+  if (c == nullptr) return fail(EEC_ERR_NULL, "coefficients is NULL");
+  double most = 1.0;
+  for (int i = 0; i < steps; ++i, c += 3) {
+    if (!(isfinite(c[0]) && isfinite(c[1]) && isfinite(c[2]))) return fail(EEC_ERR_SHAPE, "coefficients must be finite");
+    double grown = 0.0, poly = 0.0;
+    const auto at = [&](double q) {  // q = s^2
+      if (!(q >= 0.0 && q <= most * most)) return;
+      poly = std::max(poly, fabs(q * (c[1] + c[2] * q)));
+      grown = std::max(grown, fabs(sqrt(q) * (c[0] + q * (c[1] + c[2] * q))));
+    };
+    at(most * most);
+    if (c[2] != 0.0) {
+      at(-c[1] / (2.0 * c[2]));  // of the polynomial of A
+      const double d = 9.0 * c[1] * c[1] - 20.0 * c[0] * c[2];
+      if (d >= 0.0) at((-3.0 * c[1] - sqrt(d)) / (10.0 * c[2])), at((-3.0 * c[1] + sqrt(d)) / (10.0 * c[2]));
+    } else if (c[1] != 0.0) {
+      at(-c[0] / (3.0 * c[1]));
+    }
+    most = std::max(grown, 1e-30);
+    if (most > 3.5 || poly > 15.0)
+      return fail(EEC_ERR_SHAPE, "coefficients that take singular values beyond 3.5, or b s^2 + c s^4 beyond 15");
+  }
+  return EEC_OK;
+}
+
+size_t eec_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
+  if (check_update(batch, rows, cols) != EEC_OK || !float_dtype(dtype)) return 0;
+  return ortho_workspace(batch, rows, cols, dtype);
+}
+
+eec_status eec_orthogonalize(void* stream, int64_t batch, int64_t rows, int64_t cols, int32_t dtype, const void* g,
+                             int64_t ldg, int64_t stride, int32_t steps, const double* coefficients, double eps, void* y,
+                             void* workspace, size_t workspace_bytes) {
+  if (!float_dtype(dtype)) return fail(EEC_ERR_SHAPE, "dtype must be f32, f16 or bf16");
+  TRY(check_update(batch, rows, cols));
+  TRY(check_coefficients(steps, coefficients));
+  if (!(isfinite(eps) && eps > 0.0)) return fail(EEC_ERR_SHAPE, "eps must be positive");
+  const int64_t all = batch * rows;
+  const bool none = batch == 0 || rows == 0 || cols == 0;
+  if (!none) {
+    TRY(check_matrix(g, rows, cols, ldg, dtype, "g"));
+    // one matrix after another: strides between them that would make them overlap are refused
+    if (batch > 1 && (stride < (rows - 1) * ldg + cols || stride > (int64_t(1) << 48)))
+      return fail(EEC_ERR_SHAPE, "bad stride of the matrices");
+  }
+  TRY(check_matrix(y, all, cols, cols, dtype, "y"));
+  TRY(check_ws(workspace, workspace_bytes, ortho_workspace(batch, rows, cols, dtype)));
+  const size_t extent = none ? 0 : (size_t)(batch - 1) * (size_t)stride + (size_t)(rows - 1) * (size_t)ldg + (size_t)cols;
+  TRY(check_alias({matrix(y, all, cols, cols, dtype, "y"), span(workspace, workspace_bytes, "workspace")},
+                  {span(g, extent * dtype_bytes(dtype), "g")}));
+  if (none) return ok();
+  const OrthoArgs a{batch, rows, cols, dtype, g, ldg, stride, steps, coefficients, eps, y};
+  launch_ortho((hipStream_t)stream, a, (char*)workspace);
+  return launched("orthogonalize");
+}
+
 }  // extern "C"

@@ -220,6 +220,20 @@ void launch_gated(hipStream_t s, const LinearArgs& a, char* ws);
 size_t gated_bwd_workspace(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
 void launch_gated_bwd(hipStream_t s, const LinearBwdArgs& a, char* ws);
 
+// `batch` updates of one shape, each brought near the nearest matrix with orthonormal rows or columns.
+struct OrthoArgs {
+  int64_t batch, rows, cols;
+  int32_t dtype;
+  const void* g;
+  int64_t ldg, stride;  // elements from row to row, from matrix to matrix
+  int32_t steps;
+  const double* coefficients;  // [steps][3], host
+  double eps;
+  void* y;
+};
+size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, int32_t dtype);
+void launch_ortho(hipStream_t s, const OrthoArgs& a, char* ws);
+
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace eec

@@ -326,6 +326,8 @@ __device__ __forceinline__ void finish_wave_gated(const Epilogue& e, char* lds, 
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
+template <typename P>
+__device__ __forceinline__ void of_batch(P&, Epilogue&) {}  // one product a launch
 template <bool G, typename O, int HIGH, int PER, typename Acc, int GROUPS, int NB>
 __device__ __forceinline__ void finish(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split,
                                        Acc (&acc)[GROUPS][NB]) {
@@ -524,11 +526,14 @@ struct Place {
   int64_t m, n;
   int split;
 };
-template <int BM, int BN>
-__device__ __forceinline__ Place place_of(int64_t M, int64_t N) {
-  const uint32_t tiles_m = (uint32_t)((M + BM - 1) / BM), tiles_n = (uint32_t)((N + BN - 1) / BN);
+__device__ __forceinline__ uint32_t dealt() {
   const uint32_t total = gridDim.x, b = blockIdx.x, xcd = b & 7;
-  const uint32_t all = xcd * (total >> 3) + min(xcd, total & 7) + (b >> 3);
+  return xcd * (total >> 3) + min(xcd, total & 7) + (b >> 3);
+}
+template <int BM, int BN>
+__device__ __forceinline__ Place place_of(const Epilogue& e) {
+  const uint32_t tiles_m = (uint32_t)((e.M + BM - 1) / BM), tiles_n = (uint32_t)((e.N + BN - 1) / BN);
+  const uint32_t all = dealt();
   const uint32_t split = all / (tiles_m * tiles_n), t = all - split * tiles_m * tiles_n;
   const uint32_t first = t / (8 * tiles_n) * 8, in = t - first * tiles_n;
   const uint32_t high = min(8u, tiles_m - first);
@@ -596,7 +601,7 @@ __global__ void __launch_bounds__(256) k_product(Product g, Epilogue e) {
   __shared__ __attribute__((aligned(16))) char lds[TILES > SUMS ? TILES : SUMS];
   char* lds_b = lds + P * SA::PLANE;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Place place = place_of<BM, BN>(e.M, e.N);
+  const Place place = place_of<BM, BN>(e);
   const int64_t m0 = place.m, n0 = place.n;
   const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
@@ -868,9 +873,12 @@ __device__ __forceinline__ void tile_barrier() {
 // six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, 43 with
 // eight).
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
-template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS, bool G = false>
-__global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
+// E: an Epilogue, or another with its own place_of, of_batch and finish.
+template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS, bool G = false,
+          typename E = Epilogue>
+__global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, E e) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the stub alone, and drops some of them where it parses the body
+  of_batch(g, e);
   constexpr int BM = WM * MI * 16, BN = WN * 64, WAVES = WM * WN;
   using TA = Tile<T, A_KC, BM, WAVES>;
   using TB = Tile<T, B_KC, BN, WAVES, G>;
@@ -882,7 +890,7 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, Epilogue e) {
   __shared__ __attribute__((aligned(1024))) char b0[TB::BYTES], b1[TB::BYTES], b2[TB::BYTES], b3[TB::BYTES];
   __shared__ __attribute__((aligned(16))) char a4[A2], a5[A2], a6[A2], a7[A2], b4[B2], b5[B2], b6[B2], b7[B2];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const Place place = place_of<BM, BN>(e.M, e.N);
+  const Place place = place_of<BM, BN>(e);
   const int64_t m0 = place.m, n0 = place.n;
   const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / WN * MI * 16, wn = wave % WN * 64;
@@ -956,7 +964,7 @@ __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
   using TB = Tile<bf16, B_KC, 128, 8, G>;
   __shared__ __attribute__((aligned(1024))) char a0[3 * TA::BYTES], a1[3 * TA::BYTES], b0[3 * TB::BYTES], b1[3 * TB::BYTES];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const Place place = place_of<256, 128>(e.M, e.N);
+  const Place place = place_of<256, 128>(e);
   const int64_t m0 = place.m, n0 = place.n;
   const int64_t kb = place.split * g.k_split, ke = min(g.K, kb + g.k_split);
   const int wm = wave / 2 * 64, wn = wave % 2 * 64;

@@ -543,6 +543,32 @@ EEC_API eec_status eec_gated_linear_backward(void *stream, int64_t rows, int64_t
                                      void *gw, void *gbias, void *workspace, size_t workspace_bytes);
 EEC_API size_t eec_gated_linear_backward_workspace_bytes(int64_t rows, int64_t outer, int64_t inner, int32_t dtype);
 
+/* eec_orthogonalize -- an update brought near the nearest matrix with orthonormal rows or
+ * columns (its singular vectors kept, its singular values taken towards 1) by
+ * Newton-Schulz products, as an optimiser of the layers' weights applies it:
+ *   X = g / (|g| + eps)  (|g| the root of the sum of squares),  then for each step
+ *   A = X X^T,  X <- a X + (b A + c A^2) X
+ * (rows <= cols; otherwise A = X^T X and X <- a X + X (b A + c A^2), the same result).
+ *   g       [batch][rows][cols] dtype: matrices `stride` elements apart (>= their
+ *           extent; unread for batch 1), rows `ldg`
+ *   coefficients [host][steps][3]: a, b, c of each step; read before the call
+ *           returns.  Refused where they take singular values of [0, 1] beyond 3.5 or
+ *           b s^2 + c s^4 beyond 15 on the way
+ *   steps   1 to 64;  eps > 0
+ *   y       [batch][rows][cols] dtype
+ *   batch <= 65535, the longer side <= 2^20, the shorter <= 2^15
+ *   workspace >= eec_orthogonalize_workspace_bytes(batch, rows, cols, dtype)
+ * The norm is summed in float64 (no update is too large or too small for it); X is held
+ * to 22 bits and products are summed in float32.  EEC_F32: products of 22-bit operands, as exact as
+ * float32 arithmetic.  16-bit types: operands of the products rounded to 11 bits, 1e-3
+ * to 2e-3 off in norm before y is rounded.
+ * A NaN or an infinity in g makes all of its matrix NaN; a matrix of zeros stays one. */
+EEC_API eec_status eec_orthogonalize(void *stream, int64_t batch, int64_t rows, int64_t cols, int32_t dtype,
+                             const void *g, int64_t ldg, int64_t stride, int32_t steps,
+                             const double *coefficients /*[host][steps][3]*/, double eps, void *y,
+                             void *workspace, size_t workspace_bytes);
+EEC_API size_t eec_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t dtype);
+
 /* Thread-local text of the last error on this thread ("" if none). */
 EEC_API const char *eec_last_error(void);
 

@@ -3,6 +3,7 @@
     norm    s = x + residual,  rstd = (mean_j s_j^2 + eps)^(-1/2),  y = s rstd w
     linear  z = x w^T + bias,  y = act(z) + residual
     gated   (gate, value) = z = x w^T + bias, half of the columns each,  y = act(gate) value
+    orthogonalised update   X = g / (|g| + eps);  X <- a X + (b A + c A^2) X, A = X X^T, for each (a, b, c)
     rows in 8 bits   scale = max(max_j |x_j|, 2^-100) / most,  q = round(x / scale)
 
 and, with gy the gradient of y,
@@ -100,3 +101,16 @@ def quantize_i8(x):
     x = x.astype(np.float32)
     scale = np.maximum(np.abs(x).max(axis=1), np.float32(AMAX_FLOOR)) / np.float32(I8_MAX)
     return np.rint(x / scale[:, None]).astype(np.int8), scale
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(g, coefficients=(QUINTIC,) * 5, eps=1e-7):
+    x = g / (np.sqrt((g * g).sum()) + eps)
+    if x.shape[0] > x.shape[1]:
+        x = x.T
+    for a, b, c in coefficients:
+        gram = x @ x.T
+        x = a * x + (b * gram + c * (gram @ gram)) @ x
+    return x if g.shape[0] <= g.shape[1] else x.T
