@@ -22,43 +22,57 @@ namespace {
 
 constexpr float SCALE = 4096.f;
 
-struct NewtonEpilogue {
-  int64_t M, N;         // of the product
-  int64_t ld;           // of from and to
-  const f16* from;      // alpha from + beta C, or NULL
-  int64_t from_plane;   // elements to its low part, 0: none
+// Where a product's results go: alpha from + beta C, rounded into two planes or one, or (Y a
+// type) into rows of y.
+struct Planes {};
+struct NewtonTo {
+  const f16* from;     // or NULL
+  int64_t from_plane;  // elements to its low part, 0: none
   f16* to;
-  int64_t to_plane;     // 0: no low part
+  int64_t to_plane;    // 0: no low part
+  int64_t ld;          // of from and to, a multiple of 8
+  int64_t from_batch, to_batch;  // elements to the next matrix
+};
+// SYM: C is symmetric, tiles below the diagonal are not computed.  TURN: C's transpose goes to
+// `turned` as well (SYM: into C's own lower half, without TURN).
+template <typename Y, bool SYM, bool TURN = false>
+struct NewtonEpilogue {
+  int64_t M, N;  // of the product
   float alpha, beta;
-  bool symmetric;
-  int32_t dtype;        // of y
-  void* y;              // [M][N] instead of `to`, or NULL
-  int64_t a_batch, b_batch, from_batch, to_batch, y_batch;  // elements to the next matrix
+  NewtonTo rows, turned;
+  Y* y;  // [M][N] instead of rows.to
+  int64_t y_batch, a_batch, b_batch;
 };
 
-__device__ __forceinline__ void of_batch(Product& g, NewtonEpilogue& e) {
+template <typename Y, bool SYM, bool TURN>
+__device__ __forceinline__ void of_batch(Product& g, NewtonEpilogue<Y, SYM, TURN>& e) {
   const int64_t i = blockIdx.y;
   g.a = (const f16*)g.a + i * e.a_batch;
   g.b = (const f16*)g.b + i * e.b_batch;
-  if (e.from) e.from += i * e.from_batch;
-  if (e.to) e.to += i * e.to_batch;
-  if (e.y) e.y = (char*)e.y + i * e.y_batch * (e.dtype == EEC_F32 ? 4 : 2);
+  const auto next = [&](NewtonTo& s) {
+    if (s.from) s.from += i * s.from_batch;
+    s.to += i * s.to_batch;
+  };
+  next(e.rows);
+  if constexpr (TURN) next(e.turned);
+  if constexpr (!std::is_same<Y, Planes>::value) e.y += i * e.y_batch;
 }
 
 // Symmetric: the tiles that reach above the diagonal, row of tiles after row of tiles.
-template <int BM, int BN>
-__device__ __forceinline__ Place place_of(const NewtonEpilogue& e) {
+template <int BM, int BN, typename Y, bool SYM, bool TURN>
+__device__ __forceinline__ Place place_of(const NewtonEpilogue<Y, SYM, TURN>& e) {
   static_assert(BM % BN == 0, "a row of tiles starts at its diagonal");
-  if (!e.symmetric) {
+  if constexpr (SYM) {
+    const uint32_t tiles_n = (uint32_t)((e.N + BN - 1) / BN);
+    uint32_t t = dealt(), i = 0;
+    for (uint32_t row = tiles_n; t >= row; row = tiles_n - i * (BM / BN)) t -= row, ++i;
+    return Place{(int64_t)i * BM, (int64_t)(i * (BM / BN) + t) * BN, 0};
+  } else {
     Epilogue plain{};
     plain.M = e.M;
     plain.N = e.N;
     return place_of<BM, BN>(plain);
   }
-  const uint32_t tiles_n = (uint32_t)((e.N + BN - 1) / BN);
-  uint32_t t = dealt(), i = 0;
-  for (uint32_t row = tiles_n; t >= row; row = tiles_n - i * (BM / BN)) t -= row, ++i;
-  return Place{(int64_t)i * BM, (int64_t)(i * (BM / BN) + t) * BN, 0};
 }
 template <int BM, int BN>
 int64_t newton_tiles(int64_t M, int64_t N, bool symmetric) {
@@ -69,58 +83,120 @@ int64_t newton_tiles(int64_t M, int64_t N, bool symmetric) {
   return all;
 }
 
-// Eight adjacent columns of one row, `left` of which exist and are stored from column `first` on.
-__device__ __forceinline__ void finish_newton(const NewtonEpilogue& e, int64_t m, int64_t n, int64_t left, int first,
-                                              float (&v)[8]) {
-  float was[8] = {};
-  if (e.from) {
-    const f16* p = e.from + m * e.ld + n;
-    load_run(p, left, was);
-    if (e.from_plane) {
-      float low[8];
-      load_run(p + e.from_plane, left, low);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) was[i] += low[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = e.alpha * was[i] + e.beta * v[i];
-  if (e.y) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= 1.f / SCALE;
-    if (e.dtype == EEC_F32) store_run((float*)e.y + m * e.N + n, left, v);
-    if (e.dtype == EEC_F16) store_run((f16*)e.y + m * e.N + n, left, v);
-    if (e.dtype == EEC_BF16) store_run((bf16*)e.y + m * e.N + n, left, v);
-    return;
-  }
-  f16 hi[8], lo[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = (f16)v[i];
-    lo[i] = (f16)(v[i] - (float)hi[i]);
-  }
-  f16* p = e.to + m * e.ld + n;
-  if (left >= 8 && first <= 0) {
-    __builtin_memcpy(p, hi, 16);
-    if (e.to_plane) __builtin_memcpy(p + e.to_plane, lo, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left && i >= first) {
-        p[i] = hi[i];
-        if (e.to_plane) p[i + e.to_plane] = lo[i];
-      }
-  }
+__device__ __forceinline__ void split2(float v, f16& hi, f16& lo) {
+  hi = (f16)v;
+  lo = (f16)(v - (float)hi);
 }
 
-// As finish_wave.  Symmetric: elements above the diagonal (and on it) are stored, and those above
-// it once more across it, from columns of the same sums: each is written once, by one lane.
-template <bool G, typename O, int HIGH, int PER, typename Acc, int GROUPS, int NB>
-__device__ __forceinline__ void finish(const NewtonEpilogue& e, char* lds, int64_t m0, int64_t n0, int,
-                                       Acc (&acc)[GROUPS][NB]) {
-  constexpr int ROWS = PER * HIGH;
+// Eight adjacent elements of one row, from a multiple of 8 on, of which `left` exist (0: nothing
+// to do).  Planes have rows of whole runs, whose end is kept at zero, so that each run is one store.
+struct Run8 {
+  int64_t m, n, left;
+  f16 hi[8], lo[8];  // what alpha multiplies
+  __device__ __forceinline__ void load(const NewtonTo& s) {
+    if (left <= 0 || s.from == nullptr) return;
+    const f16* p = s.from + m * s.ld + n;
+    __builtin_memcpy(hi, __builtin_assume_aligned(p, 16), 16);
+    if (s.from_plane) __builtin_memcpy(lo, __builtin_assume_aligned(p + s.from_plane, 16), 16);
+  }
+  __device__ __forceinline__ void value(const NewtonTo& s, float alpha, float beta, float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= beta;
+    if (s.from) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += alpha * (s.from_plane ? (float)hi[i] + (float)lo[i] : (float)hi[i]);
+    }
+  }
+  __device__ __forceinline__ void store(const NewtonTo& s, const float (&v)[8]) const {
+    f16 h[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split2(i < left ? v[i] : 0.f, h[i], l[i]);
+    f16* p = s.to + m * s.ld + n;
+    __builtin_memcpy(__builtin_assume_aligned(p, 16), h, 16);
+    if (s.to_plane) __builtin_memcpy(__builtin_assume_aligned(p + s.to_plane, 16), l, 16);
+  }
+};
+
+__device__ __forceinline__ float sum_at(const char* lds, int r, int c) {
+  float v;
+  __builtin_memcpy(&v, lds + (r * 256 + ((c / 4) ^ (r & 15)) * 16 + c % 4 * 4), 4);
+  return v;
+}
+
+// Finishes ROWS x 64 sums of a wave, row by row of 256 bytes in its LDS as put_sums leaves them.
+// Symmetric: 8 x 8 blocks on and above the diagonal are stored, and those above it once more
+// across it, from columns of the same sums; a block on the diagonal takes its lower half from its
+// upper one.  So each element is written once, by one lane, and C is symmetric to the bit.  What
+// four runs a lane need from memory is loaded before any of them is stored.
+template <int ROWS, typename Y, bool SYM, bool TURN>
+__device__ __forceinline__ void finish_sums(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int64_t top, int64_t n0) {
+  constexpr int RUNS = ROWS / 8, TOGETHER = RUNS < 4 ? RUNS : 4;
+  static_assert(RUNS % TOGETHER == 0, "whole batches");
   const int lane = threadIdx.x & 63;
   const int r0 = lane >> 3, col = (lane & 7) * 8;
+#pragma unroll 1
+  for (int j = 0; j < RUNS; j += TOGETHER) {
+    Run8 run[TOGETHER];
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) {
+      run[i].m = top + r0 + (j + i) * 8;
+      run[i].n = n0 + col;
+      run[i].left = run[i].m < e.M && !(SYM && run[i].n + 7 < run[i].m) ? e.N - run[i].n : 0;
+      run[i].load(e.rows);
+    }
+#pragma unroll
+    for (int i = 0; i < TOGETHER; ++i) {
+      if (run[i].left <= 0) continue;
+      const int r = r0 + (j + i) * 8;
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; u += 4)
+        __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (r * 256 + (((col + u) / 4) ^ (r & 15)) * 16), 16), 16);
+      if (SYM && run[i].n < run[i].m) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (run[i].n + u < run[i].m) v[u] = sum_at(lds, (r & ~7) + u, col + (r & 7));
+      }
+      run[i].value(e.rows, e.alpha, e.beta, v);
+      if constexpr (std::is_same<Y, Planes>::value) {
+        run[i].store(e.rows, v);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] *= 1.f / SCALE;
+        store_run(e.y + run[i].m * e.N + run[i].n, run[i].left, v);
+      }
+    }
+  }
+  if constexpr (SYM || TURN) {  // row n0 + lane of the transpose: eight of this side's rows at a time
+    const NewtonTo& to = TURN ? e.turned : e.rows;
+    const int64_t m = n0 + lane;
+#pragma unroll 1
+    for (int j = 0; j < RUNS; j += TOGETHER) {
+      Run8 run[TOGETHER];
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) {
+        run[i].m = m;
+        run[i].n = top + (j + i) * 8;
+        run[i].left = m < e.N && !(SYM && run[i].n + 7 >= m) ? e.M - run[i].n : 0;  // symmetric: blocks above the diagonal
+        run[i].load(to);
+      }
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) {
+        if (run[i].left <= 0) continue;
+        const int r = (j + i) * 8;
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = sum_at(lds, r + u, lane);
+        run[i].value(to, e.alpha, e.beta, v);
+        run[i].store(to, v);
+      }
+    }
+  }
+}
+// As finish_wave.
+template <bool G, typename O, int HIGH, int PER, typename Y, bool SYM, bool TURN, typename Acc, int GROUPS, int NB>
+__device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, char* lds, int64_t m0, int64_t n0, int,
+                                       Acc (&acc)[GROUPS][NB]) {
 #pragma unroll 1
   for (int g = 0; g < GROUPS; g += PER) {
 #pragma unroll
@@ -130,34 +206,7 @@ __device__ __forceinline__ void finish(const NewtonEpilogue& e, char* lds, int64
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = i + PER < GROUPS ? acc[i + PER < GROUPS ? i + PER : 0][j] : Acc{};
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int64_t top = m0 + g * HIGH;
-#pragma unroll 1
-    for (int r = r0; r < ROWS; r += 8) {
-      const int64_t m = top + r, n = n0 + col;
-      const int64_t first = e.symmetric ? m - n : 0;
-      if (m < e.M && n < e.N && first < 8) {
-        float v[8];
-#pragma unroll
-        for (int u = 0; u < 8; u += 4)
-          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (r * 256 + (((col + u) / 4) ^ (r & 15)) * 16), 16), 16);
-        finish_newton(e, m, n, e.N - n, (int)max(first, (int64_t)0), v);
-      }
-    }
-    if (e.symmetric) {  // row n0 + lane of the other side: eight of this side's rows at a time
-      const int64_t m = n0 + lane;
-#pragma unroll 1
-      for (int r = 0; r < ROWS; r += 8) {
-        const int64_t n = top + r;
-        const int64_t left = min(m, e.N) - n;  // those above the diagonal
-        if (m < e.N && left > 0) {
-          float v[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            __builtin_memcpy(&v[u], lds + ((r + u) * 256 + ((lane / 4) ^ (r + u & 15)) * 16 + lane % 4 * 4), 4);
-          finish_newton(e, m, n, left, 0, v);
-        }
-      }
-    }
+    finish_sums<PER * HIGH>(e, lds, m0 + g * HIGH, n0);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
@@ -165,8 +214,8 @@ __device__ __forceinline__ void finish(const NewtonEpilogue& e, char* lds, int64
 // Products of two planes each, 256 x 128 of C per workgroup and 64 x 64 per wave, as k_parted:
 // a step is 32 k of all four planes, 48 KB of LDS, and does lo hi, hi lo and hi hi; three
 // buffers, so that two steps' loads run under the present one's 48 products a wave.
-template <bool A_KC, bool B_KC>
-__global__ void __launch_bounds__(512) k_pairs(Product g, NewtonEpilogue e) {
+template <bool A_KC, bool B_KC, typename E>
+__global__ void __launch_bounds__(512) k_pairs(Product g, E e) {
 #ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
   of_batch(g, e);
   using TA = Tile<f16, A_KC, 256, 8>;
@@ -232,6 +281,253 @@ __global__ void __launch_bounds__(512) k_pairs(Product g, NewtonEpilogue e) {
 #endif
 }
 
+// ------------------------------------------------------------------ small tiles
+
+// 64 x 64 of C per workgroup of four waves, P planes, both operands with k along memory: for
+// products whose large tiles would leave most CUs idle.  A workgroup gets 64 KB of operands every
+// microsecond or so whatever it does, so seven steps of 32 k are on their way at a time.
+template <int P, typename E>
+__global__ void __launch_bounds__(256) k_small(Product g, E e) {
+#ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
+  of_batch(g, e);
+  using T = Tile<f16, true, 64, 4>;
+  constexpr int LOADS = 2 * P * T::LOADS, B = P * T::BYTES;
+  __shared__ __attribute__((aligned(1024))) char a0[2 * B], a1[2 * B], a2[2 * B], a3[2 * B], a4[2 * B], a5[2 * B], a6[2 * B], a7[2 * B];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const Place place = place_of<64, 64>(e);
+  const int64_t m0 = place.m, n0 = place.n;
+  const int wm = wave / 2 * 32, wn = wave % 2 * 32;
+  f32x4 acc[2][2] = {};
+  T ta, tb;
+  ta.init(g.a, g.lda, m0, g.M, 0);
+  tb.init(g.b, g.ldb, n0, g.N, 0);
+  auto load = [&](char* to, int left) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      ta.load_from(to + p * T::BYTES, ta.base + p * g.a_plane, left);
+      tb.load_from(to + B + p * T::BYTES, tb.base + p * g.b_plane, left);
+    }
+    ta.base += ta.step;
+    tb.base += tb.step;
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step = [&](const char* la) {
+    f16x8 a[2][P], b[2][P];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        T::fragment(a[i][p], la + p * T::BYTES, wm, i);
+        T::fragment(b[i][p], la + B + p * T::BYTES, wn, i);
+      }
+    // in rising size: (lo, hi), (hi, lo), (hi, hi)
+#pragma unroll
+    for (int t = P == 2 ? 0 : 2; t < 3; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j][t == 1 ? P - 1 : 0], a[i][t == 0 ? P - 1 : 0], acc[i][j], 0, 0, 0);
+  };
+  int left = (int)g.K;
+  load(a0, left);
+  load(a1, left - 32);
+  load(a2, left - 64);
+  load(a3, left - 96);
+  load(a4, left - 128);
+  load(a5, left - 160);
+  load(a6, left - 192);
+#define EEC_STEP(T, NOW, FREE)   \
+  tile_barrier<6 * LOADS>();     \
+  load(FREE, left - (T + 7) * 32); \
+  step(NOW);                     \
+  if (left <= (T + 1) * 32) break
+  for (;; left -= 256) {
+    EEC_STEP(0, a0, a7);
+    EEC_STEP(1, a1, a0);
+    EEC_STEP(2, a2, a1);
+    EEC_STEP(3, a3, a2);
+    EEC_STEP(4, a4, a3);
+    EEC_STEP(5, a5, a4);
+    EEC_STEP(6, a6, a5);
+    EEC_STEP(7, a7, a6);
+  }
+#undef EEC_STEP
+  tile_barrier<0>();
+  // the workgroup's sums: rows 0 to 31 and 32 to 63 in 8 KB each
+  char* high = wave < 2 ? a0 : a1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) put_sums(high, 16 * i + (lane & 15), wn / 4 + 4 * j + (lane >> 4), acc[i][j]);
+  __syncthreads();
+  finish_sums<16>(e, high + wave % 2 * 4096, m0 + wave * 16, n0);
+#endif
+}
+
+// ------------------------------------------------------------------ whole updates in one workgroup
+
+// An update whose planes fit the LDS of one CU: every step of it in one launch of a workgroup of
+// 16 waves a matrix (4 of 256 x 64 float32, five steps: %%ONE%%).  X lies there by rows of
+// the shorter side, two planes of `high` rows (a multiple of 32; those past the end are zeros, and
+// so are columns past the end), and one square that holds A, then B.  Two planes in every product.
+constexpr int ONE_BYTES = 158 * 1024;
+struct NewtonOne {
+  const void* g;
+  int64_t ldg, stride;
+  int rows, cols, side, length;  // side <= length: rows and cols, in one order or the other
+  int high, xs, as;              // rows of X and of the square; elements from row to row of each
+  int steps;
+  double eps;
+  void* y;
+  float c[64][3];
+};
+template <typename T>
+__global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __attribute__((aligned(16))) char lds[ONE_BYTES];
+  __shared__ double join[16];
+  const int lane = threadIdx.x & 63, wave = wave_id(), line = lane & 15, q = lane >> 4;
+  f16* x = (f16*)lds;
+  const int x_plane = s.high * s.xs, a_plane = s.high * s.as;
+  f16* a = x + 2 * x_plane;
+  const T* g = (const T*)s.g + blockIdx.x * s.stride;
+  T* y = (T*)s.y + (int64_t)blockIdx.x * s.rows * s.cols;
+  const bool wide = s.rows <= s.cols;
+  const int total = s.rows * s.cols;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < total; i += 1024) {
+    const double v = (float)g[(int64_t)(i / s.cols) * s.ldg + i % s.cols];
+    sum += v * v;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) join[wave] = sum;
+  for (int i = threadIdx.x; i < (x_plane + a_plane) / 4; i += 1024) ((i32x4*)lds)[i] = i32x4{};  // 2 planes, 8 a store
+  __syncthreads();
+  sum = 0.0;
+  for (int i = 0; i < 16; ++i) sum += join[i];
+  const double scale = (double)SCALE / (sqrt(sum) + s.eps);
+  for (int i = threadIdx.x; i < total; i += 1024) {
+    const int r = i / s.cols, c = i % s.cols, at = wide ? r * s.xs + c : c * s.xs + r;
+    split2((float)((float)g[(int64_t)r * s.ldg + c] * scale), x[at], x[at + x_plane]);
+  }
+  __syncthreads();
+  const int tiles = (s.side + 15) / 16, strips = (s.length + 15) / 16, ks = s.high / 32;
+  const auto row8 = [](const f16* p) {
+    f16x8 v;
+    __builtin_memcpy(&v, __builtin_assume_aligned(p, 16), 16);
+    return v;
+  };
+  const auto product = [](const f16x8 (&n)[2], const f16x8 (&m)[2], f32x4 acc) {  // columns first: a lane has 4 of a row
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(n[0], m[1], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(n[1], m[0], acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(n[0], m[0], acc, 0, 0, 0);
+  };
+  // 16 rows from row 16 i and 16 from 16 j of a matrix, multiplied over n x 32 columns
+  const auto gram = [&](const f16* p, int plane, int ld, int i, int j, int n) {
+    f32x4 acc = {};
+    const f16 *pi = p + (16 * i + line) * ld + q * 8, *pj = p + (16 * j + line) * ld + q * 8;
+    for (int k = 0; k < n; ++k, pi += 32, pj += 32) {
+      const f16x8 m[2] = {row8(pi), row8(pi + plane)}, c[2] = {row8(pj), row8(pj + plane)};
+      acc = product(c, m, acc);
+    }
+    return acc;
+  };
+  // row 16 i + line, columns 16 j + 4 q and three more of a symmetric matrix: those on and above the diagonal, on both sides
+  const auto put = [&](int i, int j, const f32x4& v) {
+    const int r = 16 * i + line;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = 16 * j + 4 * q + u;
+      f16 hi, lo;
+      split2(v[u], hi, lo);
+      if (c >= r) {
+        a[r * s.as + c] = a[c * s.as + r] = hi;
+        a[r * s.as + c + a_plane] = a[c * s.as + r + a_plane] = lo;
+      }
+    }
+  };
+  // the n-th tile on or above the diagonal
+  const auto tile_at = [&](int n, int& i, int& j) {
+    for (i = 0; n >= tiles - i; ++i) n -= tiles - i;
+    j = i + n;
+  };
+  const int pairs = tiles * (tiles + 1) / 2, length32 = (s.length + 31) / 32;
+  for (int step = 0; step < s.steps; ++step) {
+    const float ca = s.c[step][0], cb = s.c[step][1], cc = s.c[step][2] / SCALE;
+    int i, j;
+    for (int n = wave; n < pairs; n += 16) {  // A
+      tile_at(n, i, j);
+      put(i, j, gram(x, x_plane, s.xs, i, j, length32) * (1.f / SCALE));
+    }
+    __syncthreads();
+    f32x4 b[3];  // B, in A's place when everybody has read A: up to 36 tiles
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const int n = wave + 16 * t;
+      if (n >= pairs) continue;
+      tile_at(n, i, j);
+      b[t] = gram(a, a_plane, s.as, i, j, ks) * cc;
+      const f16* p = a + (16 * i + line) * s.as + 16 * j + 4 * q;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) b[t][u] += cb * ((float)p[u] + (float)p[u + a_plane]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const int n = wave + 16 * t;
+      if (n >= pairs) continue;
+      tile_at(n, i, j);
+      put(i, j, b[t]);
+    }
+    __syncthreads();
+    // X: 16 columns of it depend on these alone, so a wave replaces them as soon as it has them
+    for (int n = wave; n < strips; n += 16) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      f32x4 acc[8] = {};
+      for (int k = 0; k < ks; ++k) {
+        f16x8 c[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          s16x4 h[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(x + p * x_plane + (k * 32 + q * 8 + (lane >> 2 & 3) + 4 * u) * s.xs + n * 16 +
+                                                           (lane & 3) * 4));
+          __builtin_memcpy(&c[p], h, 16);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (t >= tiles) break;
+          const f16* p = a + (16 * t + line) * s.as + k * 32 + q * 8;
+          const f16x8 m[2] = {row8(p), row8(p + a_plane)};
+          acc[t] = product(c, m, acc[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (t >= tiles) break;
+        const int r = 16 * t + line, c = n * 16 + 4 * q;
+        f16* p = x + r * s.xs + c;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float v = ca * ((float)p[u] + (float)p[u + x_plane]) + acc[t][u] * (1.f / SCALE);
+          if (r < s.side && c + u < s.length) {
+            if (step + 1 < s.steps)
+              split2(v, p[u], p[u + x_plane]);
+            else
+              y[wide ? (int64_t)r * s.cols + c + u : (int64_t)(c + u) * s.cols + r] = (T)(v * (1.f / SCALE));
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+#endif
+}
+
 // ------------------------------------------------------------------ norm and scaled planes
 
 constexpr int SUMS = 256;  // partial sums of one matrix
@@ -264,13 +560,12 @@ struct Scaling {
   const double* part;
   int groups;  // of partial sums
   double eps;
-  f16 *x, *other;             // X, and the buffer of the next step's
+  f16* x;
   int64_t ldx, plane, batch;  // elements from row to row, to the low part, to the next matrix
-  f16 *a, *b;                 // A and B
-  int64_t side, lds, ab_plane, ab_batch;  // ab_plane 0: one plane
+  f16* turned;                // X's transpose, or NULL
+  int64_t ldt, turned_plane, turned_batch;
 };
-// X = SCALE g / (|g| + eps) as two planes; the columns that pad its rows are zeros, here and in
-// the next step's buffer, and so are those that pad A and B to whole loads.
+// X = SCALE g / (|g| + eps) as two planes, whose rows are padded with zeros to whole runs of 8.
 template <typename T>
 __global__ void __launch_bounds__(256) k_scaled(Scaling s) {
   __shared__ double join[4];
@@ -282,135 +577,233 @@ __global__ void __launch_bounds__(256) k_scaled(Scaling s) {
   __syncthreads();
   const double scale = (double)SCALE / (sqrt((join[0] + join[1]) + (join[2] + join[3])) + s.eps);
   const T* g = (const T*)s.g + batch * s.stride;
-  f16 *x = s.x + batch * s.batch, *other = s.other + batch * s.batch;
-  const int64_t per_row = s.ldx / 8, total = s.rows * per_row, all = (int64_t)gridDim.x * 256;
-  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  for (int64_t i = first; i < total; i += all) {
+  f16 *x = s.x + batch * s.batch, *turned = s.turned + batch * s.turned_batch;
+  const int64_t per_row = s.ldx / 8, high = s.turned ? s.ldt : s.rows;  // the transpose's padding are rows past the end
+  const int64_t total = high * per_row, all = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += all) {
     const int64_t r = i / per_row, c = i % per_row * 8, at = r * s.ldx + c;
     float v[8];
-    load_run<true>(g + r * s.ldg + c, s.cols - c, v);
+    load_run<true>(g + r * s.ldg + c, r < s.rows ? s.cols - c : 0, v);
     f16 hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float u = (float)(v[j] * scale);
-      hi[j] = c + j < s.cols ? (f16)u : (f16)0.f;  // an infinite scale makes no NaN of the padding
-      lo[j] = c + j < s.cols ? (f16)(u - (float)hi[j]) : (f16)0.f;
+    for (int j = 0; j < 8; ++j)  // an infinite scale makes no NaN of the padding
+      split2(r < s.rows && c + j < s.cols ? (float)(v[j] * scale) : 0.f, hi[j], lo[j]);
+    if (r < s.rows) {
+      __builtin_memcpy(__builtin_assume_aligned(x + at, 16), hi, 16);
+      __builtin_memcpy(__builtin_assume_aligned(x + at + s.plane, 16), lo, 16);
     }
-    __builtin_memcpy(__builtin_assume_aligned(x + at, 16), hi, 16);
-    __builtin_memcpy(__builtin_assume_aligned(x + at + s.plane, 16), lo, 16);
-    if (c + 8 > s.cols) {  // real columns are written by the first step
-      const f16 none[8] = {};
-      __builtin_memcpy(__builtin_assume_aligned(other + at, 16), none, 16);
-      __builtin_memcpy(__builtin_assume_aligned(other + at + s.plane, 16), none, 16);
+    if (s.turned) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < s.cols) {
+          turned[(c + j) * s.ldt + r] = hi[j];
+          turned[(c + j) * s.ldt + r + s.turned_plane] = lo[j];
+        }
     }
   }
-  f16 *pa = s.a + batch * s.ab_batch, *pb = s.b + batch * s.ab_batch;
-  for (int64_t r = first; r < s.side; r += all)
-    for (int64_t c = s.side; c < up(s.side, 8); ++c) {
-      pa[r * s.lds + c] = pb[r * s.lds + c] = (f16)0.f;
-      if (s.ab_plane) pa[r * s.lds + c + s.ab_plane] = pb[r * s.lds + c + s.ab_plane] = (f16)0.f;
-    }
 }
 
 // ------------------------------------------------------------------ host
 
-// Workspace of one call: partial sums, X and the next X (two planes each), A and B.
+// How a call is run, and its workspace: partial sums, X and the next X (two planes each; with
+// small tiles their transposes too), A and B.
+enum Way { ONE, SMALL_TILES, LARGE_TILES };
 struct OrthoPlan {
+  Way way;
   bool wide;
-  int64_t side, ldx, lds, x_plane, ab_plane;  // elements
-  int planes;                                 // of A and B, and of the products' operands
-  size_t off_part, off_x, off_next, off_a, off_b, bytes;
+  int64_t side, length, ldx, ldt, lds, x_plane, t_plane, ab_plane;  // elements
+  int planes;                                                      // of A and B, and of the products' operands
+  size_t off_part, off_x, off_next, off_t, off_next_t, off_a, off_b, bytes;
 };
+NewtonOne one_of(int64_t rows, int64_t cols) {
+  NewtonOne s{};
+  s.rows = (int)rows;
+  s.cols = (int)cols;
+  s.side = (int)std::min(rows, cols);
+  s.length = (int)std::max(rows, cols);
+  s.high = (int)up(s.side, 32);
+  s.xs = (int)up(s.length, 32) + 8;  // 16 bytes more: rows start in different banks
+  s.as = s.high + 8;
+  return s;
+}
 OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
   OrthoPlan p{};
   p.wide = rows <= cols;
   p.side = std::min(rows, cols);
+  p.length = std::max(rows, cols);
+  if (p.side <= 128 && p.length <= 4096) {
+    const NewtonOne s = one_of(rows, cols);
+    if (4 * (int64_t)s.high * (s.xs + s.as) <= ONE_BYTES) {
+      p.way = ONE;
+      return p;
+    }
+  }
+  // large tiles where they fill the chip
+  p.way = batch * tiles_of(p.side, p.length, 128) >= 200 ? LARGE_TILES : SMALL_TILES;
+  p.planes = dtype != EEC_BF16 || p.side < 256 ? 2 : 1;
+  if (p.planes == 2 && dtype == EEC_BF16) p.way = SMALL_TILES;
   p.ldx = up(cols, 128);
   p.lds = up(p.side, 128);
-  p.planes = dtype == EEC_F32 ? 2 : 1;
   p.x_plane = rows * p.ldx;
   p.ab_plane = p.side * p.lds;
-  const size_t x = align256((size_t)batch * 2 * p.x_plane * 2), ab = align256((size_t)batch * p.planes * p.ab_plane * 2);
-  p.off_part = 0;
-  p.off_x = align256((size_t)batch * SUMS * 8);
-  p.off_next = p.off_x + x;
-  p.off_a = p.off_next + x;
-  p.off_b = p.off_a + ab;
-  p.bytes = p.off_b + ab;
+  if (p.way == SMALL_TILES) {
+    p.ldt = up(rows, 128);
+    p.t_plane = cols * p.ldt;
+  }
+  size_t at = 0;
+  const auto take = [&](size_t& off, int64_t elements, int size) {
+    off = at;
+    at += align256((size_t)batch * (size_t)elements * (size_t)size);
+  };
+  take(p.off_part, SUMS, 8);
+  take(p.off_x, 2 * p.x_plane, 2);
+  take(p.off_next, 2 * p.x_plane, 2);
+  take(p.off_t, 2 * p.t_plane, 2);
+  take(p.off_next_t, 2 * p.t_plane, 2);
+  take(p.off_a, p.planes * p.ab_plane, 2);
+  take(p.off_b, p.planes * p.ab_plane, 2);
+  p.bytes = at;
   return p;
 }
 
-template <bool A_KC, bool B_KC>
-void newton_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue& e, int planes) {
-  if (planes == 2) {
-    const dim3 grid((unsigned)newton_tiles<256, 128>(e.M, e.N, e.symmetric), (unsigned)batch);
-    k_pairs<A_KC, B_KC><<<grid, 512, 0, st>>>(g, e);
-    return;
+// One product on large tiles.
+template <bool A_KC, bool B_KC, typename Y, bool SYM>
+void large_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue<Y, SYM>& e, int planes) {
+  using E = NewtonEpilogue<Y, SYM>;
+  // only bf16 takes one plane
+  if constexpr (std::is_same<Y, float>::value || std::is_same<Y, f16>::value || std::is_same<Y, Planes>::value) {
+    if (planes == 2) {
+      const dim3 grid((unsigned)newton_tiles<256, 128>(e.M, e.N, SYM), (unsigned)batch);
+      k_pairs<A_KC, B_KC, E><<<grid, 512, 0, st>>>(g, e);
+      return;
+    }
   }
-  const int64_t t256 = newton_tiles<256, 256>(e.M, e.N, e.symmetric), t128 = newton_tiles<128, 128>(e.M, e.N, e.symmetric);
-  const double steps = (double)g.K / 32;  // as plan_product
-  const double us128 = (double)((t128 * batch + 255) / 256) * (10 + 0.25 * steps);
-  const double us256 = (double)((t256 * batch + 255) / 256) * (20 + 0.49 * steps);
-  if (us256 < us128)
-    k_tiled<f16, float, A_KC, B_KC, 2, 4, 8, 4, false, NewtonEpilogue><<<dim3((unsigned)t256, (unsigned)batch), 512, 0, st>>>(g, e);
-  else
-    k_tiled<f16, float, A_KC, B_KC, 2, 2, 4, 8, false, NewtonEpilogue><<<dim3((unsigned)t128, (unsigned)batch), 256, 0, st>>>(g, e);
+  if constexpr (std::is_same<Y, bf16>::value || std::is_same<Y, Planes>::value) {
+    const int64_t t256 = newton_tiles<256, 256>(e.M, e.N, SYM), t128 = newton_tiles<128, 128>(e.M, e.N, SYM);
+    const double steps = (double)g.K / 32;  // as plan_product
+    const double us128 = (double)((t128 * batch + 255) / 256) * (10 + 0.25 * steps);
+    const double us256 = (double)((t256 * batch + 255) / 256) * (20 + 0.49 * steps);
+    if (us256 < us128)
+      k_tiled<f16, float, A_KC, B_KC, 2, 4, 8, 4, false, E><<<dim3((unsigned)t256, (unsigned)batch), 512, 0, st>>>(g, e);
+    else
+      k_tiled<f16, float, A_KC, B_KC, 2, 2, 4, 8, false, E><<<dim3((unsigned)t128, (unsigned)batch), 256, 0, st>>>(g, e);
+  }
+}
+template <typename Y, bool SYM, bool TURN>
+void small_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue<Y, SYM, TURN>& e, int planes) {
+  using E = NewtonEpilogue<Y, SYM, TURN>;
+  const dim3 grid((unsigned)newton_tiles<64, 64>(e.M, e.N, SYM), (unsigned)batch);
+  if constexpr (std::is_same<Y, bf16>::value || std::is_same<Y, Planes>::value) {
+    if (planes == 1) {
+      k_small<1, E><<<grid, 256, 0, st>>>(g, e);
+      return;
+    }
+  }
+  k_small<2, E><<<grid, 256, 0, st>>>(g, e);
 }
 
 }  // namespace
 
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
-  return ortho_plan(batch, rows, cols, dtype).bytes;
+  return rows > 0 && cols > 0 ? ortho_plan(batch, rows, cols, dtype).bytes : 0;
 }
 
 void launch_ortho(hipStream_t st, const OrthoArgs& a, char* ws) {
   const OrthoPlan p = ortho_plan(a.batch, a.rows, a.cols, a.dtype);
-  double* part = (double*)(ws + p.off_part);
-  f16 *x = (f16*)(ws + p.off_x), *next = (f16*)(ws + p.off_next), *A = (f16*)(ws + p.off_a), *B = (f16*)(ws + p.off_b);
-  const int64_t x_batch = 2 * p.x_plane, ab_batch = p.planes * p.ab_plane, low = p.planes == 2 ? p.ab_plane : 0;
-  const int groups = (int)std::min<int64_t>(SUMS, (a.rows * a.cols + 4095) / 4096);
   by_type(a.dtype, [&](auto zero) {
     using T = decltype(zero);
-    k_square_sums<T><<<dim3((unsigned)groups, (unsigned)a.batch), 256, 0, st>>>((const T*)a.g, a.ldg, a.stride, a.rows, a.cols, part);
-    const Scaling s{a.g, a.ldg, a.stride, a.rows, a.cols, part, groups, a.eps, x, next, p.ldx, p.x_plane, x_batch, A, B,
-                    p.side, p.lds, low, ab_batch};
-    const int64_t chunks = a.rows * p.ldx / 8;
-    k_scaled<T><<<dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 2048), (unsigned)a.batch), 256, 0, st>>>(s);
-  });
-  for (int32_t i = 0; i < a.steps; ++i) {
-    const double* c = a.coefficients + 3 * i;
-    const bool last = i + 1 == a.steps;
-    const int64_t n = std::max(a.rows, a.cols), xp = 2 * p.x_plane, ap = 2 * p.ab_plane;  // bytes from plane to plane
-    // A = X X^T (X^T X)
-    Product gram{x, x, p.ldx, p.ldx, p.side, p.side, n, n, xp, xp};
-    NewtonEpilogue e{p.side, p.side, p.lds, nullptr, 0, A, low, 0.f, 1.f / SCALE, true, a.dtype, nullptr, x_batch, x_batch,
-                     0, ab_batch, 0};
-    if (p.wide)
-      newton_product<true, true>(st, a.batch, gram, e, p.planes);
-    else
-      newton_product<false, false>(st, a.batch, gram, e, p.planes);
-    // B = b A + c A A
-    const Product square{A, A, p.lds, p.lds, p.side, p.side, p.side, p.side, ap, ap};
-    e.from = A;
-    e.from_plane = low;
-    e.to = B;
-    e.alpha = (float)c[1];
-    e.beta = (float)(c[2] / SCALE);
-    e.a_batch = e.b_batch = e.from_batch = ab_batch;
-    newton_product<true, true>(st, a.batch, square, e, p.planes);
-    // X <- a X + B X (X B)
-    NewtonEpilogue u{a.rows, a.cols, p.ldx, x, p.x_plane, next, p.x_plane, (float)c[0], 1.f / SCALE, false, a.dtype,
-                     last ? a.y : nullptr, ab_batch, x_batch, x_batch, x_batch, a.rows * a.cols};
-    if (p.wide) {
-      const Product update{B, x, p.lds, p.ldx, a.rows, a.cols, p.side, p.side, ap, xp};
-      newton_product<true, false>(st, a.batch, update, u, p.planes);
-    } else {
-      const Product update{x, B, p.ldx, p.lds, a.rows, a.cols, p.side, p.side, xp, ap};
-      std::swap(u.a_batch, u.b_batch);
-      newton_product<true, true>(st, a.batch, update, u, p.planes);
+    if (p.way == ONE) {
+      NewtonOne s = one_of(a.rows, a.cols);
+      s.g = a.g;
+      s.ldg = a.ldg;
+      s.stride = a.stride;
+      s.steps = a.steps;
+      s.eps = a.eps;
+      s.y = a.y;
+      for (int i = 0; i < 3 * a.steps; ++i) s.c[i / 3][i % 3] = (float)a.coefficients[i];
+      k_one<T><<<dim3((unsigned)a.batch), 1024, 0, st>>>(s);
+      return;
     }
-    std::swap(x, next);
-  }
+    double* part = (double*)(ws + p.off_part);
+    f16 *x = (f16*)(ws + p.off_x), *next = (f16*)(ws + p.off_next), *A = (f16*)(ws + p.off_a), *B = (f16*)(ws + p.off_b);
+    f16 *xt = (f16*)(ws + p.off_t), *next_t = (f16*)(ws + p.off_next_t);
+    const bool small = p.way == SMALL_TILES;
+    const int64_t x_batch = 2 * p.x_plane, t_batch = 2 * p.t_plane, ab_batch = p.planes * p.ab_plane;
+    const int64_t low = p.planes == 2 ? p.ab_plane : 0;
+    const int64_t xp = 2 * p.x_plane, tp = 2 * p.t_plane, ap = 2 * p.ab_plane;  // bytes from plane to plane
+    const int groups = (int)std::min<int64_t>(SUMS, (a.rows * a.cols + 4095) / 4096);
+    k_square_sums<T><<<dim3((unsigned)groups, (unsigned)a.batch), 256, 0, st>>>((const T*)a.g, a.ldg, a.stride, a.rows, a.cols, part);
+    const Scaling s{a.g, a.ldg, a.stride, a.rows, a.cols, part, groups, a.eps, x, p.ldx, p.x_plane, x_batch,
+                    small ? xt : nullptr, p.ldt, p.t_plane, t_batch};
+    const int64_t chunks = (small ? p.ldt : a.rows) * p.ldx / 8;
+    k_scaled<T><<<dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 2048), (unsigned)a.batch), 256, 0, st>>>(s);
+    for (int32_t i = 0; i < a.steps; ++i) {
+      const double* c = a.coefficients + 3 * i;
+      const bool last = i + 1 == a.steps;
+      // A = X X^T (X^T X)
+      NewtonEpilogue<Planes, true> e{};
+      e.M = e.N = p.side;
+      e.beta = 1.f / SCALE;
+      e.rows = NewtonTo{nullptr, 0, A, low, p.lds, 0, ab_batch};
+      const bool by_rows = p.wide || !small;  // the operand is X itself
+      e.a_batch = e.b_batch = by_rows ? x_batch : t_batch;
+      const f16* of = by_rows ? x : xt;
+      const int64_t ld = by_rows ? p.ldx : p.ldt, plane = by_rows ? xp : tp;
+      const Product gram{of, of, ld, ld, p.side, p.side, p.length, p.length, plane, plane};
+      if (small)
+        small_product(st, a.batch, gram, e, p.planes);
+      else if (p.wide)
+        large_product<true, true>(st, a.batch, gram, e, p.planes);
+      else
+        large_product<false, false>(st, a.batch, gram, e, p.planes);
+      // B = b A + c A A
+      const Product square{A, A, p.lds, p.lds, p.side, p.side, p.side, p.side, ap, ap};
+      e.alpha = (float)c[1];
+      e.beta = (float)(c[2] / SCALE);
+      e.a_batch = e.b_batch = ab_batch;
+      e.rows = NewtonTo{A, low, B, low, p.lds, ab_batch, ab_batch};
+      if (small)
+        small_product(st, a.batch, square, e, p.planes);
+      else
+        large_product<true, true>(st, a.batch, square, e, p.planes);
+      // X <- a X + B X (X B); small tiles multiply rows of B, and of X, with those of X's transpose, and of B
+      const Product update = p.wide ? Product{B, small ? xt : x, p.lds, small ? p.ldt : p.ldx, a.rows, a.cols, p.side, p.side, ap, small ? tp : xp}
+                                    : Product{x, B, p.ldx, p.lds, a.rows, a.cols, p.side, p.side, xp, ap};
+      const auto fill = [&](auto u) {
+        u.M = a.rows;
+        u.N = a.cols;
+        u.alpha = (float)c[0];
+        u.beta = 1.f / SCALE;
+        u.rows = NewtonTo{x, p.x_plane, next, p.x_plane, p.ldx, x_batch, x_batch};
+        u.a_batch = p.wide ? ab_batch : x_batch;
+        u.b_batch = !p.wide ? ab_batch : small ? t_batch : x_batch;
+        return u;
+      };
+      if (last) {
+        auto u = fill(NewtonEpilogue<T, false>{});
+        u.y = (T*)a.y;
+        u.y_batch = a.rows * a.cols;
+        if (small)
+          small_product(st, a.batch, update, u, p.planes);
+        else if (p.wide)
+          large_product<true, false>(st, a.batch, update, u, p.planes);
+        else
+          large_product<true, true>(st, a.batch, update, u, p.planes);
+      } else if (small) {
+        auto u = fill(NewtonEpilogue<Planes, false, true>{});
+        u.turned = NewtonTo{xt, p.t_plane, next_t, p.t_plane, p.ldt, t_batch, t_batch};
+        small_product(st, a.batch, update, u, p.planes);
+      } else {
+        const auto u = fill(NewtonEpilogue<Planes, false>{});
+        if (p.wide)
+          large_product<true, false>(st, a.batch, update, u, p.planes);
+        else
+          large_product<true, true>(st, a.batch, update, u, p.planes);
+      }
+      std::swap(x, next);
+      std::swap(xt, next_t);
+    }
+  });
 }
 
 }  // namespace eec

@@ -33,8 +33,10 @@ def ortho(batch=2, rows=64, cols=48, dtype=F32, g=P(1), ldg=48, stride=64 * 48, 
     (lambda: ortho(g=None), "EEC_ERR_NULL"), (lambda: ortho(y=None), "EEC_ERR_NULL"),
     (lambda: ortho(ldg=47), "EEC_ERR_SHAPE"), (lambda: ortho(stride=64 * 48 - 1), "EEC_ERR_SHAPE"), (lambda: ortho(stride=-64 * 48), "EEC_ERR_SHAPE"),
     (lambda: ortho(g=ctypes.c_void_p((1 << 32) + 2)), "EEC_ERR_SHAPE"),
-    (lambda: ortho(ws=None), "EEC_ERR_WORKSPACE"), (lambda: ortho(size=1024), "EEC_ERR_WORKSPACE"),
-    (lambda: ortho(ws=ctypes.c_void_p((3 << 32) + 64)), "EEC_ERR_WORKSPACE"),
+    (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, ws=None), "EEC_ERR_WORKSPACE"),
+    (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, size=1024), "EEC_ERR_WORKSPACE"),
+    (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, ws=ctypes.c_void_p((3 << 32) + 64)), "EEC_ERR_WORKSPACE"),
+    (lambda: ortho(ws=None, size=0, y=P(1)), "EEC_ERR_ALIAS"),  # small updates need none
     (lambda: ortho(y=P(1)), "EEC_ERR_ALIAS"), (lambda: ortho(y=P(3)), "EEC_ERR_ALIAS"), (lambda: ortho(ws=P(1)), "EEC_ERR_ALIAS"),
     # y over the second matrix of the batch
     (lambda: ortho(stride=1 << 20, y=ctypes.c_void_p((1 << 32) + (4 << 20))), "EEC_ERR_ALIAS"),

@@ -77,11 +77,15 @@ def test_updates(rows, cols, dt):
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
-@pytest.mark.parametrize("rows,cols", [(1300, 2100), (2100, 1300), (1536, 1536)])
-def test_large_updates(rows, cols, dt):
-    """Many tiles of every kind, above and across the diagonal."""
-    g = update(torch.Generator().manual_seed(rows), rows, cols, dt)
-    check(B.orthogonalize(g), g, dt)
+@pytest.mark.parametrize("batch,rows,cols", [(1, 1300, 2100), (1, 1536, 1536), (1, 1700, 2100), (1, 2100, 1701), (3, 1290, 1000), (3, 1000, 1290)])
+def test_large_updates(batch, rows, cols, dt):
+    """Small and large tiles of every kind, above and across the diagonal."""
+    gen = torch.Generator().manual_seed(rows)
+    g = torch.stack([update(gen, rows, cols, dt) for _ in range(batch)])
+    y = B.orthogonalize(g)
+    check(y[-1], g[-1], dt)
+    if batch > 1:
+        check(y[0], g[0], dt)
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
@@ -216,7 +220,7 @@ def test_arguments_of_the_binding():
         with pytest.raises(ValueError):
             call()
     for call in (lambda: B.orthogonalize(g, 0), lambda: B.orthogonalize(g, eps=0.0), lambda: B.orthogonalize(g, 3, (2.0, 0.0, 0.0)),
-                 lambda: B.orthogonalize(g[None].expand(4, 6, 8)), lambda: B.orthogonalize(g, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))):
+                 lambda: B.orthogonalize(g[None].expand(4, 6, 8)), lambda: B.orthogonalize(torch.zeros((300, 300), device=DEV), workspace=torch.empty(256, dtype=torch.uint8, device=DEV))):
         with pytest.raises(B.EECError):
             call()
     assert B.orthogonalize(g[:0]).shape == (0, 8) and B.orthogonalize(g[:, :0]).shape == (6, 0) and B.orthogonalize(g[None][:0]).shape == (0, 6, 8)
