@@ -83,7 +83,10 @@ int64_t newton_tiles(int64_t M, int64_t N, bool symmetric) {
   return all;
 }
 
+// Both parts from one float32 number: left to itself the compiler fuses the sum that makes v with
+// its rounding to hi, and where that differs from the rounding of v, lo belongs to another hi (one value in 8192).
 __device__ __forceinline__ void split2(float v, f16& hi, f16& lo) {
+  asm("" : "+v"(v));
   hi = (f16)v;
   lo = (f16)(v - (float)hi);
 }
@@ -92,20 +95,23 @@ __device__ __forceinline__ void split2(float v, f16& hi, f16& lo) {
 // to do).  Planes have rows of whole runs, whose end is kept at zero, so that each run is one store.
 struct Run8 {
   int64_t m, n, left;
-  f16 hi[8], lo[8];  // what alpha multiplies
-  __device__ __forceinline__ void load(const NewtonTo& s) {
-    if (left <= 0 || s.from == nullptr) return;
-    const f16* p = s.from + m * s.ld + n;
-    __builtin_memcpy(hi, __builtin_assume_aligned(p, 16), 16);
-    if (s.from_plane) __builtin_memcpy(lo, __builtin_assume_aligned(p + s.from_plane, 16), 16);
+  f16 hi[8], lo[8];  // what alpha multiplies, or zeros
+  // `at`: elements from (row m0, column n0), both uniform, where the wave's sums start.  No branch, so that nothing
+  // waits for these loads before their use; what does not exist is read past every buffer, as zero.
+  __device__ __forceinline__ void load(const NewtonTo& s, int64_t m0, int64_t n0, uint32_t at) {
+    constexpr uint32_t NOWHERE = 0x80000000u;
+    const f16* p = s.from + m0 * s.ld + n0;
+    const auto part = [&](const f16* from, bool is, f16 (&v)[8]) {
+      const auto q = __builtin_amdgcn_raw_buffer_load_b128(
+          __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0x7fffffff, 0x00020000), is && left > 0 ? at * 2 : NOWHERE, 0, 0);
+      __builtin_memcpy(v, &q, 16);
+    };
+    part(p, s.from != nullptr, hi);
+    part(p + s.from_plane, s.from_plane != 0, lo);
   }
-  __device__ __forceinline__ void value(const NewtonTo& s, float alpha, float beta, float (&v)[8]) const {
+  __device__ __forceinline__ void value(float alpha, float beta, float (&v)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= beta;
-    if (s.from) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += alpha * (s.from_plane ? (float)hi[i] + (float)lo[i] : (float)hi[i]);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = alpha * ((float)hi[i] + (float)lo[i]) + beta * v[i];
   }
   __device__ __forceinline__ void store(const NewtonTo& s, const float (&v)[8]) const {
     f16 h[8], l[8];
@@ -123,31 +129,32 @@ __device__ __forceinline__ float sum_at(const char* lds, int r, int c) {
   return v;
 }
 
-// Finishes ROWS x 64 sums of a wave, row by row of 256 bytes in its LDS as put_sums leaves them.
+// Finishing a wave's sums, row by row of 256 bytes (64 columns) in its LDS as put_sums leaves them.
 // Symmetric: 8 x 8 blocks on and above the diagonal are stored, and those above it once more
 // across it, from columns of the same sums; a block on the diagonal takes its lower half from its
 // upper one.  So each element is written once, by one lane, and C is symmetric to the bit.  What
-// four runs a lane need from memory is loaded before any of them is stored.
-template <int ROWS, typename Y, bool SYM, bool TURN>
-__device__ __forceinline__ void finish_sums(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int64_t top, int64_t n0) {
-  constexpr int RUNS = ROWS / 8, TOGETHER = RUNS < 4 ? RUNS : 4;
-  static_assert(RUNS % TOGETHER == 0, "whole batches");
-  const int lane = threadIdx.x & 63;
-  const int r0 = lane >> 3, col = (lane & 7) * 8;
-#pragma unroll 1
-  for (int j = 0; j < RUNS; j += TOGETHER) {
-    Run8 run[TOGETHER];
+// N runs a lane need from memory is loaded before any of them is stored.
+//
+// 8 columns of rows r, r + 8, ... of a lane, r that of its eighth of the wave.
+template <int N>
+struct RowRuns {
+  Run8 run[N];
+  template <typename Y, bool SYM, bool TURN>
+  __device__ __forceinline__ void load(const NewtonEpilogue<Y, SYM, TURN>& e, int64_t top, int64_t n0, int r) {
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) {
-      run[i].m = top + r0 + (j + i) * 8;
-      run[i].n = n0 + col;
+    for (int i = 0; i < N; ++i) {
+      run[i].m = top + r + i * 8;
+      run[i].n = n0 + (threadIdx.x & 7) * 8;
       run[i].left = run[i].m < e.M && !(SYM && run[i].n + 7 < run[i].m) ? e.N - run[i].n : 0;
-      run[i].load(e.rows);
+      run[i].load(e.rows, top, n0, (uint32_t)((r + i * 8) * (int)e.rows.ld + (threadIdx.x & 7) * 8));
     }
+  }
+  template <typename Y, bool SYM, bool TURN>
+  __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int r) const {
+    const int col = (threadIdx.x & 7) * 8;
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) {
+    for (int i = 0; i < N; ++i, r += 8) {
       if (run[i].left <= 0) continue;
-      const int r = r0 + (j + i) * 8;
       float v[8];
 #pragma unroll
       for (int u = 0; u < 8; u += 4)
@@ -157,7 +164,7 @@ __device__ __forceinline__ void finish_sums(const NewtonEpilogue<Y, SYM, TURN>& 
         for (int u = 0; u < 8; ++u)
           if (run[i].n + u < run[i].m) v[u] = sum_at(lds, (r & ~7) + u, col + (r & 7));
       }
-      run[i].value(e.rows, e.alpha, e.beta, v);
+      run[i].value(e.alpha, e.beta, v);
       if constexpr (std::is_same<Y, Planes>::value) {
         run[i].store(e.rows, v);
       } else {
@@ -167,29 +174,53 @@ __device__ __forceinline__ void finish_sums(const NewtonEpilogue<Y, SYM, TURN>& 
       }
     }
   }
-  if constexpr (SYM || TURN) {  // row n0 + lane of the transpose: eight of this side's rows at a time
-    const NewtonTo& to = TURN ? e.turned : e.rows;
-    const int64_t m = n0 + lane;
+};
+// Row n0 + lane of the transpose: rows r to r + 8 N - 1 of this side.
+template <int N>
+struct TurnedRuns {
+  Run8 run[N];
+  template <typename Y, bool SYM, bool TURN>
+  static __device__ __forceinline__ const NewtonTo& to(const NewtonEpilogue<Y, SYM, TURN>& e) { return TURN ? e.turned : e.rows; }
+  template <typename Y, bool SYM, bool TURN>
+  __device__ __forceinline__ void load(const NewtonEpilogue<Y, SYM, TURN>& e, int64_t top, int64_t n0, int r) {
+    const int64_t m = n0 + (threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      run[i].m = m;
+      run[i].n = top + r + i * 8;
+      run[i].left = m < e.N && !(SYM && run[i].n + 7 >= m) ? e.M - run[i].n : 0;  // symmetric: blocks above the diagonal
+      run[i].load(to(e), n0, top, (uint32_t)((threadIdx.x & 63) * (int)to(e).ld + r + i * 8));
+    }
+  }
+  template <typename Y, bool SYM, bool TURN>
+  __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int r) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i, r += 8) {
+      if (run[i].left <= 0) continue;
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = sum_at(lds, r + u, threadIdx.x & 63);
+      run[i].value(e.alpha, e.beta, v);
+      run[i].store(to(e), v);
+    }
+  }
+};
+template <int ROWS, typename Y, bool SYM, bool TURN>
+__device__ __forceinline__ void finish_sums(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int64_t top, int64_t n0) {
+  constexpr int N = ROWS < 32 ? ROWS / 8 : 4;
+  static_assert(ROWS % (8 * N) == 0, "whole batches");
 #pragma unroll 1
-    for (int j = 0; j < RUNS; j += TOGETHER) {
-      Run8 run[TOGETHER];
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        run[i].m = m;
-        run[i].n = top + (j + i) * 8;
-        run[i].left = m < e.N && !(SYM && run[i].n + 7 >= m) ? e.M - run[i].n : 0;  // symmetric: blocks above the diagonal
-        run[i].load(to);
-      }
-#pragma unroll
-      for (int i = 0; i < TOGETHER; ++i) {
-        if (run[i].left <= 0) continue;
-        const int r = (j + i) * 8;
-        float v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = sum_at(lds, r + u, lane);
-        run[i].value(to, e.alpha, e.beta, v);
-        run[i].store(to, v);
-      }
+  for (int r = 0; r < ROWS; r += 8 * N) {
+    RowRuns<N> rows;
+    rows.load(e, top, n0, r + (threadIdx.x >> 3 & 7));
+    rows.finish(e, lds, r + (threadIdx.x >> 3 & 7));
+  }
+  if constexpr (SYM || TURN) {
+#pragma unroll 1
+    for (int r = 0; r < ROWS; r += 8 * N) {
+      TurnedRuns<N> turned;
+      turned.load(e, top, n0, r);
+      turned.finish(e, lds, r);
     }
   }
 }
@@ -283,42 +314,58 @@ __global__ void __launch_bounds__(512) k_pairs(Product g, E e) {
 
 // ------------------------------------------------------------------ small tiles
 
-// 64 x 64 of C per workgroup of four waves, P planes, both operands with k along memory: for
-// products whose large tiles would leave most CUs idle.  A workgroup gets 64 KB of operands every
-// microsecond or so whatever it does, so seven steps of 32 k are on their way at a time.
+// 64 x 64 of C per workgroup, P planes, both operands with k along memory: for products whose
+// large tiles would leave most CUs idle.  A step is 64 k of all planes, both halves of its
+// operands' cache lines, four waves (32 x 32 each) for each half, joined in LDS at the end; three
+// steps are on their way at a time, and what the epilogue reads is loaded before them (%SMALL%).
+template <typename E>
+constexpr bool SYM_OR_TURN = false;
+template <typename Y, bool SYM, bool TURN>
+constexpr bool SYM_OR_TURN<NewtonEpilogue<Y, SYM, TURN>> = SYM || TURN;
+
 template <int P, typename E>
-__global__ void __launch_bounds__(256) k_small(Product g, E e) {
+__global__ void __launch_bounds__(512) k_small(Product g, E e) {
 #ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
   of_batch(g, e);
-  using T = Tile<f16, true, 64, 4>;
-  constexpr int LOADS = 2 * P * T::LOADS, B = P * T::BYTES;
-  __shared__ __attribute__((aligned(1024))) char a0[2 * B], a1[2 * B], a2[2 * B], a3[2 * B], a4[2 * B], a5[2 * B], a6[2 * B], a7[2 * B];
-  const int lane = threadIdx.x & 63, wave = wave_id();
+  using T = Tile<f16, true, 64, 4>;  // one plane of one half of one operand
+  constexpr int LOADS = 2 * P, B = T::BYTES;
+  // of each half P planes of A, then of B
+  __shared__ __attribute__((aligned(1024))) char a0[4 * P * B], a1[4 * P * B], a2[4 * P * B], a3[4 * P * B];
+  const int lane = threadIdx.x & 63, wave = wave_id() & 3, half = wave_id() >> 2;
   const Place place = place_of<64, 64>(e);
   const int64_t m0 = place.m, n0 = place.n;
-  const int wm = wave / 2 * 32, wn = wave % 2 * 32;
+  const int wm = wave / 2 * 32, wn = wave % 2 * 32, row = wave_id() * 8;
   f32x4 acc[2][2] = {};
-  T ta, tb;
-  ta.init(g.a, g.lda, m0, g.M, 0);
-  tb.init(g.b, g.ldb, n0, g.N, 0);
+  const char *pa = (const char*)g.a + m0 * g.lda * 2 + half * 64, *pb = (const char*)g.b + n0 * g.ldb * 2 + half * 64;
+  const int line = wave * 16 + (lane >> 2), k = T::at_k(0);
+  // lines past the end: not stored
+  const uint32_t oa = (uint32_t)(min((int64_t)line, g.M - 1 - m0) * g.lda * 2) + k * 2;
+  const uint32_t ob = (uint32_t)(min((int64_t)line, g.N - 1 - n0) * g.ldb * 2) + k * 2;
   auto load = [&](char* to, int left) {
+    const bool is = half * 32 + k < left;
+    const auto one = [&](char* at, const char* from, uint32_t off) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0x7fffffff, 0x00020000),
+          (__attribute__((address_space(3))) void*)(at + wave * 1024), 16, is ? off : T::NOWHERE, 0, 0, 0);
+    };
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      ta.load_from(to + p * T::BYTES, ta.base + p * g.a_plane, left);
-      tb.load_from(to + B + p * T::BYTES, tb.base + p * g.b_plane, left);
+      one(to + (half * 2 * P + p) * B, pa + p * g.a_plane, oa);
+      one(to + (half * 2 * P + P + p) * B, pb + p * g.b_plane, ob);
     }
-    ta.base += ta.step;
-    tb.base += tb.step;
+    pa += 128;
+    pb += 128;
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto step = [&](const char* la) {
+  auto step = [&](const char* from) {
+    const char* la = from + half * 2 * P * B;
     f16x8 a[2][P], b[2][P];
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        T::fragment(a[i][p], la + p * T::BYTES, wm, i);
-        T::fragment(b[i][p], la + B + p * T::BYTES, wn, i);
+        T::fragment(a[i][p], la + p * B, wm, i);
+        T::fragment(b[i][p], la + (P + p) * B, wn, i);
       }
     // in rising size: (lo, hi), (hi, lo), (hi, hi)
 #pragma unroll
@@ -329,39 +376,47 @@ __global__ void __launch_bounds__(256) k_small(Product g, E e) {
         for (int j = 0; j < 2; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j][t == 1 ? P - 1 : 0], a[i][t == 0 ? P - 1 : 0], acc[i][j], 0, 0, 0);
   };
+  RowRuns<1> rows;
+  TurnedRuns<1> turned;
+  rows.load(e, m0, n0, row + (lane >> 3));
+  if constexpr (SYM_OR_TURN<E>) turned.load(e, m0, n0, row);
   int left = (int)g.K;
   load(a0, left);
-  load(a1, left - 32);
-  load(a2, left - 64);
-  load(a3, left - 96);
-  load(a4, left - 128);
-  load(a5, left - 160);
-  load(a6, left - 192);
-#define EEC_STEP(T, NOW, FREE)   \
-  tile_barrier<6 * LOADS>();     \
-  load(FREE, left - (T + 7) * 32); \
-  step(NOW);                     \
-  if (left <= (T + 1) * 32) break
+  load(a1, left - 64);
+  load(a2, left - 128);
+#define EEC_STEP(T, NOW, FREE)     \
+  tile_barrier<2 * LOADS>();       \
+  load(FREE, left - (T + 3) * 64); \
+  step(NOW);                       \
+  if (left <= (T + 1) * 64) break
   for (;; left -= 256) {
-    EEC_STEP(0, a0, a7);
+    EEC_STEP(0, a0, a3);
     EEC_STEP(1, a1, a0);
     EEC_STEP(2, a2, a1);
     EEC_STEP(3, a3, a2);
-    EEC_STEP(4, a4, a3);
-    EEC_STEP(5, a5, a4);
-    EEC_STEP(6, a6, a5);
-    EEC_STEP(7, a7, a6);
   }
 #undef EEC_STEP
   tile_barrier<0>();
-  // the workgroup's sums: rows 0 to 31 and 32 to 63 in 8 KB each
-  char* high = wave < 2 ? a0 : a1;
+  // sums of the first half of every step: 64 rows in a buffer of 16 KB, or two of 8 KB; of the second in the next
+  constexpr bool TWO = 4 * P * B < 16384;
+  char* mine = TWO ? (half == 0 ? (wave < 2 ? a0 : a1) : (wave < 2 ? a2 : a3)) : (half == 0 ? a0 : a1) + wave / 2 * 8192;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) put_sums(high, 16 * i + (lane & 15), wn / 4 + 4 * j + (lane >> 4), acc[i][j]);
+    for (int j = 0; j < 2; ++j) put_sums(mine, 16 * i + (lane & 15), wn / 4 + 4 * j + (lane >> 4), acc[i][j]);
   __syncthreads();
-  finish_sums<16>(e, high + wave % 2 * 4096, m0 + wave * 16, n0);
+  const int at = threadIdx.x * 32;
+  char *first = TWO && at >= 8192 ? a1 + (at - 8192) : a0 + at, *second = TWO ? (at >= 8192 ? a3 + (at - 8192) : a2 + at) : a1 + at;
+  f32x4 u[2], v[2];
+  __builtin_memcpy(u, __builtin_assume_aligned(first, 16), 32);
+  __builtin_memcpy(v, __builtin_assume_aligned(second, 16), 32);
+  u[0] += v[0];
+  u[1] += v[1];
+  __builtin_memcpy(__builtin_assume_aligned(first, 16), u, 32);
+  __syncthreads();
+  const char* sums = TWO && row >= 32 ? a1 - 8192 : a0;
+  rows.finish(e, sums, row + (lane >> 3));
+  if constexpr (SYM_OR_TURN<E>) turned.finish(e, sums, row);
 #endif
 }
 
@@ -394,23 +449,48 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
   const T* g = (const T*)s.g + blockIdx.x * s.stride;
   T* y = (T*)s.y + (int64_t)blockIdx.x * s.rows * s.cols;
   const bool wide = s.rows <= s.cols;
-  const int total = s.rows * s.cols;
+  for (int i = threadIdx.x; i < (x_plane + a_plane) / 4; i += 1024) ((i32x4*)lds)[i] = i32x4{};  // 2 planes, 8 a store
+  __syncthreads();
+  // g in runs of four elements of a row, dealt to the threads in turn; its float32 values wait
+  // for their scale where X's two parts will be, half in each
   double sum = 0.0;
-  for (int i = threadIdx.x; i < total; i += 1024) {
-    const double v = (float)g[(int64_t)(i / s.cols) * s.ldg + i % s.cols];
-    sum += v * v;
+  {
+    const int per_row = (s.cols + 3) / 4, down = 1024 / per_row, along = 1024 % per_row;
+    const int dr = wide ? s.xs : 1, dc = wide ? 1 : s.xs;
+    int r = threadIdx.x / per_row, c = threadIdx.x % per_row;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < s.rows * per_row; i += 1024) {
+      float v[4];
+      load_run(g + (int64_t)r * s.ldg + c * 4, s.cols - c * 4, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c * 4 + j < s.cols) {
+          const int at = r * dr + (c * 4 + j) * dc;
+          const uint32_t u = __float_as_uint(v[j]);
+          ((uint16_t*)x)[at] = (uint16_t)(u >> 16);
+          ((uint16_t*)x)[at + x_plane] = (uint16_t)u;
+          sum += (double)v[j] * v[j];
+        }
+      r += down, c += along;
+      if (c >= per_row) c -= per_row, ++r;
+    }
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
   if (lane == 0) join[wave] = sum;
-  for (int i = threadIdx.x; i < (x_plane + a_plane) / 4; i += 1024) ((i32x4*)lds)[i] = i32x4{};  // 2 planes, 8 a store
   __syncthreads();
   sum = 0.0;
   for (int i = 0; i < 16; ++i) sum += join[i];
   const double scale = (double)SCALE / (sqrt(sum) + s.eps);
-  for (int i = threadIdx.x; i < total; i += 1024) {
-    const int r = i / s.cols, c = i % s.cols, at = wide ? r * s.xs + c : c * s.xs + r;
-    split2((float)((float)g[(int64_t)r * s.ldg + c] * scale), x[at], x[at + x_plane]);
+  for (int i = threadIdx.x; i < x_plane / 8; i += 1024) {
+    uint16_t h[8], l[8];
+    f16 hi[8], lo[8];
+    __builtin_memcpy(h, __builtin_assume_aligned(x + i * 8, 16), 16);
+    __builtin_memcpy(l, __builtin_assume_aligned(x + x_plane + i * 8, 16), 16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split2((float)(__uint_as_float((uint32_t)h[j] << 16 | l[j]) * scale), hi[j], lo[j]);
+    __builtin_memcpy(__builtin_assume_aligned(x + i * 8, 16), hi, 16);
+    __builtin_memcpy(__builtin_assume_aligned(x + x_plane + i * 8, 16), lo, 16);
   }
   __syncthreads();
   const int tiles = (s.side + 15) / 16, strips = (s.length + 15) / 16, ks = s.high / 32;
@@ -424,15 +504,18 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(n[1], m[0], acc, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(n[0], m[0], acc, 0, 0, 0);
   };
-  // 16 rows from row 16 i and 16 from 16 j of a matrix, multiplied over n x 32 columns
-  const auto gram = [&](const f16* p, int plane, int ld, int i, int j, int n) {
-    f32x4 acc = {};
-    const f16 *pi = p + (16 * i + line) * ld + q * 8, *pj = p + (16 * j + line) * ld + q * 8;
-    for (int k = 0; k < n; ++k, pi += 32, pj += 32) {
-      const f16x8 m[2] = {row8(pi), row8(pi + plane)}, c[2] = {row8(pj), row8(pj + plane)};
-      acc = product(c, m, acc);
+  // 16 rows from row 16 i and 16 from 16 j of a matrix, multiplied over every `by`-th 32 of n x 32 columns from the k-th on
+  const auto gram = [&](const f16* p, int plane, int ld, int i, int j, int n, int k = 0, int by = 1) {
+    f32x4 acc = {}, low = {};
+    const f16 *pi = p + (16 * i + line) * ld + q * 8 + 32 * k, *pj = p + (16 * j + line) * ld + q * 8 + 32 * k;
+#pragma unroll 2
+    for (; k < n; k += by, pi += 32 * by, pj += 32 * by) {
+      const f16x8 mh = row8(pi), ml = row8(pi + plane), ch = row8(pj), cl = row8(pj + plane);
+      low = __builtin_amdgcn_mfma_f32_16x16x32_f16(ch, ml, low, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ch, mh, acc, 0, 0, 0);
+      low = __builtin_amdgcn_mfma_f32_16x16x32_f16(cl, mh, low, 0, 0, 0);
     }
-    return acc;
+    return acc + low;
   };
   // row 16 i + line, columns 16 j + 4 q and three more of a symmetric matrix: those on and above the diagonal, on both sides
   const auto put = [&](int i, int j, const f32x4& v) {
@@ -454,12 +537,26 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
     j = i + n;
   };
   const int pairs = tiles * (tiles + 1) / 2, length32 = (s.length + 31) / 32;
+  const int parts = max(1, min(16 / pairs, length32));  // waves of a tile of A
   for (int step = 0; step < s.steps; ++step) {
     const float ca = s.c[step][0], cb = s.c[step][1], cc = s.c[step][2] / SCALE;
     int i, j;
-    for (int n = wave; n < pairs; n += 16) {  // A
-      tile_at(n, i, j);
-      put(i, j, gram(x, x_plane, s.xs, i, j, length32) * (1.f / SCALE));
+    if (parts == 1) {  // A
+      for (int n = wave; n < pairs; n += 16) {
+        tile_at(n, i, j);
+        put(i, j, gram(x, x_plane, s.xs, i, j, length32) * (1.f / SCALE));
+      }
+    } else {  // every tile by several waves, joined in order; where A will be, the old B is read no more
+      f32x4* joined = (f32x4*)a;
+      tile_at(wave % pairs, i, j);
+      if (wave < parts * pairs) joined[wave * 64 + lane] = gram(x, x_plane, s.xs, i, j, length32, wave / pairs, parts);
+      __syncthreads();
+      f32x4 sum = joined[wave % pairs * 64 + lane];
+      for (int t = 1; t < parts; ++t) sum += joined[(wave % pairs + t * pairs) * 64 + lane];
+      __syncthreads();
+      for (int t = threadIdx.x; t < a_plane / 4; t += 1024) ((i32x4*)a)[t] = i32x4{};
+      __syncthreads();
+      if (wave < pairs) put(i, j, sum * (1.f / SCALE));
     }
     __syncthreads();
     f32x4 b[3];  // B, in A's place when everybody has read A: up to 36 tiles
@@ -578,28 +675,42 @@ __global__ void __launch_bounds__(256) k_scaled(Scaling s) {
   const double scale = (double)SCALE / (sqrt((join[0] + join[1]) + (join[2] + join[3])) + s.eps);
   const T* g = (const T*)s.g + batch * s.stride;
   f16 *x = s.x + batch * s.batch, *turned = s.turned + batch * s.turned_batch;
-  const int64_t per_row = s.ldx / 8, high = s.turned ? s.ldt : s.rows;  // the transpose's padding are rows past the end
-  const int64_t total = high * per_row, all = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += all) {
-    const int64_t r = i / per_row, c = i % per_row * 8, at = r * s.ldx + c;
-    float v[8];
-    load_run<true>(g + r * s.ldg + c, r < s.rows ? s.cols - c : 0, v);
+  __shared__ float tile[64][65];
+  const int64_t across = (s.cols + 63) / 64, tiles = across * ((s.rows + 63) / 64);
+  const int line = threadIdx.x >> 3, run = (threadIdx.x & 7) * 8;
+  const auto put = [](f16* to, int64_t plane, const float (&v)[8]) {
     f16 hi[8], lo[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)  // an infinite scale makes no NaN of the padding
-      split2(r < s.rows && c + j < s.cols ? (float)(v[j] * scale) : 0.f, hi[j], lo[j]);
-    if (r < s.rows) {
-      __builtin_memcpy(__builtin_assume_aligned(x + at, 16), hi, 16);
-      __builtin_memcpy(__builtin_assume_aligned(x + at + s.plane, 16), lo, 16);
-    }
-    if (s.turned) {
+    for (int j = 0; j < 8; ++j) split2(v[j], hi[j], lo[j]);
+    __builtin_memcpy(__builtin_assume_aligned(to, 16), hi, 16);
+    __builtin_memcpy(__builtin_assume_aligned(to + plane, 16), lo, 16);
+  };
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t r0 = t / across * 64, c0 = t % across * 64;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < s.cols) {
-          turned[(c + j) * s.ldt + r] = hi[j];
-          turned[(c + j) * s.ldt + r + s.turned_plane] = lo[j];
-        }
+    for (int h = 0; h < 64; h += 32) {
+      const int64_t r = r0 + line + h, c = c0 + run;
+      float v[8];
+      load_run<true>(g + r * s.ldg + c, r < s.rows ? s.cols - c : 0, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = r < s.rows && c + j < s.cols ? (float)(v[j] * scale) : 0.f;  // an infinite scale makes no NaN of the padding
+      if (r < s.rows && c < s.cols) put(x + r * s.ldx + c, s.plane, v);
+      if (s.turned) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tile[line + h][run + j] = v[j];
+      }
     }
+    if (!s.turned) continue;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 64; h += 32) {
+      const int64_t c = c0 + line + h, r = r0 + run;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = tile[run + j][line + h];
+      if (c < s.cols && r < s.rows) put(turned + c * s.ldt + r, s.turned_plane, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -633,7 +744,8 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
   p.length = std::max(rows, cols);
   if (p.side <= 128 && p.length <= 4096) {
     const NewtonOne s = one_of(rows, cols);
-    if (4 * (int64_t)s.high * (s.xs + s.as) <= ONE_BYTES) {
+    const int64_t square = std::max<int64_t>(4 * s.high * s.as, 16 * 1024);  // or a tile of each wave
+    if (4 * (int64_t)s.high * s.xs + square <= ONE_BYTES) {
       p.way = ONE;
       return p;
     }
@@ -695,11 +807,11 @@ void small_product(hipStream_t st, int64_t batch, const Product& g, const Newton
   const dim3 grid((unsigned)newton_tiles<64, 64>(e.M, e.N, SYM), (unsigned)batch);
   if constexpr (std::is_same<Y, bf16>::value || std::is_same<Y, Planes>::value) {
     if (planes == 1) {
-      k_small<1, E><<<grid, 256, 0, st>>>(g, e);
+      k_small<1, E><<<grid, 512, 0, st>>>(g, e);
       return;
     }
   }
-  k_small<2, E><<<grid, 256, 0, st>>>(g, e);
+  k_small<2, E><<<grid, 512, 0, st>>>(g, e);
 }
 
 }  // namespace
@@ -735,8 +847,8 @@ void launch_ortho(hipStream_t st, const OrthoArgs& a, char* ws) {
     k_square_sums<T><<<dim3((unsigned)groups, (unsigned)a.batch), 256, 0, st>>>((const T*)a.g, a.ldg, a.stride, a.rows, a.cols, part);
     const Scaling s{a.g, a.ldg, a.stride, a.rows, a.cols, part, groups, a.eps, x, p.ldx, p.x_plane, x_batch,
                     small ? xt : nullptr, p.ldt, p.t_plane, t_batch};
-    const int64_t chunks = (small ? p.ldt : a.rows) * p.ldx / 8;
-    k_scaled<T><<<dim3((unsigned)std::min<int64_t>((chunks + 255) / 256, 2048), (unsigned)a.batch), 256, 0, st>>>(s);
+    const int64_t tiles = tiles_of(a.rows, a.cols, 64);
+    k_scaled<T><<<dim3((unsigned)std::min<int64_t>(tiles, 4096), (unsigned)a.batch), 256, 0, st>>>(s);
     for (int32_t i = 0; i < a.steps; ++i) {
       const double* c = a.coefficients + 3 * i;
       const bool last = i + 1 == a.steps;
