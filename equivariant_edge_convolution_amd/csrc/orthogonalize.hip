@@ -422,43 +422,48 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
 
 // ------------------------------------------------------------------ whole updates in one workgroup
 
-// An update whose planes fit the LDS of one CU: every step of it in one launch of a workgroup of
-// 16 waves a matrix (4 of 256 x 64 float32, five steps: %%ONE%%).  X lies there by rows of
-// the shorter side, two planes of `high` rows (a multiple of 32; those past the end are zeros, and
-// so are columns past the end), and one square that holds A, then B.  Two planes in every product.
+// An update whose planes fit the LDS of one CU: every step of it in one launch, a workgroup of
+// 16 waves a matrix (%ONE%).  X lies there by rows of the shorter side, two planes
+// of HIGH rows (those past the end are zeros, and so are columns past the end), with one
+// square that holds A, then B.  Two planes in every product.  TILES: rows of 16 in the shorter side.
 constexpr int ONE_BYTES = 158 * 1024;
+constexpr int one_high(int tiles) { return tiles < 2 ? 32 : 16 * tiles; }
+// Bytes of the square, or of one matrix tile of each wave.
+constexpr int one_square(int tiles) { return std::max(4 * one_high(tiles) * (one_high(tiles) + 8), 16 * 1024); }
 struct NewtonOne {
   const void* g;
   int64_t ldg, stride;
-  int rows, cols, side, length;  // side <= length: rows and cols, in one order or the other
-  int high, xs, as;              // rows of X and of the square; elements from row to row of each
+  int rows, cols, length;  // length: of the longer side
+  int xs;                  // elements from row to row of X
   int steps;
   double eps;
   void* y;
   float c[64][3];
 };
-template <typename T>
+template <typename T, int TILES>
 __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
 #ifdef __HIP_DEVICE_COMPILE__
+  constexpr int HIGH = one_high(TILES), AS = HIGH + 8, A_PLANE = HIGH * AS, KS = HIGH / 32;
+  constexpr int PAIRS = TILES * (TILES + 1) / 2, EACH = (PAIRS + 15) / 16;  // tiles of A on and above the diagonal
   __shared__ __attribute__((aligned(16))) char lds[ONE_BYTES];
   __shared__ double join[16];
   const int lane = threadIdx.x & 63, wave = wave_id(), line = lane & 15, q = lane >> 4;
   f16* x = (f16*)lds;
-  const int x_plane = s.high * s.xs, a_plane = s.high * s.as;
+  const int xs = s.xs, x_plane = HIGH * xs;
   f16* a = x + 2 * x_plane;
   const T* g = (const T*)s.g + blockIdx.x * s.stride;
   T* y = (T*)s.y + (int64_t)blockIdx.x * s.rows * s.cols;
   const bool wide = s.rows <= s.cols;
-  for (int i = threadIdx.x; i < (x_plane + a_plane) / 4; i += 1024) ((i32x4*)lds)[i] = i32x4{};  // 2 planes, 8 a store
+  for (int i = threadIdx.x; i < (x_plane + A_PLANE) / 4; i += 1024) ((i32x4*)lds)[i] = i32x4{};  // 2 planes, 8 a store
   __syncthreads();
   // g in runs of four elements of a row, dealt to the threads in turn; its float32 values wait
   // for their scale where X's two parts will be, half in each
   double sum = 0.0;
   {
     const int per_row = (s.cols + 3) / 4, down = 1024 / per_row, along = 1024 % per_row;
-    const int dr = wide ? s.xs : 1, dc = wide ? 1 : s.xs;
+    const int dr = wide ? xs : 1, dc = wide ? 1 : xs;
     int r = threadIdx.x / per_row, c = threadIdx.x % per_row;
-#pragma unroll 4
+#pragma unroll 2
     for (int i = threadIdx.x; i < s.rows * per_row; i += 1024) {
       float v[4];
       load_run(g + (int64_t)r * s.ldg + c * 4, s.cols - c * 4, v);
@@ -493,19 +498,20 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
     __builtin_memcpy(__builtin_assume_aligned(x + x_plane + i * 8, 16), lo, 16);
   }
   __syncthreads();
-  const int tiles = (s.side + 15) / 16, strips = (s.length + 15) / 16, ks = s.high / 32;
   const auto row8 = [](const f16* p) {
     f16x8 v;
     __builtin_memcpy(&v, __builtin_assume_aligned(p, 16), 16);
     return v;
   };
-  const auto product = [](const f16x8 (&n)[2], const f16x8 (&m)[2], f32x4 acc) {  // columns first: a lane has 4 of a row
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(n[0], m[1], acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(n[1], m[0], acc, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(n[0], m[0], acc, 0, 0, 0);
+  const auto pair4 = [](const f16* p, int plane) {  // four values from their parts
+    f16 h[4], l[4];
+    __builtin_memcpy(h, __builtin_assume_aligned(p, 8), 8);
+    __builtin_memcpy(l, __builtin_assume_aligned(p + plane, 8), 8);
+    return f32x4{(float)h[0] + (float)l[0], (float)h[1] + (float)l[1], (float)h[2] + (float)l[2], (float)h[3] + (float)l[3]};
   };
-  // 16 rows from row 16 i and 16 from 16 j of a matrix, multiplied over every `by`-th 32 of n x 32 columns from the k-th on
-  const auto gram = [&](const f16* p, int plane, int ld, int i, int j, int n, int k = 0, int by = 1) {
+  // 16 rows from row 16 i and 16 from 16 j of a matrix, multiplied over every `by`-th 32 of n x 32 columns from the k-th on;
+  // the columns' operand first, so that a lane has 4 adjacent columns of a row
+  const auto gram = [&](const f16* p, int plane, int ld, int i, int j, int n, int k, int by) {
     f32x4 acc = {}, low = {};
     const f16 *pi = p + (16 * i + line) * ld + q * 8 + 32 * k, *pj = p + (16 * j + line) * ld + q * 8 + 32 * k;
 #pragma unroll 2
@@ -517,73 +523,77 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
     }
     return acc + low;
   };
-  // row 16 i + line, columns 16 j + 4 q and three more of a symmetric matrix: those on and above the diagonal, on both sides
+  // row 16 i + line, columns 16 j + 4 q and three more, and the same across the diagonal
   const auto put = [&](int i, int j, const f32x4& v) {
-    const int r = 16 * i + line;
+    const int r = 16 * i + line, c = 16 * j + 4 * q;
+    f16 hi[4], lo[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) split2(v[u], hi[u], lo[u]);
+    __builtin_memcpy(__builtin_assume_aligned(a + r * AS + c, 8), hi, 8);
+    __builtin_memcpy(__builtin_assume_aligned(a + r * AS + c + A_PLANE, 8), lo, 8);
+    if (i == j) return;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int c = 16 * j + 4 * q + u;
-      f16 hi, lo;
-      split2(v[u], hi, lo);
-      if (c >= r) {
-        a[r * s.as + c] = a[c * s.as + r] = hi;
-        a[r * s.as + c + a_plane] = a[c * s.as + r + a_plane] = lo;
-      }
+      a[(c + u) * AS + r] = hi[u];
+      a[(c + u) * AS + r + A_PLANE] = lo[u];
     }
   };
   // the n-th tile on or above the diagonal
   const auto tile_at = [&](int n, int& i, int& j) {
-    for (i = 0; n >= tiles - i; ++i) n -= tiles - i;
+    for (i = 0; n >= TILES - i; ++i) n -= TILES - i;
     j = i + n;
   };
-  const int pairs = tiles * (tiles + 1) / 2, length32 = (s.length + 31) / 32;
-  const int parts = max(1, min(16 / pairs, length32));  // waves of a tile of A
+  const int length32 = (s.length + 31) / 32, strips = (s.length + 15) / 16;
+  const int parts = PAIRS >= 16 ? 1 : max(1, min(16 / PAIRS, length32));  // waves of a tile of A
   for (int step = 0; step < s.steps; ++step) {
     const float ca = s.c[step][0], cb = s.c[step][1], cc = s.c[step][2] / SCALE;
     int i, j;
     if (parts == 1) {  // A
-      for (int n = wave; n < pairs; n += 16) {
+      for (int n = wave; n < PAIRS; n += 16) {
         tile_at(n, i, j);
-        put(i, j, gram(x, x_plane, s.xs, i, j, length32) * (1.f / SCALE));
+        put(i, j, gram(x, x_plane, xs, i, j, length32, 0, 1) * (1.f / SCALE));
       }
     } else {  // every tile by several waves, joined in order; where A will be, the old B is read no more
       f32x4* joined = (f32x4*)a;
-      tile_at(wave % pairs, i, j);
-      if (wave < parts * pairs) joined[wave * 64 + lane] = gram(x, x_plane, s.xs, i, j, length32, wave / pairs, parts);
-      __syncthreads();
-      f32x4 sum = joined[wave % pairs * 64 + lane];
-      for (int t = 1; t < parts; ++t) sum += joined[(wave % pairs + t * pairs) * 64 + lane];
-      __syncthreads();
-      for (int t = threadIdx.x; t < a_plane / 4; t += 1024) ((i32x4*)a)[t] = i32x4{};
-      __syncthreads();
-      if (wave < pairs) put(i, j, sum * (1.f / SCALE));
-    }
-    __syncthreads();
-    f32x4 b[3];  // B, in A's place when everybody has read A: up to 36 tiles
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      const int n = wave + 16 * t;
-      if (n >= pairs) continue;
+      const int n = wave % PAIRS;
       tile_at(n, i, j);
-      b[t] = gram(a, a_plane, s.as, i, j, ks) * cc;
-      const f16* p = a + (16 * i + line) * s.as + 16 * j + 4 * q;
+      if (wave < parts * PAIRS) joined[wave * 64 + lane] = gram(x, x_plane, xs, i, j, length32, wave / PAIRS, parts);
+      __syncthreads();
+      f32x4 all = joined[n * 64 + lane];
+      for (int t = 1; t < parts; ++t) all += joined[(n + t * PAIRS) * 64 + lane];
+      __syncthreads();
+      // a square of 32 whose second half of rows and columns is padding
+      if (TILES * 16 < HIGH)
+        for (int t = threadIdx.x; t < A_PLANE / 4; t += 1024) ((i32x4*)a)[t] = i32x4{};
+      if (TILES * 16 < HIGH) __syncthreads();
+      if (wave < PAIRS) put(i, j, all * (1.f / SCALE));
+    }
+    __syncthreads();
+    f32x4 b[EACH];  // B, in A's place when everybody has read A
 #pragma unroll
-      for (int u = 0; u < 4; ++u) b[t][u] += cb * ((float)p[u] + (float)p[u + a_plane]);
+    for (int t = 0; t < EACH; ++t) {
+      const int n = wave + 16 * t;
+      if (n >= PAIRS) break;
+      tile_at(n, i, j);
+      b[t] = gram(a, A_PLANE, AS, i, j, KS, 0, 1) * cc + pair4(a + (16 * i + line) * AS + 16 * j + 4 * q, A_PLANE) * cb;
     }
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {
+    for (int t = 0; t < EACH; ++t) {
       const int n = wave + 16 * t;
-      if (n >= pairs) continue;
+      if (n >= PAIRS) break;
       tile_at(n, i, j);
       put(i, j, b[t]);
     }
     __syncthreads();
-    // X: 16 columns of it depend on these alone, so a wave replaces them as soon as it has them
+    // X: 16 columns of it depend on these alone, so a wave replaces them as soon as it has them;
+    // rows and columns past the end stay zeros
+    const bool last = step + 1 == s.steps;
     for (int n = wave; n < strips; n += 16) {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
-      f32x4 acc[8] = {};
-      for (int k = 0; k < ks; ++k) {
+      f32x4 acc[TILES] = {};
+#pragma unroll TILES < 8 ? KS : 1  // 128 registers a lane
+      for (int k = 0; k < KS; ++k) {
         f16x8 c[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -591,32 +601,35 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(x + p * x_plane + (k * 32 + q * 8 + (lane >> 2 & 3) + 4 * u) * s.xs + n * 16 +
+                (__attribute__((address_space(3))) s16x4*)(x + p * x_plane + (k * 32 + q * 8 + (lane >> 2 & 3) + 4 * u) * xs + n * 16 +
                                                            (lane & 3) * 4));
           __builtin_memcpy(&c[p], h, 16);
         }
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          if (t >= tiles) break;
-          const f16* p = a + (16 * t + line) * s.as + k * 32 + q * 8;
-          const f16x8 m[2] = {row8(p), row8(p + a_plane)};
-          acc[t] = product(c, m, acc[t]);
+        for (int t = 0; t < TILES; ++t) {
+          const f16* p = a + (16 * t + line) * AS + k * 32 + q * 8;
+          const f16x8 mh = row8(p), ml = row8(p + A_PLANE);
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(c[0], ml, acc[t], 0, 0, 0);
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(c[1], mh, acc[t], 0, 0, 0);
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(c[0], mh, acc[t], 0, 0, 0);
         }
       }
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t >= tiles) break;
+      for (int t = 0; t < TILES; ++t) {
         const int r = 16 * t + line, c = n * 16 + 4 * q;
-        f16* p = x + r * s.xs + c;
+        f16* p = x + r * xs + c;
+        const f32x4 v = pair4(p, x_plane) * ca + acc[t] * (1.f / SCALE);
+        if (!last) {
+          f16 hi[4], lo[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float v = ca * ((float)p[u] + (float)p[u + x_plane]) + acc[t][u] * (1.f / SCALE);
-          if (r < s.side && c + u < s.length) {
-            if (step + 1 < s.steps)
-              split2(v, p[u], p[u + x_plane]);
-            else
-              y[wide ? (int64_t)r * s.cols + c + u : (int64_t)(c + u) * s.cols + r] = (T)(v * (1.f / SCALE));
-          }
+          for (int u = 0; u < 4; ++u) split2(v[u], hi[u], lo[u]);
+          __builtin_memcpy(__builtin_assume_aligned(p, 8), hi, 8);
+          __builtin_memcpy(__builtin_assume_aligned(p + x_plane, 8), lo, 8);
+        } else if (r < (wide ? s.rows : s.cols)) {
+          T* to = y + (wide ? r * s.cols + c : c * s.cols + r);
+#pragma unroll
+          for (int u = 0; u < 4; ++u, to += wide ? 1 : s.cols)
+            if (c + u < s.length) *to = (T)(v[u] * (1.f / SCALE));
         }
       }
     }
@@ -726,26 +739,18 @@ struct OrthoPlan {
   int planes;                                                      // of A and B, and of the products' operands
   size_t off_part, off_x, off_next, off_t, off_next_t, off_a, off_b, bytes;
 };
-NewtonOne one_of(int64_t rows, int64_t cols) {
-  NewtonOne s{};
-  s.rows = (int)rows;
-  s.cols = (int)cols;
-  s.side = (int)std::min(rows, cols);
-  s.length = (int)std::max(rows, cols);
-  s.high = (int)up(s.side, 32);
-  s.xs = (int)up(s.length, 32) + 8;  // 16 bytes more: rows start in different banks
-  s.as = s.high + 8;
-  return s;
-}
+// Rows of 16 that k_one holds the shorter side in, and the stride of X's rows there: 16 bytes more than
+// whole steps, so that rows start in different banks.
+int one_tiles(int64_t side) { return side <= 16 ? 1 : side <= 32 ? 2 : side <= 64 ? 4 : 8; }
+int64_t one_stride(int64_t length) { return up(length, 32) + 8; }
 OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
   OrthoPlan p{};
   p.wide = rows <= cols;
   p.side = std::min(rows, cols);
   p.length = std::max(rows, cols);
-  if (p.side <= 128 && p.length <= 4096) {
-    const NewtonOne s = one_of(rows, cols);
-    const int64_t square = std::max<int64_t>(4 * s.high * s.as, 16 * 1024);  // or a tile of each wave
-    if (4 * (int64_t)s.high * s.xs + square <= ONE_BYTES) {
+  if (p.side <= 128) {
+    const int tiles = one_tiles(p.side);
+    if (4 * one_high(tiles) * one_stride(p.length) + one_square(tiles) <= ONE_BYTES) {
       p.way = ONE;
       return p;
     }
@@ -825,15 +830,15 @@ void launch_ortho(hipStream_t st, const OrthoArgs& a, char* ws) {
   by_type(a.dtype, [&](auto zero) {
     using T = decltype(zero);
     if (p.way == ONE) {
-      NewtonOne s = one_of(a.rows, a.cols);
-      s.g = a.g;
-      s.ldg = a.ldg;
-      s.stride = a.stride;
-      s.steps = a.steps;
-      s.eps = a.eps;
-      s.y = a.y;
+      NewtonOne s{a.g,     a.ldg, a.stride, (int)a.rows, (int)a.cols, (int)p.length, (int)one_stride(p.length),
+                  a.steps, a.eps, a.y,      {}};
       for (int i = 0; i < 3 * a.steps; ++i) s.c[i / 3][i % 3] = (float)a.coefficients[i];
-      k_one<T><<<dim3((unsigned)a.batch), 1024, 0, st>>>(s);
+      const dim3 grid((unsigned)a.batch);
+      const int tiles = one_tiles(p.side);
+      if (tiles == 1) k_one<T, 1><<<grid, 1024, 0, st>>>(s);
+      if (tiles == 2) k_one<T, 2><<<grid, 1024, 0, st>>>(s);
+      if (tiles == 4) k_one<T, 4><<<grid, 1024, 0, st>>>(s);
+      if (tiles == 8) k_one<T, 8><<<grid, 1024, 0, st>>>(s);
       return;
     }
     double* part = (double*)(ws + p.off_part);
