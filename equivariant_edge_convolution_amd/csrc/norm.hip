@@ -6,8 +6,8 @@
 //   q = e4m3(y / scale).
 //   backward, with a = gy w and xhat = s rstd:
 //   gx = rstd (a - xhat mean(a xhat)) + gsum,   gw = sum_rows gy xhat.
-//   rows in 8 bits without a norm: scale = max(max|x|, 2^-100) / most (127 for integers,
-//   448 for e4m3), q = round(x / scale).
+//   rows in 8 bits without a norm: scale = max(max|x|, 2^-100) (1 / most) (most 127 for
+//   integers, 448 for e4m3), q = round(x / scale).
 //
 // All of them are bound by memory: a row is read once into registers, its sums
 // are taken there, and what is written is written from there.  A row belongs to
@@ -410,7 +410,7 @@ __device__ __forceinline__ void divide_run(float (&v)[N], float scale, float inv
 template <typename Q>
 __device__ __forceinline__ float scale_of(float amax) {
   if (!(amax <= 3.4028235e38f)) return __builtin_nanf("");  // a NaN or an infinity in the row
-  return (amax < AMAX_FLOOR ? AMAX_FLOOR : amax) / Code<Q>::MOST;
+  return (amax < AMAX_FLOOR ? AMAX_FLOOR : amax) * (1.f / Code<Q>::MOST);
 }
 
 struct QuantizeRows {

@@ -42,6 +42,11 @@ struct NewtonEpilogue {
   NewtonTo rows, turned;
   Y* y;  // [M][N] instead of rows.to
   int64_t y_batch, a_batch, b_batch;
+  // Split over k (grid.z): sums [split][matrix][part_ld][part_ld], joined by k_join_newton, instead of all of the
+  // above; or NULL.
+  float* part;
+  int64_t part_ld;
+  bool k_along;  // k along memory, in both operands
 };
 
 template <typename Y, bool SYM, bool TURN>
@@ -56,6 +61,17 @@ __device__ __forceinline__ void of_batch(Product& g, NewtonEpilogue<Y, SYM, TURN
   next(e.rows);
   if constexpr (TURN) next(e.turned);
   if constexpr (!std::is_same<Y, Planes>::value) e.y += i * e.y_batch;
+  if constexpr (SYM) {
+    if (e.part) {
+      e.part += ((int64_t)blockIdx.z * gridDim.y + i) * e.part_ld * e.part_ld;
+      const int64_t first = blockIdx.z * g.k_split;
+      const bool kc = e.k_along;
+      g.a = (const f16*)g.a + (kc ? first : first * g.lda);
+      g.b = (const f16*)g.b + (kc ? first : first * g.ldb);
+      g.K = min(g.k_split, g.K - first);
+      g.k_split = g.K;
+    }
+  }
 }
 
 // Symmetric: the tiles that reach above the diagonal, row of tiles after row of tiles.
@@ -237,7 +253,20 @@ __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, ch
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = i + PER < GROUPS ? acc[i + PER < GROUPS ? i + PER : 0][j] : Acc{};
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    finish_sums<PER * HIGH>(e, lds, m0 + g * HIGH, n0);
+    const int64_t top = m0 + g * HIGH;
+    if (SYM && e.part) {
+      if (n0 + 63 >= top) {  // below the diagonal nobody reads them
+#pragma unroll 1
+        for (int r = threadIdx.x >> 4 & 3; r < PER * HIGH; r += 4) {
+          f32x4 v;
+          const int c = threadIdx.x & 15;
+          __builtin_memcpy(&v, __builtin_assume_aligned(lds + (r * 256 + (c ^ (r & 15)) * 16), 16), 16);
+          __builtin_memcpy(__builtin_assume_aligned(e.part + (top + r) * e.part_ld + n0 + c * 4, 16), &v, 16);
+        }
+      }
+    } else {
+      finish_sums<PER * HIGH>(e, lds, top, n0);
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
@@ -322,6 +351,10 @@ template <typename E>
 constexpr bool SYM_OR_TURN = false;
 template <typename Y, bool SYM, bool TURN>
 constexpr bool SYM_OR_TURN<NewtonEpilogue<Y, SYM, TURN>> = SYM || TURN;
+template <typename E>
+constexpr bool SYM_OF = false;
+template <typename Y, bool SYM, bool TURN>
+constexpr bool SYM_OF<NewtonEpilogue<Y, SYM, TURN>> = SYM;
 
 template <int P, typename E>
 __global__ void __launch_bounds__(512) k_small(Product g, E e) {
@@ -412,11 +445,53 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
   __builtin_memcpy(v, __builtin_assume_aligned(second, 16), 32);
   u[0] += v[0];
   u[1] += v[1];
+  if constexpr (SYM_OF<E>) {
+    if (e.part) {
+      const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;  // 16-byte chunks c and c + 1, as put_sums permutes them
+      float* to = e.part + (m0 + r) * e.part_ld + n0;
+      __builtin_memcpy(__builtin_assume_aligned(to + (c ^ (r & 15)) * 4, 16), &u[0], 16);
+      __builtin_memcpy(__builtin_assume_aligned(to + ((c + 1) ^ (r & 15)) * 4, 16), &u[1], 16);
+      return;
+    }
+  }
   __builtin_memcpy(__builtin_assume_aligned(first, 16), u, 32);
   __syncthreads();
   const char* sums = TWO && row >= 32 ? a1 - 8192 : a0;
   rows.finish(e, sums, row + (lane >> 3));
   if constexpr (SYM_OR_TURN<E>) turned.finish(e, sums, row);
+#endif
+}
+
+// Adds the splits of a symmetric product in order and finishes it: a block of 64 x 64 on or above the
+// diagonal a workgroup.
+template <typename E>
+__global__ void __launch_bounds__(512) k_join_newton(E e, int splits, int64_t split_stride) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __attribute__((aligned(16))) char sums[16384];
+  const int64_t i = blockIdx.y;
+  e.rows.to += i * e.rows.to_batch;
+  e.part += i * e.part_ld * e.part_ld;
+  const Place place = place_of<64, 64>(e);
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2, row = wave_id() * 8;
+  const float* from = e.part + (place.m + r) * e.part_ld + place.n + c * 4;
+  f32x4 v[2] = {};
+  for (int s0 = 0; s0 < splits; s0 += 4) {  // four splits on their way
+    f32x4 t[4][2] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (s0 + s < splits) __builtin_memcpy(t[s], __builtin_assume_aligned(from + (s0 + s) * split_stride, 16), 32);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[0] += t[s][0], v[1] += t[s][1];
+  }
+  put_sums(sums, r, c, v[0]);
+  put_sums(sums, r, c + 1, v[1]);
+  __syncthreads();
+  RowRuns<1> rows;
+  TurnedRuns<1> turned;
+  rows.load(e, place.m, place.n, row + (threadIdx.x >> 3 & 7));
+  turned.load(e, place.m, place.n, row);
+  rows.finish(e, sums, row + (threadIdx.x >> 3 & 7));
+  turned.finish(e, sums, row);
 #endif
 }
 
@@ -737,7 +812,10 @@ struct OrthoPlan {
   bool wide;
   int64_t side, length, ldx, ldt, lds, x_plane, t_plane, ab_plane;  // elements
   int planes;                                                      // of A and B, and of the products' operands
-  size_t off_part, off_x, off_next, off_t, off_next_t, off_a, off_b, bytes;
+  int splits;        // of A = X X^T over k
+  int64_t k_split;   // a multiple of 64
+  int64_t split_ld;  // of their sums
+  size_t off_part, off_x, off_next, off_t, off_next_t, off_a, off_b, off_split, bytes;
 };
 // Rows of 16 that k_one holds the shorter side in, and the stride of X's rows there: 16 bytes more than
 // whole steps, so that rows start in different banks.
@@ -767,6 +845,22 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
     p.ldt = up(rows, 128);
     p.t_plane = cols * p.ldt;
   }
+  // A of few tiles and a long sum is split where that gains: us of a step of 32 k, of a workgroup's begin and end, and of
+  // the join with its 4 TB/s (16 x 5616 float32, 6 steps: %SPLIT%).
+  const bool small = p.way == SMALL_TILES, two = p.planes == 2;
+  const int64_t tiles = batch * (small ? newton_tiles<64, 64>(p.side, p.side, true)
+                                 : two ? newton_tiles<256, 128>(p.side, p.side, true)
+                                       : newton_tiles<128, 128>(p.side, p.side, true));
+  const double step = small ? (two ? 0.36 : 0.22) : two ? 0.7 : 0.25, fixed = small ? 4 : 10;
+  p.split_ld = up(p.side, 256);
+  double best = 1e30;
+  for (int s = 1; s <= 64 && (s == 1 || p.length / s >= 512) && tiles * s <= 1024 * (s == 1 ? tiles : 1); s = s < 8 ? s + 1 : s * 2) {
+    const double bytes = 4.0 * batch * p.side * p.side * s;
+    const double us = (double)((tiles * s + 255) / 256) * (p.length / 32.0 / s * step + fixed) + (s > 1 ? 6 + bytes / 4e6 : 0);
+    if (us < best) best = us, p.splits = s;
+  }
+  p.k_split = up((p.length + p.splits - 1) / p.splits, 64);
+  p.splits = (int)((p.length + p.k_split - 1) / p.k_split);
   size_t at = 0;
   const auto take = [&](size_t& off, int64_t elements, int size) {
     off = at;
@@ -779,37 +873,38 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
   take(p.off_next_t, 2 * p.t_plane, 2);
   take(p.off_a, p.planes * p.ab_plane, 2);
   take(p.off_b, p.planes * p.ab_plane, 2);
+  take(p.off_split, p.splits > 1 ? p.splits * p.split_ld * p.split_ld : 0, 4);
   p.bytes = at;
   return p;
 }
 
 // One product on large tiles.
 template <bool A_KC, bool B_KC, typename Y, bool SYM>
-void large_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue<Y, SYM>& e, int planes) {
+void large_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue<Y, SYM>& e, int planes, unsigned splits = 1) {
   using E = NewtonEpilogue<Y, SYM>;
   // only bf16 takes one plane
   if constexpr (std::is_same<Y, float>::value || std::is_same<Y, f16>::value || std::is_same<Y, Planes>::value) {
     if (planes == 2) {
-      const dim3 grid((unsigned)newton_tiles<256, 128>(e.M, e.N, SYM), (unsigned)batch);
+      const dim3 grid((unsigned)newton_tiles<256, 128>(e.M, e.N, SYM), (unsigned)batch, splits);
       k_pairs<A_KC, B_KC, E><<<grid, 512, 0, st>>>(g, e);
       return;
     }
   }
   if constexpr (std::is_same<Y, bf16>::value || std::is_same<Y, Planes>::value) {
     const int64_t t256 = newton_tiles<256, 256>(e.M, e.N, SYM), t128 = newton_tiles<128, 128>(e.M, e.N, SYM);
-    const double steps = (double)g.K / 32;  // as plan_product
-    const double us128 = (double)((t128 * batch + 255) / 256) * (10 + 0.25 * steps);
-    const double us256 = (double)((t256 * batch + 255) / 256) * (20 + 0.49 * steps);
+    const double steps = (double)g.K / 32 / splits;  // as plan_product
+    const double us128 = (double)((t128 * batch * splits + 255) / 256) * (10 + 0.25 * steps);
+    const double us256 = (double)((t256 * batch * splits + 255) / 256) * (20 + 0.49 * steps);
     if (us256 < us128)
-      k_tiled<f16, float, A_KC, B_KC, 2, 4, 8, 4, false, E><<<dim3((unsigned)t256, (unsigned)batch), 512, 0, st>>>(g, e);
+      k_tiled<f16, float, A_KC, B_KC, 2, 4, 8, 4, false, E><<<dim3((unsigned)t256, (unsigned)batch, splits), 512, 0, st>>>(g, e);
     else
-      k_tiled<f16, float, A_KC, B_KC, 2, 2, 4, 8, false, E><<<dim3((unsigned)t128, (unsigned)batch), 256, 0, st>>>(g, e);
+      k_tiled<f16, float, A_KC, B_KC, 2, 2, 4, 8, false, E><<<dim3((unsigned)t128, (unsigned)batch, splits), 256, 0, st>>>(g, e);
   }
 }
 template <typename Y, bool SYM, bool TURN>
-void small_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue<Y, SYM, TURN>& e, int planes) {
+void small_product(hipStream_t st, int64_t batch, const Product& g, const NewtonEpilogue<Y, SYM, TURN>& e, int planes, unsigned splits = 1) {
   using E = NewtonEpilogue<Y, SYM, TURN>;
-  const dim3 grid((unsigned)newton_tiles<64, 64>(e.M, e.N, SYM), (unsigned)batch);
+  const dim3 grid((unsigned)newton_tiles<64, 64>(e.M, e.N, SYM), (unsigned)batch, splits);
   if constexpr (std::is_same<Y, bf16>::value || std::is_same<Y, Planes>::value) {
     if (planes == 1) {
       k_small<1, E><<<grid, 512, 0, st>>>(g, e);
@@ -866,13 +961,22 @@ void launch_ortho(hipStream_t st, const OrthoArgs& a, char* ws) {
       e.a_batch = e.b_batch = by_rows ? x_batch : t_batch;
       const f16* of = by_rows ? x : xt;
       const int64_t ld = by_rows ? p.ldx : p.ldt, plane = by_rows ? xp : tp;
-      const Product gram{of, of, ld, ld, p.side, p.side, p.length, p.length, plane, plane};
+      const Product gram{of, of, ld, ld, p.side, p.side, p.length, p.k_split, plane, plane};
+      const unsigned splits = (unsigned)p.splits;
+      e.part = splits > 1 ? (float*)(ws + p.off_split) : nullptr;
+      e.part_ld = p.split_ld;
+      e.k_along = small || p.wide;
       if (small)
-        small_product(st, a.batch, gram, e, p.planes);
+        small_product(st, a.batch, gram, e, p.planes, splits);
       else if (p.wide)
-        large_product<true, true>(st, a.batch, gram, e, p.planes);
+        large_product<true, true>(st, a.batch, gram, e, p.planes, splits);
       else
-        large_product<false, false>(st, a.batch, gram, e, p.planes);
+        large_product<false, false>(st, a.batch, gram, e, p.planes, splits);
+      if (splits > 1) {
+        const dim3 grid((unsigned)newton_tiles<64, 64>(p.side, p.side, true), (unsigned)a.batch);
+        k_join_newton<<<grid, 512, 0, st>>>(e, p.splits, a.batch * p.split_ld * p.split_ld);
+        e.part = nullptr;
+      }
       // B = b A + c A A
       const Product square{A, A, p.lds, p.lds, p.side, p.side, p.side, p.side, ap, ap};
       e.alpha = (float)c[1];

@@ -452,9 +452,9 @@ EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t w
 
 /* eec_quantize_rows -- rows in 8 bits, as eec_linear takes them: tokens (rows of x) and
  * channels (rows of w) alike.  Per row of `width` (>= 1) elements
- *   scale = max(max_j |x_j|, 2^-100) / 127 (EEC_I8) or / 448 (EEC_E4M3),
+ *   scale = max(max_j |x_j|, 2^-100) times 1/127 (EEC_I8) or 1/448 (EEC_E4M3),
  *   y_j   = x_j / scale, rounded to the nearest code (to even);
- * scale and quotient are float32, each correctly rounded.
+ * the factor, scale and the quotient are float32, each correctly rounded.
  *   dtype   EEC_F32, EEC_F16 or EEC_BF16: the type of x
  *   codes   EEC_I8 (codes -127 to 127) or EEC_E4M3: the type of y
  *   y       [rows][width], scale [rows] float32

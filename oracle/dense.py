@@ -97,9 +97,9 @@ def gated_backward(gy, x, w, z, act_name="silu"):
 
 
 def quantize_i8(x):
-    """Codes and float32 scales of float32 rows: quotients rounded to float32 as scales are, then to the nearest integer."""
+    """Codes and float32 scales of float32 rows: quotients rounded to float32, as scales and 1 / 127 are, then to the nearest integer."""
     x = x.astype(np.float32)
-    scale = np.maximum(np.abs(x).max(axis=1), np.float32(AMAX_FLOOR)) / np.float32(I8_MAX)
+    scale = np.maximum(np.abs(x).max(axis=1), np.float32(AMAX_FLOOR)) * (np.float32(1) / np.float32(I8_MAX))
     return np.rint(x / scale[:, None]).astype(np.int8), scale
 
 

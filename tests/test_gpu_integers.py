@@ -23,7 +23,7 @@ WIDTHS = [(1, 1), (3, 7), (5, 64), (2, 513), (7, 1000), (130, 512), (3, 2047), (
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
 @pytest.mark.parametrize("rows,width", WIDTHS)
 def test_quantized_rows(rows, width, dt):
-    """Codes and scales are those of correctly rounded float32 divisions, bit for bit."""
+    """Codes and scales are those of the float32 arithmetic that the header states, bit for bit."""
     g = torch.Generator().manual_seed(rows * 7919 + width)
     for pad, size in ((0, 1.0), (3, 1e-4), (8, 300.0)):
         x = view(rand(g, rows, width, dtype=dt, scale=size), pad, 1 if pad else 0)
@@ -37,7 +37,7 @@ def test_quantized_rows(rows, width, dt):
         assert np.array_equal(np_(out["y"]), q)
         # e4m3: half a step of the code around the quotient, 2^-4 of it or 2^-10 below its normal range
         eight = B.quantize_rows(x, E4M3)
-        scale = np.maximum(np.abs(x.cpu().float().numpy()).max(axis=1), np.float32(2.0 ** -100)) / np.float32(448)
+        scale = np.maximum(np.abs(x.cpu().float().numpy()).max(axis=1), np.float32(2.0 ** -100)) * (np.float32(1) / np.float32(448))
         assert np.array_equal(np_(eight["scale"]), scale)
         v = f64(x) / scale.astype(np.float64)[:, None]
         within(eight["y"].float(), v, np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10) + 2 * EPS * np.abs(v), "e4m3")
@@ -49,7 +49,7 @@ def test_quotients_of_every_size():
     rows = []
     for p in list(range(-149, 128, 5)) + [127, -100, -99, -81, -80, -79, -74, -73]:
         amax = np.float32(1.9) * np.float32(2.0) ** np.float32(p) if p > -149 else np.float32(2.0 ** -149)
-        scale = np.maximum(amax, np.float32(2.0 ** -100)) / np.float32(127)
+        scale = np.maximum(amax, np.float32(2.0 ** -100)) * (np.float32(1) / np.float32(127))
         halves = (r.integers(-127, 127, 500) + 0.5).astype(np.float32) * scale
         near = np.nextafter(halves, r.choice([-np.inf, np.inf], 500).astype(np.float32), dtype=np.float32)
         x = np.concatenate([[amax], halves, near, r.uniform(-1, 1, 23).astype(np.float32) * amax]).astype(np.float32)
@@ -69,7 +69,7 @@ def test_empty_and_special_rows(width):
     # 1e-35 is 0.0016 of the least scale of integers, 0.0057 of that of e4m3, whose smallest codes are multiples of 2^-9
     for codes, most, small in ((torch.int8, 127, 0.0), (E4M3, 448, 3 * 2.0 ** -9)):
         out = B.quantize_rows(x, codes)
-        scale, y, least = np_(out["scale"]), out["y"].float().cpu().numpy(), np.float32(2.0 ** -100) / np.float32(most)
+        scale, y, least = np_(out["scale"]), out["y"].float().cpu().numpy(), np.float32(2.0 ** -100) * (np.float32(1) / np.float32(most))
         assert scale[0] == least and np.all(y[0] == 0.0) and scale[3] == least and np.all(y[3] == small)
         for bad in (1, 2, 4):
             assert np.isnan(scale[bad]) and np.all(y[bad] == 0.0 if codes == torch.int8 else np.isnan(y[bad]))

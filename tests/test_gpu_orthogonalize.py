@@ -89,6 +89,18 @@ def test_large_updates(batch, rows, cols, dt):
 
 
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("batch,rows,cols", [(1, 53, 5616), (1, 9000, 16), (2, 200, 6001), (1, 260, 20001), (1, 20001, 260), (1, 1, 70000), (70, 20, 300)])
+def test_long_updates(batch, rows, cols, dt):
+    """Few tiles of long sums, which are split and joined; many small matrices."""
+    gen = torch.Generator().manual_seed(rows)
+    g = torch.stack([update(gen, rows, cols, dt) for _ in range(batch)])
+    y = B.orthogonalize(g)
+    check(y[-1], g[-1], dt)
+    assert torch.equal(B.orthogonalize(g[0]), y[0]) or batch > 1  # how a sum is split goes by the batch
+    check(y[0], g[0], dt)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
 def test_normal_and_steep_updates(dt):
     """Singular values close together, and over many decades."""
     g = torch.Generator().manual_seed(3)

@@ -33,7 +33,7 @@ def test_gated_known_values():
 def test_integer_codes():
     q, scale = D.quantize_i8(np.array([[0.0, 0.0], [254.0, -1.0], [-63.5, 1.25], [1e-3, 5e-4]]))
     assert q.dtype == np.int8 and scale.dtype == np.float32
-    assert q[0].tolist() == [0, 0] and scale[0] == np.float32(2.0 ** -100) / np.float32(127)
+    assert q[0].tolist() == [0, 0] and scale[0] == np.float32(2.0 ** -100) * (np.float32(1) / np.float32(127))
     assert q[1].tolist() == [127, 0] and scale[1] == 2.0   # -0.5 goes to the even 0
     assert q[2].tolist() == [-127, 2] and scale[2] == 0.5  # 2.5 goes to the even 2
     assert q[3].tolist() == [127, 64]                      # 63.5 goes to the even 64
