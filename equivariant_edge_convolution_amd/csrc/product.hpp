@@ -1018,12 +1018,33 @@ __global__ void __launch_bounds__(512) k_parted(Product g, Epilogue e) {
 
 // ------------------------------------------------------------------ few rows
 
+// BYTES bytes of memory at any address, by whole dwords of it: a load of 16 bytes whose address is
+// not a multiple of 4 takes several times as long (30 x 3299 -> 6600 bf16 48 us, 30 x 3300 19).
+// Loaded now, put together (v_alignbyte) when they are used.
+template <int BYTES>
+struct Words {
+  uint32_t w[BYTES / 4 + 1];
+  uint32_t shift;
+  __device__ __forceinline__ void load(const void* p) {
+    shift = (uint32_t)(uintptr_t)p & 3;
+    const char* at = (const char*)p - shift;
+    __builtin_memcpy(w, __builtin_assume_aligned(at, 4), BYTES);
+    // the last dword holds some of the bytes, or is read twice: never one without any
+    __builtin_memcpy(&w[BYTES / 4], __builtin_assume_aligned(at + (shift ? BYTES : BYTES - 4), 4), 4);
+  }
+  __device__ __forceinline__ void get(uint32_t (&v)[BYTES / 4]) const {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) v[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], shift);
+  }
+};
+
 // Up to 16 MT rows of x against 16 columns (rows of w) per workgroup: w goes from
 // memory straight into the first factor of the matrix instruction, once, x (a few
 // rows, in the L2) into the second.  The 8 waves deal runs of 128 bytes of k in
 // turn and are joined in LDS, in wave order, so one launch does it all.
 // Gated: 8 rows of the gate and the same 8 of the value, which meet after the join.
-template <typename T, typename O, int MT, bool G = false>
+// ODD: rows whose addresses are not multiples of 4 bytes.
+template <typename T, typename O, int MT, bool G = false, bool ODD = false>
 __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   using M_ = Mat<T>;
   constexpr int WAVES = 8, P = M_::PLANES;
@@ -1049,6 +1070,27 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   // multiplies the s-th 8 (the same k of both operands meet, which is all a sum asks).
   struct Run {
     Raw<T> v[STEPS];
+  };
+  static_assert(sizeof(Run) == 32, "a run of a lane");
+  struct Loaded {  // a run as it comes from memory
+    std::conditional_t<ODD, Words<32>, Run> is;
+    __device__ __forceinline__ void load(const T* p) {
+      if constexpr (ODD)
+        is.load(p);
+      else
+        __builtin_memcpy(&is, p, 32);
+    }
+    __device__ __forceinline__ Run get() const {
+      if constexpr (ODD) {
+        uint32_t v[8];
+        is.get(v);
+        Run r;
+        __builtin_memcpy(&r, v, 32);
+        return r;
+      } else {
+        return is;
+      }
+    }
   };
   auto parts = [](const Raw<T>& r, typename M_::Frag (&f)[P]) {
     if constexpr (P == 3) {
@@ -1076,24 +1118,33 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   const int own = q * STEPS * 8;
   int64_t c = wave;
   for (; c + WAVES * (TOGETHER - 1) < full; c += WAVES * TOGETHER) {
-    Run wr[TOGETHER], xr[TOGETHER][MT];
+    Loaded wl[TOGETHER], xl[TOGETHER][MT];
 #pragma unroll
     for (int i = 0; i < TOGETHER; ++i) {
       const int64_t k = (c + WAVES * i) * CHUNK + own;
-      __builtin_memcpy(&wr[i], w + k, sizeof(Run));
+      wl[i].load(w + k);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) __builtin_memcpy(&xr[i][t], x[t] + k, sizeof(Run));
+      for (int t = 0; t < MT; ++t) xl[i][t].load(x[t] + k);
     }
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) product(wr[i], xr[i]);
+    for (int i = 0; i < TOGETHER; ++i) {
+      Run xr[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) xr[t] = xl[i][t].get();
+      product(wl[i].get(), xr);
+    }
   }
   for (; c * CHUNK < g.K; c += WAVES) {
     Run wr, xr[MT];
     const int64_t k = c * CHUNK + own, left = g.K - k;
     if (c < full) {
-      __builtin_memcpy(&wr, w + k, sizeof(Run));
+      Loaded wl, xl[MT];
+      wl.load(w + k);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) __builtin_memcpy(&xr[t], x[t] + k, sizeof(Run));
+      for (int t = 0; t < MT; ++t) xl[t].load(x[t] + k);
+      wr = wl.get();
+#pragma unroll
+      for (int t = 0; t < MT; ++t) xr[t] = xl[t].get();
     } else {
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
@@ -1156,7 +1207,16 @@ __global__ void __launch_bounds__(256) k_pack(Packings all) {
     for (uint32_t i = threadIdx.x; i < total; i += 256) {
       const int64_t row = r0 + i / chunks, col = (int64_t)(i % chunks) * V;
       T v[V];
-      load_raw((const T*)p.from + row * p.ld + col, row < p.rows ? p.cols - col : 0, v);
+      const T* from = (const T*)p.from + row * p.ld + col;
+      if (sizeof(T) < 4 && row < p.rows && p.cols - col >= V) {
+        Words<V * (int)sizeof(T)> words;
+        uint32_t u[V * sizeof(T) / 4];
+        words.load(from);
+        words.get(u);
+        __builtin_memcpy(v, u, sizeof(v));
+      } else {
+        load_raw(from, row < p.rows ? p.cols - col : 0, v);
+      }
       if constexpr (std::is_same<T, float>::value) {
         bf16 q[3][V];
 #pragma unroll
@@ -1341,8 +1401,13 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   }
   if constexpr (A_KC && B_KC) {
     const dim3 columns((unsigned)(G ? (g.N + 7) / 8 : (g.N + 15) / 16));
-    if (p.kind == FEW && g.M <= 16) k_few<T, O, 1, G><<<columns, 512, 0, st>>>(g, e);
-    if (p.kind == FEW && g.M > 16) k_few<T, O, 2, G><<<columns, 512, 0, st>>>(g, e);
+    const bool odd = (((uintptr_t)g.a | (uintptr_t)g.b | (uint64_t)(g.lda | g.ldb) * sizeof(T)) & 3) != 0;
+    if constexpr (sizeof(T) < 4) {
+      if (p.kind == FEW && odd && g.M <= 16) k_few<T, O, 1, G, true><<<columns, 512, 0, st>>>(g, e);
+      if (p.kind == FEW && odd && g.M > 16) k_few<T, O, 2, G, true><<<columns, 512, 0, st>>>(g, e);
+    }
+    if (p.kind == FEW && !odd && g.M <= 16) k_few<T, O, 1, G><<<columns, 512, 0, st>>>(g, e);
+    if (p.kind == FEW && !odd && g.M > 16) k_few<T, O, 2, G><<<columns, 512, 0, st>>>(g, e);
   }
   if (p.kind == GENERAL) k_product<T, O, A_KC, B_KC, 2, 2, 4, G><<<grid, 256, 0, st>>>(g, e);
   if (p.kind == SMALL) k_product<T, O, A_KC, B_KC, 4, 1, 1, G><<<grid, 256, 0, st>>>(g, e);
