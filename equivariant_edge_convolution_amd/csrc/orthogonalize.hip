@@ -271,20 +271,24 @@ __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, ch
   }
 }
 
-// Products of two planes each, 256 x 128 of C per workgroup and 64 x 64 per wave, as k_parted:
-// a step is 32 k of all four planes, 48 KB of LDS, and does lo hi, hi lo and hi hi; three
-// buffers, so that two steps' loads run under the present one's 48 products a wave.
-template <bool A_KC, bool B_KC, typename E>
-__global__ void __launch_bounds__(512) k_pairs(Product g, E e) {
+// Products of two planes each, BM x 128 of C per workgroup and 64 x 64 per wave, as k_parted: a
+// step is 32 k of all four planes, 48 KB of LDS (32 KB at 128 x 128), and does lo hi, hi lo and
+// hi hi; three (four) buffers, so that two (three) steps' loads run under the present one's 48
+// products a wave (float32 2048 x 4096: X's product 103 us, 1.0 PFLOP/s of float16).
+template <bool A_KC, bool B_KC, int BM, typename E>
+__global__ void __launch_bounds__(2 * BM) k_pairs(Product g, E e) {
 #ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
   of_batch(g, e);
-  using TA = Tile<f16, A_KC, 256, 8>;
-  using TB = Tile<f16, B_KC, 128, 8>;
+  constexpr int WAVES = BM / 32, BUFS = BM == 256 ? 3 : 4;
+  using TA = Tile<f16, A_KC, BM, WAVES>;
+  using TB = Tile<f16, B_KC, 128, WAVES>;
   constexpr int LOADS = 2 * (TA::LOADS + TB::LOADS);
+  constexpr int A3 = BUFS == 4 ? 2 * TA::BYTES : 16, B3 = BUFS == 4 ? 2 * TB::BYTES : 16;
   __shared__ __attribute__((aligned(1024))) char a0[2 * TA::BYTES], a1[2 * TA::BYTES], a2[2 * TA::BYTES];
   __shared__ __attribute__((aligned(1024))) char b0[2 * TB::BYTES], b1[2 * TB::BYTES], b2[2 * TB::BYTES];
+  __shared__ __attribute__((aligned(16))) char a3[A3], b3[B3];
   const int wave = wave_id();
-  const Place place = place_of<256, 128>(e);
+  const Place place = place_of<BM, 128>(e);
   const int64_t m0 = place.m, n0 = place.n;
   const int wm = wave / 2 * 64, wn = wave % 2 * 64;
   f32x4 acc[4][4] = {};
@@ -321,22 +325,34 @@ __global__ void __launch_bounds__(512) k_pairs(Product g, E e) {
     }
   };
   int left = (int)g.K;
+// Of a group of BUFS steps, those past the end are zeros.
+#define EEC_STEP(T, A, B, FREE_A, FREE_B)                  \
+  tile_barrier<(BUFS - 2) * LOADS>();                      \
+  load(FREE_A, FREE_B, left - (T + BUFS - 1) * TA::BK);    \
+  step(A, B)
   load(a0, b0, left);
   load(a1, b1, left - TA::BK);
-  for (; left > 0; left -= 3 * TA::BK) {  // three steps, of which those past the end are zeros
-    tile_barrier<LOADS>();
-    load(a2, b2, left - 2 * TA::BK);
-    step(a0, b0);
-    tile_barrier<LOADS>();
-    load(a0, b0, left - 3 * TA::BK);
-    step(a1, b1);
-    tile_barrier<LOADS>();
-    load(a1, b1, left - 4 * TA::BK);
-    step(a2, b2);
+  if constexpr (BUFS == 4) load(a2, b2, left - 2 * TA::BK);
+  for (; left > 0; left -= BUFS * TA::BK) {
+    if constexpr (BUFS == 4) {
+      EEC_STEP(0, a0, b0, a3, b3);
+      EEC_STEP(1, a1, b1, a0, b0);
+      EEC_STEP(2, a2, b2, a1, b1);
+      EEC_STEP(3, a3, b3, a2, b2);
+    } else {
+      EEC_STEP(0, a0, b0, a2, b2);
+      EEC_STEP(1, a1, b1, a0, b0);
+      EEC_STEP(2, a2, b2, a1, b1);
+    }
   }
+#undef EEC_STEP
   tile_barrier<0>();
-  // 64 rows of sums in 16 KB for each wave: two in an A buffer, one in a B buffer
-  char* mine = wave < 2 ? a0 + wave * 16384 : wave < 4 ? a1 + (wave - 2) * 16384 : wave < 6 ? a2 + (wave - 4) * 16384 : wave == 6 ? b0 : b1;
+  // 64 rows of sums in 16 KB for each wave: an A buffer holds one or two, a B buffer one
+  char* mine;
+  if constexpr (BUFS == 4)
+    mine = wave == 0 ? a0 : wave == 1 ? a1 : wave == 2 ? a2 : a3;
+  else
+    mine = wave < 2 ? a0 + wave * 16384 : wave < 4 ? a1 + (wave - 2) * 16384 : wave < 6 ? a2 + (wave - 4) * 16384 : wave == 6 ? b0 : b1;
   finish<false, float, 16, 4>(e, mine, m0 + wm, n0 + wn, 0, acc);
 #endif
 }
@@ -723,14 +739,44 @@ __global__ void __launch_bounds__(256) k_square_sums(const T* __restrict__ g, in
   constexpr int V = VEC<T>;
   __shared__ double join[4];
   const T* p = g + blockIdx.y * stride;
-  const int64_t per_row = (cols + V - 1) / V, total = rows * per_row;
+  // runs of 16 bytes dealt to the threads in turn, four at a time on their way
+  const uint32_t per_row = (uint32_t)((cols + V - 1) / V), all = gridDim.x * 256, first = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t down = all / per_row, along = all % per_row;
+  int64_t r = first / per_row;
+  uint32_t c = first % per_row;
   double sum = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / per_row, c = i % per_row * V;
-    float v[V];
-    load_run(p + r * ldg + c, cols - c, v);
+  const auto next = [&] {
+    r += down, c += along;
+    if (c >= per_row) c -= per_row, ++r;
+  };
+  if (cols >= V) {
+    while (r < rows) {
+      // no branch, so that all four are on their way: a run past the row's end starts earlier, and one past the last row
+      // is the last run again; what they read twice counts once
+      T v[4][V];
+      int from[4];
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum += (double)v[j] * v[j];
+      for (int t = 0; t < 4; ++t) {
+        const int64_t at = (int64_t)c * V, there = min(at, cols - V);
+        from[t] = r < rows ? (int)(at - there) : V;
+        __builtin_memcpy(v[t], p + min(r, rows - 1) * ldg + there, 16);
+        next();
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float u = j >= from[t] ? (float)v[t][j] : 0.f;
+          sum += (double)u * u;
+        }
+    }
+  } else {
+    for (; r < rows; next()) {
+      float v[V];
+      load_run(p + r * ldg, cols, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum += (double)v[j] * v[j];
+    }
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
@@ -804,6 +850,14 @@ __global__ void __launch_bounds__(256) k_scaled(Scaling s) {
 
 // ------------------------------------------------------------------ host
 
+// us of products of pairs on 256 x 128 tiles and on half of these: a round of the 256 CUs for every step of 32 k, and
+// for a tile's begin and end (float32 2048 x 4096, A A: 72 wide tiles 85 us, 136
+// of the others 62).
+double pairs_us(int64_t tiles, int64_t K, bool wide) {
+  return (double)((tiles + 255) / 256) * (wide ? 30 + 0.8 * K / 32 : 15 + 0.75 * K / 32);
+}
+bool wide_pairs(int64_t t256, int64_t t128, int64_t K) { return pairs_us(t256, K, true) <= pairs_us(t128, K, false); }
+
 // How a call is run, and its workspace: partial sums, X and the next X (two planes each; with
 // small tiles their transposes too), A and B.
 enum Way { ONE, SMALL_TILES, LARGE_TILES };
@@ -845,18 +899,20 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
     p.ldt = up(rows, 128);
     p.t_plane = cols * p.ldt;
   }
-  // A of few tiles and a long sum is split where that gains: us of a step of 32 k, of a workgroup's begin and end, and of
-  // the join with its 4 TB/s (16 x 5616 float32, 6 steps: %SPLIT%).
+  // The sum of A's tiles is split where that gains: us of a step of 32 k, of a tile's begin and end, and of the join
+  // with its 5 TB/s (53 x 5616 float16, six steps: %SPLIT%).
   const bool small = p.way == SMALL_TILES, two = p.planes == 2;
-  const int64_t tiles = batch * (small ? newton_tiles<64, 64>(p.side, p.side, true)
-                                 : two ? newton_tiles<256, 128>(p.side, p.side, true)
-                                       : newton_tiles<128, 128>(p.side, p.side, true));
-  const double step = small ? (two ? 0.36 : 0.22) : two ? 0.7 : 0.25, fixed = small ? 4 : 10;
+  const int64_t t64 = batch * newton_tiles<64, 64>(p.side, p.side, true), t128 = batch * newton_tiles<128, 128>(p.side, p.side, true);
+  const int64_t t256 = batch * newton_tiles<256, 128>(p.side, p.side, true);
+  const auto product_us = [&](int64_t s) {
+    const int64_t K = p.length / s;
+    if (!small && two) return std::min(pairs_us(t256 * s, K, true), pairs_us(t128 * s, K, false));
+    return (double)(((small ? t64 : t128) * s + 255) / 256) * (small ? 4 + (two ? 0.36 : 0.22) * K / 32 : 10 + 0.25 * K / 32);
+  };
   p.split_ld = up(p.side, 256);
   double best = 1e30;
-  for (int s = 1; s <= 64 && (s == 1 || p.length / s >= 512) && tiles * s <= 1024 * (s == 1 ? tiles : 1); s = s < 8 ? s + 1 : s * 2) {
-    const double bytes = 4.0 * batch * p.side * p.side * s;
-    const double us = (double)((tiles * s + 255) / 256) * (p.length / 32.0 / s * step + fixed) + (s > 1 ? 6 + bytes / 4e6 : 0);
+  for (int s = 1; s == 1 || (s <= 64 && p.length / s >= 512 && t64 * s <= 8192); s = s < 8 ? s + 1 : s * 2) {
+    const double us = product_us(s) + (s > 1 ? 9 + 2.0 * batch * p.side * p.side * s / 5e6 : 0);
     if (us < best) best = us, p.splits = s;
   }
   p.k_split = up((p.length + p.splits - 1) / p.splits, 64);
@@ -885,8 +941,11 @@ void large_product(hipStream_t st, int64_t batch, const Product& g, const Newton
   // only bf16 takes one plane
   if constexpr (std::is_same<Y, float>::value || std::is_same<Y, f16>::value || std::is_same<Y, Planes>::value) {
     if (planes == 2) {
-      const dim3 grid((unsigned)newton_tiles<256, 128>(e.M, e.N, SYM), (unsigned)batch, splits);
-      k_pairs<A_KC, B_KC, E><<<grid, 512, 0, st>>>(g, e);
+      const int64_t t256 = newton_tiles<256, 128>(e.M, e.N, SYM), t128 = newton_tiles<128, 128>(e.M, e.N, SYM);
+      if (wide_pairs(t256 * batch * splits, t128 * batch * splits, g.K / splits))
+        k_pairs<A_KC, B_KC, 256, E><<<dim3((unsigned)t256, (unsigned)batch, splits), 512, 0, st>>>(g, e);
+      else
+        k_pairs<A_KC, B_KC, 128, E><<<dim3((unsigned)t128, (unsigned)batch, splits), 256, 0, st>>>(g, e);
       return;
     }
   }
