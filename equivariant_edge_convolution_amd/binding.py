@@ -182,6 +182,15 @@ def _raw_stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _on(device: torch.device, fn, *args) -> int:
+    """fn(stream, *args) on the current stream of the tensors' device, with that device current (the null stream is
+    the current device's, whichever that is)."""
+    if torch._C._cuda_getDevice() == device.index:
+        return fn(_raw_stream(device), *args)
+    with torch.cuda.device(device):
+        return fn(_raw_stream(device), *args)
+
+
 @dataclass
 class Model:
     """Model weights resident on the device (float32, contiguous)."""
@@ -524,9 +533,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: 
         scale = out["scale"] = torch.empty(rows, dtype=torch.float32, device=dev)
     if save_rstd:
         rstd = out["rstd"] = torch.empty(rows, dtype=torch.float32, device=dev)
-    _check(lib().eec_add_rms_norm(_raw_stream(dev), rows, n, DTYPES[dt], x.data_ptr(), ldx, _address(residual), ldr, w,
-                                  float(eps), _address(total), y.data_ptr(), _address(scale), _address(rstd)),
-           "add_rms_norm")
+    _check(_on(dev, lib().eec_add_rms_norm, rows, n, DTYPES[dt], x.data_ptr(), ldx, _address(residual), ldr, w,
+               float(eps), _address(total), y.data_ptr(), _address(scale), _address(rstd)), "add_rms_norm")
     return out
 
 
@@ -549,9 +557,8 @@ def add_rms_norm_backward(gy: torch.Tensor, sum: torch.Tensor, weight: torch.Ten
         if workspace is None:
             workspace = _workspace(lib().eec_add_rms_norm_backward_workspace_bytes(rows, n), dev)
             ws, size = workspace.data_ptr(), workspace.numel()
-    _check(lib().eec_add_rms_norm_backward(_raw_stream(dev), rows, n, DTYPES[dt], gy.data_ptr(), ldgy, sum.data_ptr(),
-                                           lds, w, rs, _address(gsum), ldgs, gx.data_ptr(), _address(gw), ws, size),
-           "add_rms_norm_backward")
+    _check(_on(dev, lib().eec_add_rms_norm_backward, rows, n, DTYPES[dt], gy.data_ptr(), ldgy, sum.data_ptr(), lds, w,
+               rs, _address(gsum), ldgs, gx.data_ptr(), _address(gw), ws, size), "add_rms_norm_backward")
     return dict(gx=gx, gweight=gw)
 
 
@@ -564,8 +571,8 @@ def quantize_rows(x: torch.Tensor, dtype: torch.dtype = torch.int8) -> dict:
     ldx = _matrix(x, "x", rows, n, dt, dev)
     y = torch.empty((rows, n), dtype=dtype, device=dev)
     scale = torch.empty(rows, dtype=torch.float32, device=dev)
-    _check(lib().eec_quantize_rows(_raw_stream(dev), rows, n, DTYPES[dt], DTYPES[dtype], x.data_ptr(), ldx, y.data_ptr(),
-                                   scale.data_ptr()), "quantize_rows")
+    _check(_on(dev, lib().eec_quantize_rows, rows, n, DTYPES[dt], DTYPES[dtype], x.data_ptr(), ldx, y.data_ptr(),
+               scale.data_ptr()), "quantize_rows")
     return dict(y=y, scale=scale)
 
 
@@ -598,9 +605,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None, a
     elif need := _linear_workspace(rows, n, k, dt, ot):
         workspace = _workspace(need, dev)
         ws, size = workspace.data_ptr(), need
-    _check(lib().eec_linear(_raw_stream(dev), rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(),
-                            ldw, wsc, b, _address(residual), ldr, ACTS[act], y.data_ptr(), _address(out.get("preact")),
-                            ws, size), "linear")
+    _check(_on(dev, lib().eec_linear, rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, wsc, b,
+               _address(residual), ldr, ACTS[act], y.data_ptr(), _address(out.get("preact")), ws, size), "linear")
     return out
 
 
@@ -626,9 +632,9 @@ def linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: 
     if workspace is None:
         workspace = _workspace(lib().eec_linear_backward_workspace_bytes(rows, n, k, DTYPES[dt], ACTS[act]), dev)
     ws, size = _given(workspace, dev)
-    _check(lib().eec_linear_backward(_raw_stream(dev), rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
-                                     x.data_ptr(), ldx, w.data_ptr(), ldw, _address(preact), gx.data_ptr(),
-                                     gw.data_ptr(), _address(gb), ws, size), "linear_backward")
+    _check(_on(dev, lib().eec_linear_backward, rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy, x.data_ptr(),
+               ldx, w.data_ptr(), ldw, _address(preact), gx.data_ptr(), gw.data_ptr(), _address(gb), ws, size),
+               "linear_backward")
     return dict(gx=gx, gw=gw, gbias=gb)
 
 
@@ -678,8 +684,8 @@ def gated_linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = N
     elif need := _gated_workspace(rows, n, k, dt, ot):
         workspace = _workspace(need, dev)
         ws, size = workspace.data_ptr(), need
-    _check(lib().eec_gated_linear(_raw_stream(dev), rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, wsc, b,
-                                  ACTS[act], y.data_ptr(), _address(out.get("preact")), ws, size), "gated_linear")
+    _check(_on(dev, lib().eec_gated_linear, rows, n, k, dt, ot, x.data_ptr(), ldx, xs, w.data_ptr(), ldw, wsc, b,
+               ACTS[act], y.data_ptr(), _address(out.get("preact")), ws, size), "gated_linear")
     return out
 
 
@@ -702,9 +708,9 @@ def gated_linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pr
     if workspace is None:
         workspace = _workspace(_gated_backward_workspace(rows, n, k, DTYPES[dt]), dev)
     ws, size = _given(workspace, dev)
-    _check(lib().eec_gated_linear_backward(_raw_stream(dev), rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
-                                           x.data_ptr(), ldx, w.data_ptr(), ldw, preact.data_ptr(), gx.data_ptr(),
-                                           gw.data_ptr(), _address(gb), ws, size), "gated_linear_backward")
+    _check(_on(dev, lib().eec_gated_linear_backward, rows, n, k, DTYPES[dt], ACTS[act], gy.data_ptr(), ldgy,
+               x.data_ptr(), ldx, w.data_ptr(), ldw, preact.data_ptr(), gx.data_ptr(), gw.data_ptr(), _address(gb),
+               ws, size), "gated_linear_backward")
     return dict(gx=gx, gw=gw, gbias=gb)
 
 
@@ -728,8 +734,8 @@ def _orthogonalize_workspace(batch: int, rows: int, cols: int, dtype: int) -> in
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7,
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """eec_orthogonalize of a matrix, or of each of a batch [batch][rows][cols] (any
-    strides of rows and matrices that do not overlap).  ``coefficients``: (a, b, c)
-    of every step, or a tuple of one for each."""
+    strides of rows and matrices).  ``coefficients``: (a, b, c) of every step, or
+    a tuple of one for each."""
     if g.dim() not in (2, 3) or g.dtype not in DTYPES or not g.is_cuda:
         raise ValueError("g must be a device matrix, or a batch of them, of float32, float16 or bfloat16")
     batch, (rows, cols) = 1 if g.dim() == 2 else g.shape[0], g.shape[-2:]
@@ -738,16 +744,14 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ, e
         raise ValueError("the columns of g must be adjacent")
     ldg = g.stride(-2) if rows > 1 else cols
     stride = g.stride(0) if batch > 1 and g.dim() == 3 else 0
-    # what a list holds is not hashable
-    each = coefficients if isinstance(coefficients, tuple) else tuple(
-        v if isinstance(v, (int, float)) else tuple(v) for v in coefficients)
+    each = tuple(v if isinstance(v, (int, float)) else tuple(v) for v in coefficients)
     c = _coefficients(int(steps), each)
     y = torch.empty(g.shape, dtype=g.dtype, device=dev)
     if workspace is None:
         workspace = _workspace(_orthogonalize_workspace(batch, rows, cols, dt), dev)
     ws, size = _given(workspace, dev)
-    _check(lib().eec_orthogonalize(_raw_stream(dev), batch, rows, cols, dt, g.data_ptr(), ldg, stride, int(steps), c,
-                                   float(eps), y.data_ptr(), ws, size), "orthogonalize")
+    _check(_on(dev, lib().eec_orthogonalize, batch, rows, cols, dt, g.data_ptr(), ldg, stride, int(steps), c,
+               float(eps), y.data_ptr(), ws, size), "orthogonalize")
     return y
 
 

@@ -854,9 +854,8 @@ eec_status eec_orthogonalize(void* stream, int64_t batch, int64_t rows, int64_t 
   const bool none = batch == 0 || rows == 0 || cols == 0;
   if (!none) {
     TRY(check_matrix(g, rows, cols, ldg, dtype, "g"));
-    // one matrix after another: strides between them that would make them overlap are refused
-    if (batch > 1 && (stride < (rows - 1) * ldg + cols || stride > (int64_t(1) << 48)))
-      return fail(EEC_ERR_SHAPE, "bad stride of the matrices");
+    // matrices may interleave, or be one: they are only read
+    if (batch > 1 && (stride < 0 || stride > int64_t(1) << 48)) return fail(EEC_ERR_SHAPE, "bad stride of the matrices");
   }
   TRY(check_matrix(y, all, cols, cols, dtype, "y"));
   TRY(check_ws(workspace, workspace_bytes, ortho_workspace(batch, rows, cols, dtype)));

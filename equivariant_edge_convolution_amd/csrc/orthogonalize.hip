@@ -8,13 +8,13 @@
 //
 // Numbers.  Everything is held 2^12 times its value in float16 planes: X as hi + lo (22 bits),
 // so that a X carries no rounding of 11 bits from step to step, where small singular values
-// grow 3.4-fold each.  The products take hi alone for 16-bit types, where their error, 1e-3 to
-// 2e-3 of the result in norm, is of the output's own size (bf16 operands: 1e-2 for normal g,
-// up to 0.3 where a few directions dominate; without lo 4e-2 there), and hi hi + hi lo + lo hi
-// for float32, as exact as float32 products (2e-7 to 1e-5, those 1e-6 to 2e-5).  B is
-// computed from A as rounded: the errors of b A and c A^2 then cancel at singular values near 1.
-// Singular values stay below 3.5 (checked on the host), so 2^12 of them fit float16, and
-// elements down to 2^-26 of the largest possible keep 11 bits.
+// grow 3.4-fold each.  Two planes: hi hi + hi lo + lo hi in every product, as exact as float32
+// products (2e-7 to 1e-5 off in norm, those 1e-6 to 2e-5).  One plane, for large bf16 updates:
+// hi alone in the products, 1e-3 to 2e-3 off, which is the output's own size (bf16 operands: 1e-2
+// for normal g, up to 0.3 where a few directions dominate; float16 ones without X's lo 4e-2
+// there).  B is computed from A as rounded: the errors of b A and c A^2 then cancel at singular
+// values near 1.  These stay below 3.5 (checked on the host), so that 2^12 of them fit float16;
+// elements of X keep 11 bits in hi down to 2^-26, and are held to 2^-37.
 #include "product.hpp"
 
 namespace eec {
@@ -889,6 +889,8 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
   }
   // large tiles where they fill the chip
   p.way = batch * tiles_of(p.side, p.length, 128) >= 200 ? LARGE_TILES : SMALL_TILES;
+  // one plane where its error is of the output's size: 2.1e-3 to 2.5e-3 with the output's rounding below a side of 256, where
+  // two cost little (small products wait for memory), 1.9e-3 to 2.1e-3 above; a float16 output would show it eightfold
   p.planes = dtype != EEC_BF16 || p.side < 256 ? 2 : 1;
   if (p.planes == 2 && dtype == EEC_BF16) p.way = SMALL_TILES;
   p.ldx = up(cols, 128);

@@ -549,8 +549,8 @@ EEC_API size_t eec_gated_linear_backward_workspace_bytes(int64_t rows, int64_t o
  *   X = g / (|g| + eps)  (|g| the root of the sum of squares),  then for each step
  *   A = X X^T,  X <- a X + (b A + c A^2) X
  * (rows <= cols; otherwise A = X^T X and X <- a X + X (b A + c A^2), the same result).
- *   g       [batch][rows][cols] dtype: matrices `stride` elements apart (>= their
- *           extent; unread for batch 1), rows `ldg`
+ *   g       [batch][rows][cols] dtype: matrices `stride` elements apart (>= 0: they may
+ *           interleave, or be the same; unread for batch 1), rows `ldg`
  *   coefficients [host][steps][3]: a, b, c of each step; read before the call
  *           returns.  Refused where they take singular values of [0, 1] beyond 3.5 or
  *           b s^2 + c s^4 beyond 15 on the way
@@ -558,10 +558,12 @@ EEC_API size_t eec_gated_linear_backward_workspace_bytes(int64_t rows, int64_t o
  *   y       [batch][rows][cols] dtype
  *   batch <= 65535, the longer side <= 2^20, the shorter <= 2^15
  *   workspace >= eec_orthogonalize_workspace_bytes(batch, rows, cols, dtype)
- * The norm is summed in float64 (no update is too large or too small for it); X is held
- * to 22 bits and products are summed in float32.  EEC_F32: products of 22-bit operands, as exact as
- * float32 arithmetic.  16-bit types: operands of the products rounded to 11 bits, 1e-3
- * to 2e-3 off in norm before y is rounded.
+ * The norm is summed in float64 (no update is too large or too small for it).  X is held
+ * to 22 bits (and to 2^-37), products are summed in float32.  EEC_F32, EEC_F16, and EEC_BF16
+ * where the shorter side is below 256: products of 22-bit operands, as exact as
+ * float32 arithmetic.  EEC_BF16 otherwise: operands of the products rounded to 11 bits, 1e-3
+ * to 2e-3 off in norm before y is rounded.  How the sums are ordered goes by the sizes and
+ * by batch, so a matrix on its own and in a batch may differ in last bits.
  * A NaN or an infinity in g makes all of its matrix NaN; a matrix of zeros stays one. */
 EEC_API eec_status eec_orthogonalize(void *stream, int64_t batch, int64_t rows, int64_t cols, int32_t dtype,
                              const void *g, int64_t ldg, int64_t stride, int32_t steps,

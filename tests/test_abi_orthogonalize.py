@@ -31,7 +31,7 @@ def ortho(batch=2, rows=64, cols=48, dtype=F32, g=P(1), ldg=48, stride=64 * 48, 
     (lambda: ortho(eps=0.0), "EEC_ERR_SHAPE"), (lambda: ortho(eps=-1.0), "EEC_ERR_SHAPE"), (lambda: ortho(eps=float("nan")), "EEC_ERR_SHAPE"),
     (lambda: ortho(eps=float("inf")), "EEC_ERR_SHAPE"),
     (lambda: ortho(g=None), "EEC_ERR_NULL"), (lambda: ortho(y=None), "EEC_ERR_NULL"),
-    (lambda: ortho(ldg=47), "EEC_ERR_SHAPE"), (lambda: ortho(stride=64 * 48 - 1), "EEC_ERR_SHAPE"), (lambda: ortho(stride=-64 * 48), "EEC_ERR_SHAPE"),
+    (lambda: ortho(ldg=47), "EEC_ERR_SHAPE"), (lambda: ortho(stride=-64 * 48), "EEC_ERR_SHAPE"),
     (lambda: ortho(g=ctypes.c_void_p((1 << 32) + 2)), "EEC_ERR_SHAPE"),
     (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, ws=None), "EEC_ERR_WORKSPACE"),
     (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, size=1024), "EEC_ERR_WORKSPACE"),
@@ -46,7 +46,10 @@ def ortho(batch=2, rows=64, cols=48, dtype=F32, g=P(1), ldg=48, stride=64 * 48, 
     # 1 goes to 1.98 and to 1.97, 0.376 to 1.99 and 2.08, which these take to 7
     (lambda: ortho(y=P(1), steps=3, coef=(8.28, -23.6, 17.3, 4.1, -2.95, 0.55, 1.875, -1.25, 0.375)), "EEC_ERR_SHAPE"),
     (lambda: ortho(y=P(1), steps=1, coef=(3.5, 0.0, 0.0)), "EEC_ERR_ALIAS"),
-    (lambda: ortho(batch=1, stride=0, y=P(1)), "EEC_ERR_ALIAS"),
+    (lambda: ortho(batch=1, stride=0, y=P(1)), "EEC_ERR_ALIAS"), (lambda: ortho(stride=48, ldg=96, y=P(1)), "EEC_ERR_ALIAS"),
+    (lambda: ortho(stride=0, y=P(1)), "EEC_ERR_ALIAS"),
+    # y in the rows of the last of two interleaved matrices
+    (lambda: ortho(stride=48, ldg=96, y=ctypes.c_void_p((1 << 32) + 4 * (48 + 63 * 96 + 47))), "EEC_ERR_ALIAS"),
 ])
 def test_refusals(call, status):
     assert call() == status
