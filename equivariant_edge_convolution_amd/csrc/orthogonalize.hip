@@ -37,6 +37,8 @@ struct NewtonTo {
 // `turned` as well (SYM: into C's own lower half, without TURN).
 template <typename Y, bool SYM, bool TURN = false>
 struct NewtonEpilogue {
+  static constexpr bool SYMMETRIC = SYM, ACROSS = SYM || TURN, IN_PLANES = std::is_same<Y, Planes>::value;
+  __device__ __forceinline__ const NewtonTo& across() const { return TURN ? turned : rows; }
   int64_t M, N;  // of the product
   float alpha, beta;
   NewtonTo rows, turned;
@@ -60,7 +62,7 @@ __device__ __forceinline__ void of_batch(Product& g, NewtonEpilogue<Y, SYM, TURN
   };
   next(e.rows);
   if constexpr (TURN) next(e.turned);
-  if constexpr (!std::is_same<Y, Planes>::value) e.y += i * e.y_batch;
+  if constexpr (!NewtonEpilogue<Y, SYM, TURN>::IN_PLANES) e.y += i * e.y_batch;
   if constexpr (SYM) {
     if (e.part) {
       e.part += ((int64_t)blockIdx.z * gridDim.y + i) * e.part_ld * e.part_ld;
@@ -107,19 +109,17 @@ __device__ __forceinline__ void split2(float v, f16& hi, f16& lo) {
   lo = (f16)(v - (float)hi);
 }
 
-// Eight adjacent elements of one row, from a multiple of 8 on, of which `left` exist (0: nothing
-// to do).  Planes have rows of whole runs, whose end is kept at zero, so that each run is one store.
+// What alpha multiplies of eight adjacent elements of one row, from a multiple of 8 on; zeros where there is none.
 struct Run8 {
-  int64_t m, n, left;
-  f16 hi[8], lo[8];  // what alpha multiplies, or zeros
+  f16 hi[8], lo[8];
   // `at`: elements from (row m0, column n0), both uniform, where the wave's sums start.  No branch, so that nothing
   // waits for these loads before their use; what does not exist is read past every buffer, as zero.
-  __device__ __forceinline__ void load(const NewtonTo& s, int64_t m0, int64_t n0, uint32_t at) {
+  __device__ __forceinline__ void load(const NewtonTo& s, int64_t m0, int64_t n0, uint32_t at, bool exists) {
     constexpr uint32_t NOWHERE = 0x80000000u;
     const f16* p = s.from + m0 * s.ld + n0;
     const auto part = [&](const f16* from, bool is, f16 (&v)[8]) {
       const auto q = __builtin_amdgcn_raw_buffer_load_b128(
-          __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0x7fffffff, 0x00020000), is && left > 0 ? at * 2 : NOWHERE, 0, 0);
+          __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0x7fffffff, 0x00020000), is && exists ? at * 2 : NOWHERE, 0, 0);
       __builtin_memcpy(v, &q, 16);
     };
     part(p, s.from != nullptr, hi);
@@ -129,15 +129,16 @@ struct Run8 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = alpha * ((float)hi[i] + (float)lo[i]) + beta * v[i];
   }
-  __device__ __forceinline__ void store(const NewtonTo& s, const float (&v)[8]) const {
-    f16 h[8], l[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) split2(i < left ? v[i] : 0.f, h[i], l[i]);
-    f16* p = s.to + m * s.ld + n;
-    __builtin_memcpy(__builtin_assume_aligned(p, 16), h, 16);
-    if (s.to_plane) __builtin_memcpy(__builtin_assume_aligned(p + s.to_plane, 16), l, 16);
-  }
 };
+// Rows of planes are whole runs, whose end (all but `left` of the last) is kept at zero, so that each run is one store.
+__device__ __forceinline__ void store_planes(const NewtonTo& s, int64_t m, int64_t n, int64_t left, const float (&v)[8]) {
+  f16 h[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split2(i < left ? v[i] : 0.f, h[i], l[i]);
+  f16* p = s.to + m * s.ld + n;
+  __builtin_memcpy(__builtin_assume_aligned(p, 16), h, 16);
+  if (s.to_plane) __builtin_memcpy(__builtin_assume_aligned(p + s.to_plane, 16), l, 16);
+}
 
 __device__ __forceinline__ float sum_at(const char* lds, int r, int c) {
   float v;
@@ -148,102 +149,95 @@ __device__ __forceinline__ float sum_at(const char* lds, int r, int c) {
 // Finishing a wave's sums, row by row of 256 bytes (64 columns) in its LDS as put_sums leaves them.
 // Symmetric: 8 x 8 blocks on and above the diagonal are stored, and those above it once more
 // across it, from columns of the same sums; a block on the diagonal takes its lower half from its
-// upper one.  So each element is written once, by one lane, and C is symmetric to the bit.  What
-// N runs a lane need from memory is loaded before any of them is stored.
+// upper one.  So each element is written once, by one lane, and C is symmetric to the bit.
 //
-// 8 columns of rows r, r + 8, ... of a lane, r that of its eighth of the wave.
+// N rows a lane, 8 columns each: rows r + 8 i of the wave's, r its eighth's.
 template <int N>
 struct RowRuns {
   Run8 run[N];
-  template <typename Y, bool SYM, bool TURN>
-  __device__ __forceinline__ void load(const NewtonEpilogue<Y, SYM, TURN>& e, int64_t top, int64_t n0, int r) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      run[i].m = top + r + i * 8;
-      run[i].n = n0 + (threadIdx.x & 7) * 8;
-      run[i].left = run[i].m < e.M && !(SYM && run[i].n + 7 < run[i].m) ? e.N - run[i].n : 0;
-      run[i].load(e.rows, top, n0, (uint32_t)((r + i * 8) * (int)e.rows.ld + (threadIdx.x & 7) * 8));
-    }
+  template <typename E>
+  static __device__ __forceinline__ int64_t left(const E& e, int64_t m, int64_t n) {
+    return m < e.M && !(E::SYMMETRIC && n + 7 < m) ? e.N - n : 0;
   }
-  template <typename Y, bool SYM, bool TURN>
-  __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int r) const {
+  template <typename E>
+  __device__ __forceinline__ void load(const E& e, int64_t top, int64_t n0, int r) {
     const int col = (threadIdx.x & 7) * 8;
 #pragma unroll
+    for (int i = 0; i < N; ++i, r += 8)
+      run[i].load(e.rows, top, n0, (uint32_t)(r * (int)e.rows.ld + col), left(e, top + r, n0 + col) > 0);
+  }
+  // `lds`: the sums of row `from` on.
+  template <typename E>
+  __device__ __forceinline__ void finish(const E& e, const char* lds, int64_t top, int64_t n0, int r, int from) const {
+    const int col = (threadIdx.x & 7) * 8;
+    const int64_t n = n0 + col;
+#pragma unroll
     for (int i = 0; i < N; ++i, r += 8) {
-      if (run[i].left <= 0) continue;
+      const int64_t m = top + r, some = left(e, m, n);
+      if (some <= 0) continue;
+      const int at = r - from;
       float v[8];
 #pragma unroll
       for (int u = 0; u < 8; u += 4)
-        __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (r * 256 + (((col + u) / 4) ^ (r & 15)) * 16), 16), 16);
-      if (SYM && run[i].n < run[i].m) {
+        __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (at * 256 + (((col + u) / 4) ^ (at & 15)) * 16), 16), 16);
+      if (E::SYMMETRIC && n < m) {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (run[i].n + u < run[i].m) v[u] = sum_at(lds, (r & ~7) + u, col + (r & 7));
+          if (n + u < m) v[u] = sum_at(lds, (at & ~7) + u, col + (at & 7));
       }
       run[i].value(e.alpha, e.beta, v);
-      if constexpr (std::is_same<Y, Planes>::value) {
-        run[i].store(e.rows, v);
+      if constexpr (E::IN_PLANES) {
+        store_planes(e.rows, m, n, some, v);
       } else {
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] *= 1.f / SCALE;
-        store_run(e.y + run[i].m * e.N + run[i].n, run[i].left, v);
+        store_run(e.y + m * e.N + n, some, v);
       }
     }
   }
 };
-// Row n0 + lane of the transpose: rows r to r + 8 N - 1 of this side.
+// Row n0 + lane of the transpose: rows r to r + 8 N - 1 of the wave's.
 template <int N>
 struct TurnedRuns {
   Run8 run[N];
-  template <typename Y, bool SYM, bool TURN>
-  static __device__ __forceinline__ const NewtonTo& to(const NewtonEpilogue<Y, SYM, TURN>& e) { return TURN ? e.turned : e.rows; }
-  template <typename Y, bool SYM, bool TURN>
-  __device__ __forceinline__ void load(const NewtonEpilogue<Y, SYM, TURN>& e, int64_t top, int64_t n0, int r) {
-    const int64_t m = n0 + (threadIdx.x & 63);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      run[i].m = m;
-      run[i].n = top + r + i * 8;
-      run[i].left = m < e.N && !(SYM && run[i].n + 7 >= m) ? e.M - run[i].n : 0;  // symmetric: blocks above the diagonal
-      run[i].load(to(e), n0, top, (uint32_t)((threadIdx.x & 63) * (int)to(e).ld + r + i * 8));
-    }
+  template <typename E>
+  static __device__ __forceinline__ int64_t left(const E& e, int64_t m, int64_t n) {  // symmetric: blocks above the diagonal
+    return m < e.N && !(E::SYMMETRIC && n + 7 >= m) ? e.M - n : 0;
   }
-  template <typename Y, bool SYM, bool TURN>
-  __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int r) const {
+  template <typename E>
+  __device__ __forceinline__ void load(const E& e, int64_t top, int64_t n0, int r) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < N; ++i, r += 8)
+      run[i].load(e.across(), n0, top, (uint32_t)(lane * (int)e.across().ld + r), left(e, n0 + lane, top + r) > 0);
+  }
+  template <typename E>
+  __device__ __forceinline__ void finish(const E& e, const char* lds, int64_t top, int64_t n0, int r, int from) const {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < N; ++i, r += 8) {
-      if (run[i].left <= 0) continue;
+      const int64_t m = n0 + lane, n = top + r, some = left(e, m, n);
+      if (some <= 0) continue;
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = sum_at(lds, r + u, threadIdx.x & 63);
+      for (int u = 0; u < 8; ++u) v[u] = sum_at(lds, r - from + u, lane);
       run[i].value(e.alpha, e.beta, v);
-      run[i].store(to(e), v);
+      store_planes(e.across(), m, n, some, v);
     }
   }
 };
-template <int ROWS, typename Y, bool SYM, bool TURN>
-__device__ __forceinline__ void finish_sums(const NewtonEpilogue<Y, SYM, TURN>& e, const char* lds, int64_t top, int64_t n0) {
-  constexpr int N = ROWS < 32 ? ROWS / 8 : 4;
-  static_assert(ROWS % (8 * N) == 0, "whole batches");
-#pragma unroll 1
-  for (int r = 0; r < ROWS; r += 8 * N) {
-    RowRuns<N> rows;
-    rows.load(e, top, n0, r + (threadIdx.x >> 3 & 7));
-    rows.finish(e, lds, r + (threadIdx.x >> 3 & 7));
-  }
-  if constexpr (SYM || TURN) {
-#pragma unroll 1
-    for (int r = 0; r < ROWS; r += 8 * N) {
-      TurnedRuns<N> turned;
-      turned.load(e, top, n0, r);
-      turned.finish(e, lds, r);
-    }
-  }
-}
-// As finish_wave.
+// As finish_wave: what a batch of rows needs from memory is loaded before any of it is stored, and where registers are
+// left (not in symmetric products, which finish two blocks at a time) before the stores of the batch ahead of it.
 template <bool G, typename O, int HIGH, int PER, typename Y, bool SYM, bool TURN, typename Acc, int GROUPS, int NB>
 __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, char* lds, int64_t m0, int64_t n0, int,
                                        Acc (&acc)[GROUPS][NB]) {
+  static_assert(!TURN, "large tiles have no transposes");
+  constexpr int ROWS = PER * HIGH;
+  static_assert(ROWS % 32 == 0, "whole batches");
+  const int r0 = threadIdx.x >> 3 & 7;
+  const bool whole = SYM && e.part;
+  RowRuns<4> next;
+  if constexpr (!SYM) next.load(e, m0, n0, r0);
 #pragma unroll 1
   for (int g = 0; g < GROUPS; g += PER) {
 #pragma unroll
@@ -253,19 +247,33 @@ __device__ __forceinline__ void finish(const NewtonEpilogue<Y, SYM, TURN>& e, ch
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = i + PER < GROUPS ? acc[i + PER < GROUPS ? i + PER : 0][j] : Acc{};
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int64_t top = m0 + g * HIGH;
-    if (SYM && e.part) {
-      if (n0 + 63 >= top) {  // below the diagonal nobody reads them
+    const int from = g * HIGH;
+    if (whole) {
+      if (n0 + 63 >= m0 + from) {  // below the diagonal nobody reads them
 #pragma unroll 1
-        for (int r = threadIdx.x >> 4 & 3; r < PER * HIGH; r += 4) {
+        for (int r = threadIdx.x >> 4 & 3; r < ROWS; r += 4) {
           f32x4 v;
           const int c = threadIdx.x & 15;
           __builtin_memcpy(&v, __builtin_assume_aligned(lds + (r * 256 + (c ^ (r & 15)) * 16), 16), 16);
-          __builtin_memcpy(__builtin_assume_aligned(e.part + (top + r) * e.part_ld + n0 + c * 4, 16), &v, 16);
+          __builtin_memcpy(__builtin_assume_aligned(e.part + (m0 + from + r) * e.part_ld + n0 + c * 4, 16), &v, 16);
         }
       }
     } else {
-      finish_sums<PER * HIGH>(e, lds, top, n0);
+#pragma unroll 1
+      for (int r = from; r < from + ROWS; r += SYM ? 16 : 32) {
+        if constexpr (SYM) {
+          RowRuns<2> rows;
+          TurnedRuns<2> turned;
+          rows.load(e, m0, n0, r + r0);
+          turned.load(e, m0, n0, r);
+          rows.finish(e, lds, m0, n0, r + r0, from);
+          turned.finish(e, lds, m0, n0, r, from);
+        } else {
+          const RowRuns<4> rows = next;
+          if (r + 32 < GROUPS * HIGH) next.load(e, m0, n0, r + 32 + r0);
+          rows.finish(e, lds, m0, n0, r + r0, from);
+        }
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
@@ -362,16 +370,8 @@ __global__ void __launch_bounds__(2 * BM) k_pairs(Product g, E e) {
 // 64 x 64 of C per workgroup, P planes, both operands with k along memory: for products whose
 // large tiles would leave most CUs idle.  A step is 64 k of all planes, both halves of its
 // operands' cache lines, four waves (32 x 32 each) for each half, joined in LDS at the end; three
-// steps are on their way at a time, and what the epilogue reads is loaded before them (%SMALL%).
-template <typename E>
-constexpr bool SYM_OR_TURN = false;
-template <typename Y, bool SYM, bool TURN>
-constexpr bool SYM_OR_TURN<NewtonEpilogue<Y, SYM, TURN>> = SYM || TURN;
-template <typename E>
-constexpr bool SYM_OF = false;
-template <typename Y, bool SYM, bool TURN>
-constexpr bool SYM_OF<NewtonEpilogue<Y, SYM, TURN>> = SYM;
-
+// steps are on their way at a time, and what the epilogue reads is loaded before them (771 x 1025 float32: 13 us for A,
+// 11 for A A and 12 for X's product, of which a launch and a tile's begin and end take 4).
 template <int P, typename E>
 __global__ void __launch_bounds__(512) k_small(Product g, E e) {
 #ifdef __HIP_DEVICE_COMPILE__  // see k_tiled
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
   RowRuns<1> rows;
   TurnedRuns<1> turned;
   rows.load(e, m0, n0, row + (lane >> 3));
-  if constexpr (SYM_OR_TURN<E>) turned.load(e, m0, n0, row);
+  if constexpr (E::ACROSS) turned.load(e, m0, n0, row);
   int left = (int)g.K;
   load(a0, left);
   load(a1, left - 64);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
   __builtin_memcpy(v, __builtin_assume_aligned(second, 16), 32);
   u[0] += v[0];
   u[1] += v[1];
-  if constexpr (SYM_OF<E>) {
+  if constexpr (E::SYMMETRIC) {
     if (e.part) {
       const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;  // 16-byte chunks c and c + 1, as put_sums permutes them
       float* to = e.part + (m0 + r) * e.part_ld + n0;
@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
   __builtin_memcpy(__builtin_assume_aligned(first, 16), u, 32);
   __syncthreads();
   const char* sums = TWO && row >= 32 ? a1 - 8192 : a0;
-  rows.finish(e, sums, row + (lane >> 3));
-  if constexpr (SYM_OR_TURN<E>) turned.finish(e, sums, row);
+  rows.finish(e, sums, m0, n0, row + (lane >> 3), 0);
+  if constexpr (E::ACROSS) turned.finish(e, sums, m0, n0, row, 0);
 #endif
 }
 
@@ -506,15 +506,15 @@ __global__ void __launch_bounds__(512) k_join_newton(E e, int splits, int64_t sp
   TurnedRuns<1> turned;
   rows.load(e, place.m, place.n, row + (threadIdx.x >> 3 & 7));
   turned.load(e, place.m, place.n, row);
-  rows.finish(e, sums, row + (threadIdx.x >> 3 & 7));
-  turned.finish(e, sums, row);
+  rows.finish(e, sums, place.m, place.n, row + (threadIdx.x >> 3 & 7), 0);
+  turned.finish(e, sums, place.m, place.n, row, 0);
 #endif
 }
 
 // ------------------------------------------------------------------ whole updates in one workgroup
 
 // An update whose planes fit the LDS of one CU: every step of it in one launch, a workgroup of
-// 16 waves a matrix (%ONE%).  X lies there by rows of the shorter side, two planes
+// 16 waves a matrix (4 of 256 x 64 float32, five steps: 31 us).  X lies there by rows of the shorter side, two planes
 // of HIGH rows (those past the end are zeros, and so are columns past the end), with one
 // square that holds A, then B.  Two planes in every product.  TILES: rows of 16 in the shorter side.
 constexpr int ONE_BYTES = 158 * 1024;
@@ -902,7 +902,7 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols, int32_t dtype) {
     p.t_plane = cols * p.ldt;
   }
   // The sum of A's tiles is split where that gains: us of a step of 32 k, of a tile's begin and end, and of the join
-  // with its 5 TB/s (53 x 5616 float16, six steps: %SPLIT%).
+  // with its 5 TB/s (53 x 5616 float16, six steps: 303 us whole, 146 so).
   const bool small = p.way == SMALL_TILES, two = p.planes == 2;
   const int64_t t64 = batch * newton_tiles<64, 64>(p.side, p.side, true), t128 = batch * newton_tiles<128, 128>(p.side, p.side, true);
   const int64_t t256 = batch * newton_tiles<256, 128>(p.side, p.side, true);
