@@ -855,7 +855,7 @@ eec_status eec_orthogonalize(void* stream, int64_t batch, int64_t rows, int64_t 
   if (!none) {
     TRY(check_matrix(g, rows, cols, ldg, dtype, "g"));
     // matrices may interleave, or be one: they are only read
-    if (batch > 1 && (stride < 0 || stride > int64_t(1) << 48)) return fail(EEC_ERR_SHAPE, "bad stride of the matrices");
+    if (batch > 1 && (stride < 0 || stride > int64_t(1) << 40)) return fail(EEC_ERR_SHAPE, "bad stride of the matrices");
   }
   TRY(check_matrix(y, all, cols, cols, dtype, "y"));
   TRY(check_ws(workspace, workspace_bytes, ortho_workspace(batch, rows, cols, dtype)));

@@ -50,10 +50,30 @@ template <typename O, int L>
 struct Incoming {
   O residual[L];
   float scale;
+  __device__ __forceinline__ void load_residual(const Epilogue& e, int64_t m, const Columns<O, L>& c) {
+    if (m < e.M) load_raw<true>((const O*)e.residual + m * e.ldr + c.n, c.left, residual);
+  }
   __device__ __forceinline__ void load(const Epilogue& e, int64_t m, const Columns<O, L>& c) {
-    if (m >= e.M) return;
-    if (e.residual) load_raw<true>((const O*)e.residual + m * e.ldr + c.n, c.left, residual);
-    if (e.x_scale) scale = e.x_scale[m];
+    if (e.residual) load_residual(e, m, c);
+    if (e.x_scale && m < e.M) scale = e.x_scale[m];
+  }
+};
+// The scales of a wave's rows, one a lane (rows past the end: 0), loaded ahead of its first store
+// and handed out across lanes: a load between the stores would wait for them (see finish_wave).
+template <int ROWS>
+struct RowScales {
+  static constexpr int N = (ROWS + 63) / 64;
+  float of[N];
+  __device__ __forceinline__ RowScales(const Epilogue& e, int64_t m0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t m = m0 + i * 64 + (threadIdx.x & 63);
+      of[i] = e.x_scale && !e.part && m < e.M ? e.x_scale[m] : 0.f;
+    }
+  }
+  // Rows `first` (uniform, and none of the wave's 64s ends within what is asked for) + r.
+  __device__ __forceinline__ float get(int first, int r) const {
+    return __shfl(N > 1 && first >= 64 ? of[N - 1] : of[0], (first + r) & 63);
   }
 };
 
@@ -84,7 +104,7 @@ __device__ __forceinline__ void scale_run(float (&v)[L], float row, const float 
 }
 
 // L adjacent columns of one row, from their sums over k.
-template <typename O, int L>
+template <bool RESIDUAL = true, typename O, int L>
 __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const Columns<O, L>& c, const Incoming<O, L>& in,
                                            float (&v)[L]) {
   if (m >= e.M) return;
@@ -97,7 +117,7 @@ __device__ __forceinline__ void finish_run(const Epilogue& e, int64_t m, const C
   const bool once = e.N * (int64_t)sizeof(O) % 128 == 0;
   if (e.preact) store_run((O*)e.preact + m * e.N + c.n, c.left, v, once);
   act_values<O>(v, e.act);
-  if (e.residual) {
+  if (RESIDUAL && e.residual) {
 #pragma unroll
     for (int i = 0; i < L; ++i) v[i] += (float)in.residual[i];
   }
@@ -171,8 +191,10 @@ __device__ __forceinline__ void put_tile(const Acc (&acc)[2], char* rows) {
 // fits the instruction cache (8192 x 8192 x 32 bf16: 64 us, this 46 us).
 // What up to four rows a lane need from memory is on its way before the stores of the
 // four ahead of them (8192 x 2048 x 8192 bf16 with residual, bias and SiLU 299 us with
-// the loads behind those stores, 287 so; 2048 x 1024 x 2048 float32 60 and 48; with
-// nothing to load and no activation it costs 1 to 4 %).
+// the loads behind those stores, 287 so; 2048 x 1024 x 2048 float32 60 and 48).  Without
+// a residual nothing is loaded between the stores, and so nothing waits for them (the
+// end of a tile of 256 x 256 bf16 8.2 us -> 6.2; 8192 x 4096 x 4096: int8 136 -> 131 us,
+// e4m3 124 -> 119).
 template <typename O, int HIGH, int PER, typename Acc, int GROUPS, int NB>
 __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_t m0, int64_t n0, int split,
                                             Acc (&acc)[GROUPS][NB]) {
@@ -185,13 +207,45 @@ __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_
   const int r0 = lane / (64 / L), col = lane % (64 / L) * L;
   const bool whole = col + L <= columns;
   const Columns<O, L> c(e, n0 + col, whole ? L : 0);
+  const RowScales<ALL> scales(e, m0);
   Incoming<O, L> next[TOGETHER];
   const auto load = [&](int row) {
-    if (!whole || part != nullptr || row - r0 >= ALL) return;
+    if (!whole || row - r0 >= ALL) return;
 #pragma unroll
-    for (int i = 0; i < TOGETHER; ++i) next[i].load(e, m0 + row + i * APART, c);
+    for (int i = 0; i < TOGETHER; ++i) next[i].load_residual(e, m0 + row + i * APART, c);
   };
-  load(r0);
+  const bool residual = e.residual && part == nullptr;
+  if (residual) load(r0);
+  const auto finish_batches = [&](int g, auto with_residual) {
+#pragma unroll 1
+    for (int at = 0; at < ROWS; at += BATCH) {
+      const int r = at + r0;
+      Incoming<O, L> in[TOGETHER];
+      if constexpr (decltype(with_residual)::value) {
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) in[i] = next[i];
+        load(g * HIGH + r + BATCH);
+      }
+      if (e.x_scale) {  // from all lanes
+#pragma unroll
+        for (int i = 0; i < TOGETHER; ++i) in[i].scale = scales.get(g * HIGH + at, r0 + i * APART);
+      }
+      if (!whole) continue;
+#pragma unroll
+      for (int i = 0; i < TOGETHER; ++i) {
+        const int row = r + i * APART;
+        const int64_t m = m0 + g * HIGH + row;
+        float v[L];
+#pragma unroll
+        for (int u = 0; u < L; u += 4)
+          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
+        if (part == nullptr)
+          finish_run<decltype(with_residual)::value>(e, m, c, in[i], v);
+        else if (m < e.M)
+          store_run(part + m * e.N + n0 + col, L, v);
+      }
+    }
+  };
 #pragma unroll 1
   for (int g = 0; g < GROUPS; g += PER) {
 #pragma unroll
@@ -202,27 +256,10 @@ __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_
       for (int j = 0; j < NB; ++j) acc[i][j] = i + PER < GROUPS ? acc[i + PER < GROUPS ? i + PER : 0][j] : Acc{};
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const int64_t top = m0 + g * HIGH;
-    if (whole) {
-#pragma unroll 1
-      for (int r = r0; r < ROWS; r += BATCH) {
-        Incoming<O, L> in[TOGETHER];
-#pragma unroll
-        for (int i = 0; i < TOGETHER; ++i) in[i] = next[i];
-        load(g * HIGH + r + BATCH);
-#pragma unroll
-        for (int i = 0; i < TOGETHER; ++i) {
-          const int row = r + i * APART;
-          float v[L];
-#pragma unroll
-          for (int u = 0; u < L; u += 4)
-            __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
-          if (part == nullptr)
-            finish_run<O, L>(e, top + row, c, in[i], v);
-          else if (top + row < e.M)
-            store_run(part + (top + row) * e.N + n0 + col, L, v);
-        }
-      }
-    }
+    if (residual)
+      finish_batches(g, std::true_type());
+    else
+      finish_batches(g, std::false_type());
     // the last columns of C that make no whole run: a row a lane, a column at a time
     if (columns % L > 0 && lane < ROWS) {
       const int64_t m = top + lane;
@@ -234,7 +271,7 @@ __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_
         float v[1];
         __builtin_memcpy(v, lds + (lane * 256 + ((at / 4) ^ (lane & 15)) * 16 + at % 4 * 4), 4);
         if (part == nullptr)
-          finish_run<O, 1>(e, m, one, in, v);
+          finish_run(e, m, one, in, v);
         else if (m < e.M)
           part[m * e.N + n0 + at] = v[0];
       }
@@ -257,14 +294,7 @@ __device__ __forceinline__ void finish_wave_gated(const Epilogue& e, char* lds, 
   const int r0 = lane / (32 / L), col = lane % (32 / L) * L;
   const bool whole = col + L <= columns;
   const Columns<O, L> gate(e, h0 + col, whole ? L : 0), value(e, e.outer + h0 + col, whole ? L : 0);
-  float next[TOGETHER];
-  const auto load = [&](int row) {
-    if (!e.x_scale || row - r0 >= ALL) return;
-#pragma unroll
-    for (int i = 0; i < TOGETHER; ++i)
-      if (m0 + row + i * APART < e.M) next[i] = e.x_scale[m0 + row + i * APART];
-  };
-  load(r0);
+  const RowScales<ALL> scales(e, m0);
 #pragma unroll 1
   for (int g = 0; g < GROUPS; g += PER) {
 #pragma unroll
@@ -278,30 +308,31 @@ __device__ __forceinline__ void finish_wave_gated(const Epilogue& e, char* lds, 
     const auto sums = [&](int row, int at, float* to, int bytes) {
       __builtin_memcpy(to, lds + (row * 256 + ((at / 4) ^ (row & 15)) * 16 + at % 4 * 4), bytes);
     };
-    if (whole) {
 #pragma unroll 1
-      for (int r = r0; r < ROWS; r += BATCH) {
-        float scale[TOGETHER];
+    for (int at = 0; at < ROWS; at += BATCH) {
+      const int r = at + r0;
+      float scale[TOGETHER];
+      if (e.x_scale) {  // from all lanes
 #pragma unroll
-        for (int i = 0; i < TOGETHER; ++i) scale[i] = next[i];
-        load(g * HIGH + r + BATCH);
+        for (int i = 0; i < TOGETHER; ++i) scale[i] = scales.get(g * HIGH + at, r0 + i * APART);
+      }
+      if (!whole) continue;
 #pragma unroll
-        for (int i = 0; i < TOGETHER; ++i) {
-          const int row = r + i * APART;
-          float a[L], v[L];
+      for (int i = 0; i < TOGETHER; ++i) {
+        const int row = r + i * APART;
+        float a[L], v[L];
 #pragma unroll
-          for (int u = 0; u < L; u += 4) {
-            const int c = (col + u) / 4;
-            __builtin_memcpy(&a[u], __builtin_assume_aligned(lds + (row * 256 + (c ^ (row & 15)) * 16), 16), 16);
-            __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + ((c + 8) ^ (row & 15)) * 16), 16), 16);
-          }
-          if (part == nullptr) {
-            finish_gated<O, L>(e, top + row, gate, value, scale[i], a, v);
-          } else if (top + row < e.M) {
-            float* to = part + (top + row) * e.N + n0 + col;
-            store_run(to, L, a);
-            store_run(to + 32, L, v);
-          }
+        for (int u = 0; u < L; u += 4) {
+          const int c = (col + u) / 4;
+          __builtin_memcpy(&a[u], __builtin_assume_aligned(lds + (row * 256 + (c ^ (row & 15)) * 16), 16), 16);
+          __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + ((c + 8) ^ (row & 15)) * 16), 16), 16);
+        }
+        if (part == nullptr) {
+          finish_gated<O, L>(e, top + row, gate, value, scale[i], a, v);
+        } else if (top + row < e.M) {
+          float* to = part + (top + row) * e.N + n0 + col;
+          store_run(to, L, a);
+          store_run(to + 32, L, v);
         }
       }
     }
@@ -368,7 +399,7 @@ __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
       const Columns<O, 4> c(e, n, left);
       Incoming<O, 4> in;
       in.load(e, m, c);
-      finish_run<O, 4>(e, m, c, in, v);
+      finish_run(e, m, c, in, v);
     }
   }
 }
@@ -1174,7 +1205,7 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
       for (int i = 0; i < 4; ++i) b[i] = __shfl_xor(r[i], 32);
       if (q < 2 && n < e.outer) finish_gated<O, 4>(e, m, columns, value, in.scale, r, b);
     } else {
-      if (n0 + q * 4 < e.N) finish_run<O, 4>(e, m, columns, in, r);
+      if (n0 + q * 4 < e.N) finish_run(e, m, columns, in, r);
     }
   }
 }

@@ -549,8 +549,8 @@ EEC_API size_t eec_gated_linear_backward_workspace_bytes(int64_t rows, int64_t o
  *   X = g / (|g| + eps)  (|g| the root of the sum of squares),  then for each step
  *   A = X X^T,  X <- a X + (b A + c A^2) X
  * (rows <= cols; otherwise A = X^T X and X <- a X + X (b A + c A^2), the same result).
- *   g       [batch][rows][cols] dtype: matrices `stride` elements apart (>= 0: they may
- *           interleave, or be the same; unread for batch 1), rows `ldg`
+ *   g       [batch][rows][cols] dtype: matrices `stride` elements apart (0 to 2^40: they
+ *           may interleave, or be the same; unread for batch 1), rows `ldg`
  *   coefficients [host][steps][3]: a, b, c of each step; read before the call
  *           returns.  Refused where they take singular values of [0, 1] beyond 3.5 or
  *           b s^2 + c s^4 beyond 15 on the way

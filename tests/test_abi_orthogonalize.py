@@ -32,6 +32,7 @@ def ortho(batch=2, rows=64, cols=48, dtype=F32, g=P(1), ldg=48, stride=64 * 48, 
     (lambda: ortho(eps=float("inf")), "EEC_ERR_SHAPE"),
     (lambda: ortho(g=None), "EEC_ERR_NULL"), (lambda: ortho(y=None), "EEC_ERR_NULL"),
     (lambda: ortho(ldg=47), "EEC_ERR_SHAPE"), (lambda: ortho(stride=-64 * 48), "EEC_ERR_SHAPE"),
+    (lambda: ortho(stride=(1 << 40) + 1), "EEC_ERR_SHAPE"),
     (lambda: ortho(g=ctypes.c_void_p((1 << 32) + 2)), "EEC_ERR_SHAPE"),
     (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, ws=None), "EEC_ERR_WORKSPACE"),
     (lambda: ortho(rows=640, cols=480, ldg=480, stride=640 * 480, size=1024), "EEC_ERR_WORKSPACE"),
