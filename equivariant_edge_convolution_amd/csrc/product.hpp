@@ -864,13 +864,15 @@ __device__ __forceinline__ void multiply(S& c, const Ahead<S>& f, const char* la
   typename S::Frag a[S::GROUPS];
 #pragma unroll
   for (int i = 0; i < S::GROUPS; ++i) {
-    constexpr int LATE = S::GROUPS - S::NB;  // the last groups read one fragment of B each
+    // the last groups read one fragment of B each; fewer groups than fragments, several
+    constexpr int LATE = S::GROUPS > S::NB ? S::GROUPS - S::NB : 0, EACH_B = S::GROUPS > S::NB ? 1 : S::NB / S::GROUPS;
     if (i < S::AHEAD) a[i] = f.a[i];
     if (i + S::AHEAD < S::GROUPS)
       TA::fragment(a[i + S::AHEAD], la, wm, i + S::AHEAD);
     else
       TA::fragment(next.a[i + S::AHEAD - S::GROUPS], na, wm, i + S::AHEAD - S::GROUPS);
-    if (i >= LATE) TB::fragment(next.b[i - LATE], nb, wn, i - LATE);
+#pragma unroll
+    for (int j = (i - LATE) * EACH_B; i >= LATE && j < (i - LATE + 1) * EACH_B; ++j) TB::fragment(next.b[j], nb, wn, j);
 #pragma unroll
     for (int j = 0; j < S::NB; ++j) c.mul(i, j, f.b[j], a[i]);
   }
@@ -881,7 +883,7 @@ __device__ __forceinline__ void multiply(S& c, const Ahead<S>& f, const char* la
     if (i < S::GROUPS - S::NB)                                                   // LDS reads
       __builtin_amdgcn_sched_group_barrier(0x100, TA::READS, 0);
     else
-      __builtin_amdgcn_sched_group_barrier(0x100, TA::READS + TB::READS, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, TA::READS + TB::READS * (S::GROUPS > S::NB ? 1 : S::NB / S::GROUPS), 0);
     __builtin_amdgcn_sched_group_barrier(0x008, S::PRODUCTS, 0);  // products
   }
 }
@@ -903,6 +905,7 @@ __device__ __forceinline__ void tile_barrier() {
 // 1030 at 256 x 256, where two on their way do, and 258 at 128 x 128, where it takes
 // six and the whole LDS (1024 x 4096 x 4096 bf16: 58 us with four buffers, 43 with
 // eight).
+// 128 x 64 (a wave 32 x 64) has short ends of tiles, and other workgroups to run under them.
 // Needs 16-byte aligned rows and lengths (see tiled_operand).
 // E: an Epilogue, or another with its own place_of, of_batch and finish.
 template <typename T, typename O, bool A_KC, bool B_KC, int WM, int WN, int MI, int BUFS, bool G = false,
@@ -975,10 +978,11 @@ __global__ void __launch_bounds__(64 * WM * WN) k_tiled(Product g, E e) {
   tile_barrier<0>();  // nobody's loads or reads are left in the buffers
   // a buffer of its own for each wave: 64 rows of sums in 16 KB, or 32 in 8
   constexpr int SUMS = TA::BYTES >= 16384 && TB::BYTES >= 16384 ? 64 : 32;
-  static_assert(TA::BYTES >= SUMS * 256 && TB::BYTES >= SUMS * 256 && WAVES <= 8, "room for the sums");
-  const int pair = wave >> 1;
+  constexpr bool NARROW = TB::BYTES < SUMS * 256;  // those of A alone
+  static_assert(TA::BYTES >= SUMS * 256 && WAVES <= (NARROW ? 4 : 8), "room for the sums");
+  const int pair = NARROW ? wave : wave >> 1;
   char *even = pair == 0 ? a0 : pair == 1 ? a1 : pair == 2 ? a2 : a3, *odd = pair == 0 ? b0 : pair == 1 ? b1 : pair == 2 ? b2 : b3;
-  finish<G, O, S::ROWS, SUMS / S::ROWS>(e, wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, c.acc);
+  finish<G, O, S::ROWS, SUMS / S::ROWS>(e, !NARROW && wave & 1 ? odd : even, m0 + wm, n0 + wn, place.split, c.acc);
 #endif
 }
 
@@ -1286,7 +1290,7 @@ void pack(hipStream_t st, const Packings& all) {
 
 // ------------------------------------------------------------------ plans
 
-enum Kind { SMALL, GENERAL, TILE128, TILE128X2, TILE256, PARTED, FEW };  // SMALL: the general kernel in 64 x 64 tiles
+enum Kind { SMALL, GENERAL, TILE64, TILE128, TILE128X2, TILE256, PARTED, FEW };  // SMALL: the general kernel in 64 x 64 tiles
 struct Plan {
   Kind kind;
   bool packed;  // operands through k_pack
@@ -1329,7 +1333,7 @@ inline bool worth_packing(int64_t M, int64_t N, int64_t K, int32_t dtype, bool f
 // kernel (aligned, or packed).  k is split where the tiles alone leave most of the
 // 256 CUs idle: joining the sums costs about 5 us, in which a 128 x 128 tile gets
 // through 1200 k and the general kernel, which waits for memory at every step,
-// through some 200.
+// through some 200.  Every tiled kernel adds its k in the same order, so the choice between them changes no result.
 inline Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool tiled, bool packed, bool forward) {
   Plan p{};
   if (forward && M <= FEW_ROWS && N <= FEW_COLUMNS) {
@@ -1348,8 +1352,15 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool ti
   const double us128 = (double)((t128 + 255) / 256) * (10 + 0.25 * steps);
   const double us256 = (double)((t256 + 255) / 256) * (20 + 0.49 * steps);
   const bool shared = t128 > 256 && t128 <= 512 && steps <= 128;
+  // Forward, k too short to split: 128 x 64 tiles, of which three workgroups fit a CU.  Where they are one round,
+  // bf16 256 x 2048 x 1024 takes 9.0 us (128 x 128: 13.2), 1024 x 1024 x 256 5.3 (8.2), int8 1024^3 6.9 (10.5);
+  // up to three, all at once, on a few steps: int8 1536 x 2816 x 1024 with bias and GELU 17.3 (19.3), bf16 x 256 12.1
+  // (14.9); past that they lose (bf16 x 1024 20.9 against 19.2; 2048 x 4096 x 1024 28.9, 25.6; split, 1024 x 1024 x
+  // 4096 26.9, 24.9).
+  const int64_t t64 = ((M + 127) / 128) * ((N + 63) / 64);
+  const bool narrow = forward && K < 2048 && (t64 <= 256 || (t64 <= 768 && steps <= 20));
   p.kind = packed && dtype == EEC_F32 ? PARTED
-           : tiled || packed ? (shared ? TILE128X2 : us256 < us128 ? TILE256 : TILE128)
+           : tiled || packed ? (narrow ? TILE64 : shared ? TILE128X2 : us256 < us128 ? TILE256 : TILE128)
            : t128 >= 256     ? GENERAL
                              : SMALL;
   p.tiles = p.kind == TILE256  ? t256
@@ -1363,6 +1374,7 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, bool ti
   s = std::max<int64_t>(1, s);
   p.k_split = std::max<int64_t>(step, up((K + s - 1) / s, step));
   p.splits = std::max<int64_t>(1, (K + p.k_split - 1) / p.k_split);
+  if (p.kind == TILE64) p.tiles = t64;
   return p;
 }
 // Room for the split sums, however the operands turn out to be aligned.
@@ -1427,6 +1439,8 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
     if (p.kind == PARTED) k_parted<A_KC, B_KC, G><<<grid, 512, 0, st>>>(t, e);
   } else if constexpr (!std::is_same<T, e4m3_wide>::value) {
     if (p.kind == TILE256) k_tiled<T, O, A_KC, B_KC, 2, 4, 8, 4, G><<<grid, 512, 0, st>>>(t, e);
+    if constexpr (A_KC && B_KC)
+      if (p.kind == TILE64) k_tiled<T, O, A_KC, B_KC, 4, 1, 2, 4, G><<<grid, 256, 0, st>>>(t, e);
     if (p.kind == TILE128X2) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 4, G><<<grid, 256, 0, st>>>(t, e);
     if (p.kind == TILE128) k_tiled<T, O, A_KC, B_KC, 2, 2, 4, 8, G><<<grid, 256, 0, st>>>(t, e);
   }
