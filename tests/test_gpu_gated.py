@@ -23,7 +23,8 @@ pytestmark = pytest.mark.gpu
 SHAPES = [  # rows, inner, outer
     (1, 1, 1), (1, 64, 64), (3, 0, 5), (0, 16, 8), (17, 33, 65), (128, 128, 128), (129, 257, 130), (300, 1029, 7),
     (5, 2050, 300), (1000, 64, 256), (16, 512, 48), (33, 4096, 264), (64, 96, 1000), (257, 320, 513), (2, 8, 4096),
-    (512, 1024, 512), (1, 5000, 3), (31, 40, 31), (40, 40, 33)]
+    (512, 1024, 512), (1, 5000, 3), (31, 40, 31), (40, 40, 33), (70, 272, 100), (129, 16, 33), (257, 1040, 65),
+    (1000, 1504, 500)]
 USES = (("silu", True, 0, 0), ("none", False, 0, 0), ("gelu", True, 3, 1), ("relu", False, 8, 8))
 
 

@@ -81,7 +81,8 @@ def test_empty_and_special_rows(width):
 SHAPES = [  # rows, inner, outer
     (1, 1, 1), (1, 64, 64), (3, 0, 5), (0, 16, 8), (17, 33, 65), (32, 4096, 264), (33, 4096, 264), (128, 128, 128), (129, 257, 130),
     (300, 1029, 7), (5, 2050, 300), (64, 96, 1000), (257, 320, 513), (512, 1024, 512), (1, 5000, 3), (600, 4096, 320),
-    (1024, 4096, 2048), (2048, 512, 4096), (1536, 1024, 2816), (1501, 1505, 1503), (4100, 160, 264), (40, 8192, 48)]
+    (1024, 4096, 2048), (2048, 512, 4096), (1536, 1024, 2816), (1501, 1505, 1503), (4100, 160, 264), (40, 8192, 48),
+    (70, 272, 200), (129, 16, 66), (257, 1040, 130), (1000, 1504, 1000), (1531, 1029, 2771)]
 
 
 def codes(g, *s):
