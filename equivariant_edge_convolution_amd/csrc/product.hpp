@@ -1085,7 +1085,6 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   constexpr int WAVES = 8, P = M_::PLANES;
   constexpr int CHUNK = sizeof(T) == 4 ? 32 : sizeof(T) == 2 ? 64 : 128;  // k of one run
   constexpr int STEPS = CHUNK / 32;                                      // matrix steps of one run
-  constexpr int TOGETHER = MT == 1 ? 4 : 2;                              // runs in flight
   __shared__ typename M_::Acc join[WAVES][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * (G ? 8 : 16);
@@ -1152,7 +1151,11 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   const int64_t full = g.K / CHUNK;
   const int own = q * STEPS * 8;
   int64_t c = wave;
-  for (; c + WAVES * (TOGETHER - 1) < full; c += WAVES * TOGETHER) {
+  // `together` runs in flight: four, and two of what is left (int8 17 x 4096 x 4096 7.1 us, two at a time 9.3; 8 x 16384 x
+  // 2048 12.8, one at a time past the fours 20.9); two for two tiles of rows and more than 8 bits (float32 30 x
+  // 6600 x 3299 53 us, four at a time 62; bf16 even)
+  const auto some = [&](auto together) {
+    constexpr int TOGETHER = decltype(together)::value;
     Loaded wl[TOGETHER], xl[TOGETHER][MT];
 #pragma unroll
     for (int i = 0; i < TOGETHER; ++i) {
@@ -1168,7 +1171,12 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
       for (int t = 0; t < MT; ++t) xr[t] = xl[i][t].get();
       product(wl[i].get(), xr);
     }
-  }
+    c += WAVES * TOGETHER;
+  };
+  constexpr int MOST = MT == 1 || sizeof(T) == 1 ? 4 : 2;
+  while (c + WAVES * (MOST - 1) < full) some(std::integral_constant<int, MOST>());
+  if constexpr (MOST > 2)
+    if (c + WAVES < full) some(std::integral_constant<int, 2>());
   for (; c * CHUNK < g.K; c += WAVES) {
     Run wr, xr[MT];
     const int64_t k = c * CHUNK + own, left = g.K - k;
