@@ -30,7 +30,7 @@ struct Epilogue {
   void *y, *preact;
   int64_t M, N;  // of the product
   int64_t outer; // gated: columns of y
-  float* part;  // split sums [split][M][N] instead of all of the above, or NULL
+  float* part;  // split sums [split][M][N] (of 8-bit integers: as 32-bit ones) instead of all of the above, or NULL
 };
 
 // What L adjacent columns, `left` of which exist, have in common over the rows.
@@ -162,14 +162,13 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ void put_sums(char* rows, int row, int c, const f32x4& v) {
   __builtin_memcpy(__builtin_assume_aligned(rows + (row * 256 + (c ^ (row & 15)) * 16), 16), &v, 16);
 }
-// The tiles as the matrix instructions leave them: 16 rows x 4 x 16 columns, 32 x 2 x 32.
-// Sums of integers are exact, and rounded once here.
-__device__ __forceinline__ f32x4 as_floats(const f32x4& v) { return v; }
-__device__ __forceinline__ f32x4 as_floats(const i32x4& v) { return __builtin_convertvector(v, f32x4); }
+// The tiles as the matrix instructions leave them: 16 rows x 4 x 16 columns, 32 x 2 x 32. Sums of
+// integers stay integers (in the floats' places) until all of k is in them, and are rounded once then.
 template <typename Acc>
 __device__ __forceinline__ void put_tile(const Acc (&acc)[4], char* rows) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), as_floats(acc[j]));
+  for (int j = 0; j < 4; ++j)
+    put_sums(rows, threadIdx.x & 15, j * 4 + (threadIdx.x >> 4 & 3), __builtin_bit_cast(f32x4, acc[j]));
 }
 template <typename Acc>
 __device__ __forceinline__ void put_tile(const Acc (&acc)[2], char* rows) {
@@ -177,9 +176,20 @@ __device__ __forceinline__ void put_tile(const Acc (&acc)[2], char* rows) {
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const f32x4 v = {(float)acc[j][4 * a], (float)acc[j][4 * a + 1], (float)acc[j][4 * a + 2], (float)acc[j][4 * a + 3]};
+      f32x4 v;
+      __builtin_memcpy(&v, (const char*)&acc[j] + 16 * a, 16);
       put_sums(rows, threadIdx.x & 31, j * 8 + a * 2 + (threadIdx.x >> 5 & 1), v);
     }
+}
+// Acc: a vector of sums; whether they are integers, and such sums as floats.
+template <typename Acc>
+constexpr bool INTEGERS = std::is_same<decltype(Acc{}[0] + 0), int>::value;
+template <bool INTEGER, int L>
+__device__ __forceinline__ void to_floats(float (&v)[L]) {
+  if constexpr (INTEGER) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) v[i] = (float)__builtin_bit_cast(int, v[i]);
+  }
 }
 
 // Finishes (or, split, stores) all of a wave's GROUPS matrix tiles of HIGH rows x 64
@@ -239,10 +249,12 @@ __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_
 #pragma unroll
         for (int u = 0; u < L; u += 4)
           __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + (((col + u) / 4) ^ (row & 15)) * 16), 16), 16);
-        if (part == nullptr)
+        if (part == nullptr) {
+          to_floats<INTEGERS<Acc>>(v);
           finish_run<decltype(with_residual)::value>(e, m, c, in[i], v);
-        else if (m < e.M)
+        } else if (m < e.M) {
           store_run(part + m * e.N + n0 + col, L, v);
+        }
       }
     }
   };
@@ -270,10 +282,12 @@ __device__ __forceinline__ void finish_wave(const Epilogue& e, char* lds, int64_
         in.load(e, m, one);
         float v[1];
         __builtin_memcpy(v, lds + (lane * 256 + ((at / 4) ^ (lane & 15)) * 16 + at % 4 * 4), 4);
-        if (part == nullptr)
+        if (part == nullptr) {
+          to_floats<INTEGERS<Acc>>(v);
           finish_run(e, m, one, in, v);
-        else if (m < e.M)
+        } else if (m < e.M) {
           part[m * e.N + n0 + at] = v[0];
+        }
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -328,6 +342,8 @@ __device__ __forceinline__ void finish_wave_gated(const Epilogue& e, char* lds, 
           __builtin_memcpy(&v[u], __builtin_assume_aligned(lds + (row * 256 + ((c + 8) ^ (row & 15)) * 16), 16), 16);
         }
         if (part == nullptr) {
+          to_floats<INTEGERS<Acc>>(a);
+          to_floats<INTEGERS<Acc>>(v);
           finish_gated<O, L>(e, top + row, gate, value, scale[i], a, v);
         } else if (top + row < e.M) {
           float* to = part + (top + row) * e.N + n0 + col;
@@ -346,6 +362,8 @@ __device__ __forceinline__ void finish_wave_gated(const Epilogue& e, char* lds, 
         sums(lane, at + 32, v, 4);
         if (part == nullptr) {
           const Columns<O, 1> one(e, h0 + at, 1), two(e, e.outer + h0 + at, 1);
+          to_floats<INTEGERS<Acc>>(a);
+          to_floats<INTEGERS<Acc>>(v);
           finish_gated<O, 1>(e, m, one, two, e.x_scale && m < e.M ? e.x_scale[m] : 0.f, a, v);
         } else if (m < e.M) {
           float* to = part + m * e.N + n0 + at;
@@ -369,33 +387,38 @@ __device__ __forceinline__ void finish(const Epilogue& e, char* lds, int64_t m0,
 }
 
 // Four adjacent columns of row m, the splits added in order.
+template <bool INTEGER>
 __device__ __forceinline__ void join_run(const Epilogue& e, int splits, int64_t m, int64_t n, int64_t left, float (&v)[4]) {
+  using Sum = std::conditional_t<INTEGER, int, float>;
+  Sum all[4] = {};
   for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads on their way
-    float t[8][4];
+    Sum t[8][4];
 #pragma unroll
     for (int s = 0; s < 8; ++s)
-      load_run(e.part + ((int64_t)(s0 + s) * e.M + m) * e.N + n, s0 + s < splits ? left : 0, t[s]);
+      load_raw((const Sum*)e.part + ((int64_t)(s0 + s) * e.M + m) * e.N + n, s0 + s < splits ? left : 0, t[s]);
 #pragma unroll
     for (int s = 0; s < 8; ++s)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += t[s][c];
+      for (int c = 0; c < 4; ++c) all[c] += t[s][c];
   }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = (float)all[c];
 }
 // Adds the splits in order and finishes: 4 columns (outputs) a thread.
-template <typename O, bool G = false>
+template <typename O, bool G = false, bool INTEGER = false>
 __global__ void __launch_bounds__(256) k_join_splits(Epilogue e, int splits) {
   const int64_t width = G ? e.outer : e.N, per_row = (width + 3) / 4, total = e.M * per_row;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / per_row, n = i % per_row * 4, left = width - n;
     if constexpr (G) {
-      float a[4] = {}, v[4] = {};
-      join_run(e, splits, m, gate_column(n), left, a);
-      join_run(e, splits, m, gate_column(n) + 32, left, v);
+      float a[4], v[4];
+      join_run<INTEGER>(e, splits, m, gate_column(n), left, a);
+      join_run<INTEGER>(e, splits, m, gate_column(n) + 32, left, v);
       const Columns<O, 4> gate(e, n, left), value(e, e.outer + n, left);
       finish_gated<O, 4>(e, m, gate, value, e.x_scale ? e.x_scale[m] : 0.f, a, v);
     } else {
-      float v[4] = {};
-      join_run(e, splits, m, n, left, v);
+      float v[4];
+      join_run<INTEGER>(e, splits, m, n, left, v);
       const Columns<O, 4> c(e, n, left);
       Incoming<O, 4> in;
       in.load(e, m, c);
@@ -469,7 +492,7 @@ struct Mat<e4m3> {
     return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(b[0], a[0], c, 0, 0, 0);
   }
 };
-// 8-bit integers: sums of up to MAX_INNER_I8 products of (-128)^2 are exact in 32 bits.
+// 8-bit integers: sums of up to MAX_INNER_I8 products of (-128)^2 are exact in 32 bits, and so are parts of them.
 template <>
 struct Mat<int8_t> {
   using E = int8_t;
@@ -1466,7 +1489,7 @@ void product(hipStream_t st, Product g, Epilogue e, float* ws, int32_t dtype, bo
   if (p.kind == SMALL) k_product<T, O, A_KC, B_KC, 4, 1, 1, G><<<grid, 256, 0, st>>>(g, e);
   if (p.splits > 1) {
     const int64_t runs = g.M * ((g.N + 3) / 4);
-    k_join_splits<O, G><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)p.splits);
+    k_join_splits<O, G, std::is_same<T, int8_t>::value><<<dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 4096)), 256, 0, st>>>(e, (int)p.splits);
   }
 }
 

@@ -484,9 +484,8 @@ EEC_API eec_status eec_quantize_rows(void *stream, int64_t rows, int64_t width, 
  * (codes at random: 1.6e-4 at inner = 64, 2e-5 at 4096; normal values 2e-5 and
  * 1.3e-6), which can exceed a 16-bit output's own rounding where the sum
  * cancels.  With a float32 output they are summed in float32.  EEC_I8 products
- * (codes -128 to 127, inner at most 131071) are summed exactly, in 32-bit integers;
- * the sum is rounded once to float32 and scaled there (summed in parts over k,
- * where a few large outputs make that faster, each part is rounded). */
+ * (codes -128 to 127, inner at most 131071) are summed exactly, in 32-bit integers,
+ * whatever the sizes; the sum is rounded once to float32 and scaled there. */
 EEC_API eec_status eec_linear(void *stream, int64_t rows, int64_t outer, int64_t inner, int32_t dtype,
                       int32_t out_dtype, const void *x, int64_t ldx, const float *x_scale, const void *w,
                       int64_t ldw, const float *w_scale, const void *bias, const void *residual, int64_t ldr,
