@@ -22,6 +22,13 @@ namespace {
 
 constexpr float SCALE = 4096.f;
 
+// What g is multiplied with, SCALE / (|g| + eps), from its sum of squares.  Only beside a norm of zero (others are 2^-149 at
+// least) can that pass float64's range: bounded, it leaves a matrix of zeros one.  A NaN stays.
+__device__ __forceinline__ double scale_of(double sum, double eps) {
+  const double scale = (double)SCALE / (sqrt(sum) + eps);
+  return scale > 1e300 ? 1e300 : scale;
+}
+
 // Where a product's results go: alpha from + beta C, rounded into two planes or one, or (Y a
 // type) into rows of y.
 struct Planes {};
@@ -577,7 +584,7 @@ __global__ void __launch_bounds__(1024) k_one(NewtonOne s) {
   __syncthreads();
   sum = 0.0;
   for (int i = 0; i < 16; ++i) sum += join[i];
-  const double scale = (double)SCALE / (sqrt(sum) + s.eps);
+  const double scale = scale_of(sum, s.eps);
   for (int i = threadIdx.x; i < x_plane / 8; i += 1024) {
     uint16_t h[8], l[8];
     f16 hi[8], lo[8];
@@ -806,7 +813,7 @@ __global__ void __launch_bounds__(256) k_scaled(Scaling s) {
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
   if ((threadIdx.x & 63) == 0) join[threadIdx.x >> 6] = sum;
   __syncthreads();
-  const double scale = (double)SCALE / (sqrt((join[0] + join[1]) + (join[2] + join[3])) + s.eps);
+  const double scale = scale_of((join[0] + join[1]) + (join[2] + join[3]), s.eps);
   const T* g = (const T*)s.g + batch * s.stride;
   f16 *x = s.x + batch * s.batch, *turned = s.turned + batch * s.turned_batch;
   __shared__ float tile[64][65];
@@ -827,7 +834,7 @@ __global__ void __launch_bounds__(256) k_scaled(Scaling s) {
       float v[8];
       load_run<true>(g + r * s.ldg + c, r < s.rows ? s.cols - c : 0, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = r < s.rows && c + j < s.cols ? (float)(v[j] * scale) : 0.f;  // an infinite scale makes no NaN of the padding
+      for (int j = 0; j < 8; ++j) v[j] = r < s.rows && c + j < s.cols ? (float)(v[j] * scale) : 0.f;  // a NaN makes none of the padding
       if (r < s.rows && c < s.cols) put(x + r * s.ldx + c, s.plane, v);
       if (s.turned) {
 #pragma unroll
