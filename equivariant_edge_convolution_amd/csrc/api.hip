@@ -824,12 +824,14 @@ static eec_status check_coefficients(int32_t steps, const double* c) {
       grown = std::max(grown, fabs(sqrt(q) * (c[0] + q * (c[1] + c[2] * q))));
     };
     at(most * most);
-    if (c[2] != 0.0) {
-      at(-c[1] / (2.0 * c[2]));  // of the polynomial of A
-      const double d = 9.0 * c[1] * c[1] - 20.0 * c[0] * c[2];
-      if (d >= 0.0) at((-3.0 * c[1] - sqrt(d)) / (10.0 * c[2])), at((-3.0 * c[1] + sqrt(d)) / (10.0 * c[2]));
-    } else if (c[1] != 0.0) {
-      at(-c[0] / (3.0 * c[1]));
+    at(-c[1] / (2.0 * c[2]));  // where the polynomial of A turns
+    // where s does, a + 3 b q + 5 c q^2 = 0: both roots from the sum that does not cancel, so that neither is lost
+    // where c is next to nothing (or 0: one root, the other infinite or none)
+    const double d = 9.0 * c[1] * c[1] - 20.0 * c[0] * c[2];
+    if (d >= 0.0) {
+      const double t = -0.5 * (3.0 * c[1] + copysign(sqrt(d), c[1]));
+      at(t / (5.0 * c[2]));
+      at(c[0] / t);
     }
     most = std::max(grown, 1e-30);
     if (most > 3.5 || poly > 15.0)
