@@ -453,16 +453,16 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
   }
 #undef EEC_STEP
   tile_barrier<0>();
-  // sums of the first half of every step: 64 rows in a buffer of 16 KB, or two of 8 KB; of the second in the next
-  constexpr bool TWO = 4 * P * B < 16384;
-  char* mine = TWO ? (half == 0 ? (wave < 2 ? a0 : a1) : (wave < 2 ? a2 : a3)) : (half == 0 ? a0 : a1) + wave / 2 * 8192;
+  // sums of the first half of every step: 64 rows in a buffer of 16 KB; of the second in the next
+  static_assert(4 * P * B >= 16384, "room for the sums");
+  char* mine = (half == 0 ? a0 : a1) + wave / 2 * 8192;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) put_sums(mine, 16 * i + (lane & 15), wn / 4 + 4 * j + (lane >> 4), acc[i][j]);
   __syncthreads();
   const int at = threadIdx.x * 32;
-  char *first = TWO && at >= 8192 ? a1 + (at - 8192) : a0 + at, *second = TWO ? (at >= 8192 ? a3 + (at - 8192) : a2 + at) : a1 + at;
+  char *first = a0 + at, *second = a1 + at;
   f32x4 u[2], v[2];
   __builtin_memcpy(u, __builtin_assume_aligned(first, 16), 32);
   __builtin_memcpy(v, __builtin_assume_aligned(second, 16), 32);
@@ -479,9 +479,8 @@ __global__ void __launch_bounds__(512) k_small(Product g, E e) {
   }
   __builtin_memcpy(__builtin_assume_aligned(first, 16), u, 32);
   __syncthreads();
-  const char* sums = TWO && row >= 32 ? a1 - 8192 : a0;
-  rows.finish(e, sums, m0, n0, row + (lane >> 3), 0);
-  if constexpr (E::ACROSS) turned.finish(e, sums, m0, n0, row, 0);
+  rows.finish(e, a0, m0, n0, row + (lane >> 3), 0);
+  if constexpr (E::ACROSS) turned.finish(e, a0, m0, n0, row, 0);
 #endif
 }
 
