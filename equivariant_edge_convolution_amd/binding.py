@@ -718,12 +718,17 @@ def gated_linear_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pr
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 
 
+def _each(coefficients) -> tuple:
+    """(a, b, c), or one of these for each step, from sequences or arrays."""
+    return tuple(tuple(v) if isinstance(v, (tuple, list)) or getattr(v, "ndim", 0) else float(v) for v in coefficients)
+
+
 @functools.lru_cache(maxsize=256)
 def _coefficients(steps: int, each: tuple) -> ctypes.Array:
-    rows = (each,) * steps if isinstance(each[0], (int, float)) else each
-    if len(rows) != steps or any(len(r) != 3 for r in rows):
+    rows = each if any(isinstance(r, tuple) for r in each) else (each,) * steps
+    if len(rows) != steps or any(not isinstance(r, tuple) or len(r) != 3 for r in rows):
         raise ValueError("coefficients are (a, b, c), or one of these for each step")
-    return (ctypes.c_double * (3 * max(steps, 1)))(*(float(v) for r in rows for v in r))
+    return (ctypes.c_double * (3 * steps))(*(float(v) for r in rows for v in r))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -744,8 +749,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ, e
         raise ValueError("the columns of g must be adjacent")
     ldg = g.stride(-2) if rows > 1 else cols
     stride = g.stride(0) if batch > 1 and g.dim() == 3 else 0
-    each = tuple(v if isinstance(v, (int, float)) else tuple(v) for v in coefficients)
-    c = _coefficients(int(steps), each)
+    c = _coefficients(int(steps), _each(coefficients))
     y = torch.empty(g.shape, dtype=g.dtype, device=dev)
     if workspace is None:
         workspace = _workspace(_orthogonalize_workspace(batch, rows, cols, dt), dev)
