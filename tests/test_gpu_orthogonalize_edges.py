@@ -1,12 +1,11 @@
 """The orthogonalised update at the ends of its arguments' ranges."""
-import numpy as np
 import pytest
 import torch
 
 from equivariant_edge_convolution_amd import binding as B
 
 from gpu_util import DEV, say
-from test_gpu_dense import TYPES, ids
+from test_gpu_dense import TYPES, U, ids
 from test_gpu_orthogonalize import update
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +41,26 @@ def test_repeats_to_the_bit(rows, cols, dt):
     y = B.orthogonalize(g)
     for _ in range(3):
         assert torch.equal(B.orthogonalize(g), y)
+
+
+@pytest.mark.parametrize("rows,cols,steps,dt", [
+    (1 << 20, 1, 5, torch.float32), (1, 1 << 20, 5, torch.bfloat16), (1 << 20, 130, 3, torch.float16), (300, 1 << 20, 2, torch.bfloat16),
+    (16384, 20001, 1, torch.bfloat16), (20001, 16384, 1, torch.float32)], ids=ids)
+def test_the_largest_sides(rows, cols, steps, dt):
+    """Sides up to 2^20, in norm against the same steps in 64 bits on the device.
+
+    Two planes: 22 bits of each factor, 2^-16 over these steps; one plane (bf16, sides of 256 on): 11 bits, 3 2^-11; and U
+    of the output."""
+    g = torch.randn(rows, cols, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dt)
+    y = B.orthogonalize(g, steps)
+    X = g.double()
+    X = X / (X.norm() + 1e-7)
+    X = X.t().contiguous() if rows > cols else X
+    a, b, c = B.NEWTON_SCHULZ
+    for _ in range(steps):
+        A = X @ X.t()
+        X = torch.addmm(X, torch.addmm(A, A, A, beta=b, alpha=c), X, beta=a)
+    X = X.t() if rows > cols else X
+    err = float((y.double() - X).norm() / X.norm())
+    say(f"[orthogonalize] {rows}x{cols} {dt}: {err:.2g}")
+    assert err <= U[dt] + (3 * 2.0 ** -11 if dt == torch.bfloat16 and min(rows, cols) >= 256 else 2.0 ** -16)
