@@ -1096,14 +1096,46 @@ struct Words {
   }
 };
 
+// The first `bytes` of 32, none perhaps, at a multiple of 4 (ODD: at any address) as `row`, which has
+// one at least; the others are zeros.  By dwords that hold one of them (past the last of these: it
+// again), all on their way at once, so that nothing else is read and no lane waits for a branch.
+// Element by element a row's end took 50 registers more in 8 bits, and with them a CU one
+// workgroup instead of two (e4m3 2 x 2736 -> 4563 15.2 us, 5.7 so; 18 x 1524 -> 11 10.6, 4.2).
+template <bool ODD>
+struct Rest {
+  uint32_t w[8 + ODD], shift;
+  int bytes;
+  __device__ __forceinline__ void load(const void* p, const void* row, int bytes_) {
+    bytes = bytes_;
+    const char* from = (const char*)(bytes > 0 ? p : row);
+    shift = ODD ? (uint32_t)(uintptr_t)from & 3 : 0;
+    const int last = ((int)shift + max(min(bytes, 32), 1) - 1) / 4;
+#pragma unroll
+    for (int i = 0; i < 8 + ODD; ++i)
+      __builtin_memcpy(&w[i], __builtin_assume_aligned(from - shift + 4 * min(i, last), 4), 4);
+  }
+  __device__ __forceinline__ void get(uint32_t (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = ODD ? __builtin_amdgcn_alignbyte(w[i + ODD], w[i], shift) : w[i];
+      const int here = bytes - 4 * i;
+      v[i] = here >= 4 ? v[i] : here > 0 ? v[i] & ((1u << 8 * here) - 1) : 0;
+    }
+  }
+};
+
 // Up to 16 MT rows of x against 16 columns (rows of w) per workgroup: w goes from
 // memory straight into the first factor of the matrix instruction, once, x (a few
 // rows, in the L2) into the second.  The 8 waves deal runs of 128 bytes of k in
 // turn and are joined in LDS, in wave order, so one launch does it all.
 // Gated: 8 rows of the gate and the same 8 of the value, which meet after the join.
 // ODD: rows whose addresses are not multiples of 4 bytes.
+// Registers a lane: 128, for two workgroups (four waves a SIMD) on a CU, where that needs no spills (e4m3 30 x 1024 ->
+// 4096 in float32 5.4 us so, 4.6 left free); two tiles of 16 bits are below 128 by themselves.
+template <typename T, int MT>
+constexpr int FEW_WAVES = !std::is_same<T, e4m3_wide>::value && (MT == 1 || sizeof(T) == 1) ? 4 : 2;
 template <typename T, typename O, int MT, bool G = false, bool ODD = false>
-__global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
+__global__ void __launch_bounds__(512, (FEW_WAVES<T, MT>)) k_few(Product g, Epilogue e) {
   using M_ = Mat<T>;
   constexpr int WAVES = 8, P = M_::PLANES;
   constexpr int CHUNK = sizeof(T) == 4 ? 32 : sizeof(T) == 2 ? 64 : 128;  // k of one run
@@ -1129,24 +1161,24 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
     Raw<T> v[STEPS];
   };
   static_assert(sizeof(Run) == 32, "a run of a lane");
-  struct Loaded {  // a run as it comes from memory
-    std::conditional_t<ODD, Words<32>, Run> is;
-    __device__ __forceinline__ void load(const T* p) {
-      if constexpr (ODD)
-        is.load(p);
-      else
-        __builtin_memcpy(&is, p, 32);
+  struct Pair {  // 32 bytes in two accesses; as a copy of elements some of them become loads of 2 bytes (30 x 3328 -> 6600
+                 // e4m3 14.4 us, 11.5 so)
+    i32x4 q[2];
+    __device__ __forceinline__ void load(const void* p) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) q[i] = ((const i32x4_any*)p)[i];
     }
+    __device__ __forceinline__ void get(uint32_t (&v)[8]) const { __builtin_memcpy(v, q, 32); }
+  };
+  struct Loaded {  // a run as it comes from memory
+    std::conditional_t<ODD, Words<32>, Pair> is;
+    __device__ __forceinline__ void load(const T* p) { is.load(p); }
     __device__ __forceinline__ Run get() const {
-      if constexpr (ODD) {
-        uint32_t v[8];
-        is.get(v);
-        Run r;
-        __builtin_memcpy(&r, v, 32);
-        return r;
-      } else {
-        return is;
-      }
+      uint32_t v[8];
+      is.get(v);
+      Run r;
+      __builtin_memcpy(&r, v, 32);
+      return r;
     }
   };
   auto parts = [](const Raw<T>& r, typename M_::Frag (&f)[P]) {
@@ -1174,9 +1206,8 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
   const int64_t full = g.K / CHUNK;
   const int own = q * STEPS * 8;
   int64_t c = wave;
-  // `together` runs in flight: four, and two of what is left (int8 17 x 4096 x 4096 7.1 us, two at a time 9.3; 8 x 16384 x
-  // 2048 12.8, one at a time past the fours 20.9); two for two tiles of rows and more than 8 bits (float32 30 x
-  // 6600 x 3299 53 us, four at a time 62; bf16 even)
+  // `together` runs in flight: four, and two of what is left; two for two tiles of rows (float32 30 x 6600 x 3299
+  // 53 us, four at a time 62; 8 bits: 30 x 6081 x 4814 21.4 and 22.6, 20 x 8192 x 8192 21.0 and 20.6; 16 even)
   const auto some = [&](auto together) {
     constexpr int TOGETHER = decltype(together)::value;
     Loaded wl[TOGETHER], xl[TOGETHER][MT];
@@ -1196,31 +1227,26 @@ __global__ void __launch_bounds__(512) k_few(Product g, Epilogue e) {
     }
     c += WAVES * TOGETHER;
   };
-  constexpr int MOST = MT == 1 || sizeof(T) == 1 ? 4 : 2;
+  constexpr int MOST = MT == 1 ? 4 : 2;
   while (c + WAVES * (MOST - 1) < full) some(std::integral_constant<int, MOST>());
   if constexpr (MOST > 2)
     if (c + WAVES < full) some(std::integral_constant<int, 2>());
-  for (; c * CHUNK < g.K; c += WAVES) {
+  if (c < full) some(std::integral_constant<int, 1>());
+  if (c * CHUNK < g.K) {
+    const int64_t k = c * CHUNK + own;
+    const int bytes = (int)(g.K - k) * (int)sizeof(T);
+    Rest<ODD> wl, xl[MT];
+    wl.load(w + k, w, bytes);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xl[t].load(x[t] + k, x[t], bytes);
+    uint32_t v[8];
     Run wr, xr[MT];
-    const int64_t k = c * CHUNK + own, left = g.K - k;
-    if (c < full) {
-      Loaded wl, xl[MT];
-      wl.load(w + k);
+    wl.get(v);
+    __builtin_memcpy(&wr, v, 32);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) xl[t].load(x[t] + k);
-      wr = wl.get();
-#pragma unroll
-      for (int t = 0; t < MT; ++t) xr[t] = xl[t].get();
-    } else {
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool is = s * 8 + i < left;
-          wr.v[s].v[i] = is ? w[k + s * 8 + i] : T{};
-#pragma unroll
-          for (int t = 0; t < MT; ++t) xr[t].v[s].v[i] = is ? x[t][k + s * 8 + i] : T{};
-        }
+    for (int t = 0; t < MT; ++t) {
+      xl[t].get(v);
+      __builtin_memcpy(&xr[t], v, 32);
     }
     product(wr, xr);
   }
