@@ -407,6 +407,8 @@ __device__ __forceinline__ void divide_run(float (&v)[N], float scale, float inv
     for (int i = 0; i < N; ++i) v[i] /= scale;
   }
 }
+// A product, as a tensor library's division of device rows by the number MOST is: its codes are these bit for bit
+// (k_norm's scale is the quotient, and stays so; the two may differ in the last bit).
 template <typename Q>
 __device__ __forceinline__ float scale_of(float amax) {
   if (!(amax <= 3.4028235e38f)) return __builtin_nanf("");  // a NaN or an infinity in the row

@@ -454,7 +454,10 @@ EEC_API size_t eec_add_rms_norm_backward_workspace_bytes(int64_t rows, int64_t w
  * channels (rows of w) alike.  Per row of `width` (>= 1) elements
  *   scale = max(max_j |x_j|, 2^-100) times 1/127 (EEC_I8) or 1/448 (EEC_E4M3),
  *   y_j   = x_j / scale, rounded to the nearest code (to even);
- * the factor, scale and the quotient are float32, each correctly rounded.
+ * the factor, scale and the quotient are float32, each correctly rounded.  The product with
+ * 1/127 is what dividing a device tensor by the number 127 gives in PyTorch, so that its codes are these.
+ * (eec_add_rms_norm's scale is the quotient max / 448, which may differ in its last bit: each
+ * call's codes belong to that call's scales.)
  *   dtype   EEC_F32, EEC_F16 or EEC_BF16: the type of x
  *   codes   EEC_I8 (codes -127 to 127) or EEC_E4M3: the type of y
  *   y       [rows][width], scale [rows] float32
